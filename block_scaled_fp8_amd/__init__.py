@@ -27,7 +27,7 @@ __all__ = [
     "transform_sf", "get_mn_major_tma_aligned_tensor", "get_mn_major_tma_aligned_packed_ue8m0_tensor",
     "per_token_group_cast_fp8", "k_grouped_fp8_gemm_nt_contiguous", "k_grouped_fp8_gemm_tn_contiguous", "transform_sf_into_required_layout",
     "fp8_fp4_gemm_nt", "m_grouped_fp8_fp4_gemm_nt_contiguous", "m_grouped_fp8_fp4_gemm_nt_masked", "get_tma_aligned_size", "get_mk_alignment_for_contiguous_layout", "set_num_sms", "get_num_sms",
-    "get_gemm_config", "LIB_PATH",
+    "get_gemm_config", "fp8_kv_cache_empty", "fp8_kv_cache_write", "fp8_kv_cache_read", "fp8_paged_attention", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdg.so")
@@ -58,6 +58,11 @@ _SIGS = {
     "dg_k_grouped_fp8_gemm_nt_contiguous": (_i32, [_i32, _i32, _i32, _p, _p, _i64, _p, _p, _i64, _p, _p, _p, _p]),
     "dg_k_grouped_fp8_gemm_tn_contiguous": (_i32, [_i32, _i32, _i32, _p, _p, _i64, _p, _p, _i64, _p, _p, _p, _p]),
     "dg_per_token_group_cast_fp8": (_i32, [_i32, _i32, _p, _i64, _i32, _p, _i64, _p, _i64, _i32, _p]),
+    "dg_fp8_kv_cache_write": (_i32, [_p, _i32, _p, _i64, _i64, _p, _i64, _i64, _i32, _p, _p]),
+    "dg_fp8_kv_cache_read": (_i32, [_p, _i32, _p, _i64, _i64, _p, _i64, _i64, _i32, _p, _p]),
+    "dg_fp8_paged_attention": (_i32, [_p, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32,
+                                      ctypes.c_float, _i32, _i32, _p, _i64, _i64, _p, _p, _i64, _p]),
+    "dg_fp8_paged_attention_workspace": (_i64, [_i32] * 10),
     "dg_get_tma_aligned_size": (_i64, [_i64, _i32]),
     "dg_get_mk_alignment_for_contiguous_layout": (_i32, []),
     "dg_set_num_sms": (_i32, [_i32]),
@@ -550,3 +555,139 @@ def m_grouped_fp8_fp4_gemm_nt_masked(a, b, d, masked_m, expected_m=0):
         _ptr(B), B.stride(1), B.stride(0), _ptr(sfb_t), sfb_t.stride(-1), sfb_t.stride(0),
         _ptr(d), d.stride(1), d.stride(0), _out_dtype(d), _ptr(masked_m), int(expected_m), _stream(d)))
     return d
+
+
+# ---------------------------------------------------------------- FP8 key/value cache
+class _KvCache(ctypes.Structure):
+    """dg_fp8_kv_cache (include/dg.h)."""
+    _fields_ = [("k", _p), ("v", _p), ("k_sf", _p), ("v_sf", _p),
+                ("num_pages", _i32), ("num_heads", _i32), ("page_size", _i32), ("head_dim", _i32),
+                ("page_stride", _i64), ("head_stride", _i64), ("token_stride", _i64),
+                ("sf_page_stride", _i64), ("sf_head_stride", _i64), ("sf_token_stride", _i64)]
+
+
+_CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+_SF_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def fp8_kv_cache_empty(num_pages, num_kv_heads, page_size, head_dim, device="cuda"):
+    """``(k_cache, v_cache)`` of zeros, each ``(codes uint8 [pages, heads, page size, head dim],
+    UE8M0 scale codes uint8 [pages, heads, page size])``."""
+    def one():
+        return (torch.zeros((num_pages, num_kv_heads, page_size, head_dim), dtype=torch.uint8, device=device),
+                torch.full((num_pages, num_kv_heads, page_size), 127, dtype=torch.uint8, device=device))
+    return one(), one()
+
+
+def _kv_cache(k_cache, v_cache):
+    """The C struct of a cache, and its shape."""
+    (kc, ks), (vc, vs) = k_cache, v_cache
+    if kc.dtype not in _CODE_TYPES or vc.dtype not in _CODE_TYPES:
+        raise TypeError(f"cache codes must be uint8 or float8_e4m3fn, got {kc.dtype} and {vc.dtype}")
+    if ks.dtype not in _SF_TYPES or vs.dtype not in _SF_TYPES:
+        raise TypeError(f"cache scales must be uint8 or float8_e8m0fnu, got {ks.dtype} and {vs.dtype}")
+    shape, st, sf = kc.shape, kc.stride(), ks.stride()
+    if len(shape) != 4 or st[3] != 1 or vc.shape != shape or vc.stride() != st:
+        raise ValueError("cache codes must be [pages, heads, page size, head dim], contiguous along the last "
+                         "dimension, keys and values with the same shape and strides")
+    if ks.shape != shape[:3] or vs.shape != shape[:3] or vs.stride() != sf:
+        raise ValueError("cache scales must be [pages, heads, page size], keys' and values' with the same strides")
+    dev = kc.device
+    if not kc.is_cuda or vc.device != dev or ks.device != dev or vs.device != dev:
+        raise ValueError("the cache must be on one GPU")
+    return _KvCache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2], shape[3],
+                    st[0], st[1], st[2], sf[0], sf[1], sf[2]), shape, dev
+
+
+_IN_TYPES = {torch.bfloat16: DG_IN_BF16, torch.float32: DG_IN_F32}
+
+
+def _kv_move(fn, c, k, v, slots, shape, dev):
+    if k.dtype not in _IN_TYPES or v.dtype != k.dtype:
+        raise TypeError(f"k and v must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
+    n = slots.shape[0] if slots.dim() == 1 else -1
+    want = (n, shape[1], shape[3])
+    ks, vs = k.stride(), v.stride()
+    if tuple(k.shape) != want or tuple(v.shape) != want or ks[2] != 1 or vs[2] != 1:
+        raise ValueError(f"k and v must be [tokens, {shape[1]}, {shape[3]}], contiguous along the last dimension, with one slot for each token")
+    if slots.dtype != torch.int64 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 vector")
+    if k.device != dev or v.device != dev or slots.device != dev:
+        raise ValueError("k, v and slots must be on the cache's GPU")
+    _check(fn(ctypes.byref(c), n, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _IN_TYPES[k.dtype],
+              slots.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
+
+
+def fp8_kv_cache_write(k, v, k_cache, v_cache, slots):
+    """Quantise keys and values [tokens, kv heads, head dim] (BF16 or FP32) into the cache's slots.
+
+    ``k_cache``, ``v_cache``: ``(codes, scale codes)`` as ``fp8_kv_cache_empty`` makes them (any strides that
+    keep the head dimension contiguous), written in place.  ``slots``: int64 [tokens], page * page_size +
+    place in the page; a negative one, or one past the cache, is skipped.  No slot may be given twice."""
+    c, shape, dev = _kv_cache(k_cache, v_cache)
+    _kv_move(lib().dg_fp8_kv_cache_write, c, k, v, slots, shape, dev)
+
+
+def fp8_kv_cache_read(k_cache, v_cache, slots, out_dtype=torch.bfloat16, out=None):
+    """Keys and values of ``slots`` as ``(k, v)`` [tokens, kv heads, head dim] in BF16 or FP32, exact; zeros
+    for slots that are negative or past the cache.  ``out``: ``(k, v)`` to write into."""
+    c, shape, dev = _kv_cache(k_cache, v_cache)
+    if out is None:
+        want = (slots.shape[0], shape[1], shape[3])
+        out = (torch.empty(want, dtype=out_dtype, device=dev), torch.empty(want, dtype=out_dtype, device=dev))
+    k, v = out
+    _kv_move(lib().dg_fp8_kv_cache_read, c, k, v, slots, shape, dev)
+    return k, v
+
+
+def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q=None, max_seqlen_q=None,
+                        max_seqlen_k=None, sm_scale=None, window=0, sinks=0, out=None, return_lse=False):
+    """Causal attention of each sequence's newest tokens over its pages of an FP8 cache (their own keys and
+    values are already written).
+
+    ``q``: BF16 [total tokens, query heads, head dim], the sequences' new tokens one after the other.
+    ``block_table``: int32 [batch, columns], each sequence's pages in order.  ``seq_lens``: int32 [batch], tokens
+    in the cache, the new ones included.  ``cu_seqlens_q``: int32 [batch + 1], first row of each sequence; without
+    it every sequence has the same number of new tokens.  ``max_seqlen_q``: a bound of the new tokens of a
+    sequence (needed for a good split where ``cu_seqlens_q`` is given; default: all rows).  ``max_seqlen_k``: a
+    bound of ``seq_lens`` that only guides the split (default: the table's width).  ``sm_scale``: default
+    head_dim ** -0.5.  ``window`` > 0: a query sees its own and the ``window`` - 1 tokens before it, and the first
+    ``sinks`` tokens.  Returns ``out`` BF16 [total tokens, query heads, head dim], with ``return_lse`` also the
+    FP32 log sum of exponentials [total tokens, query heads]; a query that sees nothing gives zeros and -inf."""
+    c, shape, dev = _kv_cache(k_cache, v_cache)
+    hk, d = shape[1], shape[3]
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d or q.stride(2) != 1:
+        raise ValueError(f"q must be bfloat16 [tokens, heads, {d}], contiguous along the last dimension")
+    total, hq = q.shape[0], q.shape[1]
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [batch, columns], contiguous along its columns")
+    batch, cols = block_table.shape
+    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (batch,) or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens must be contiguous int32 [{batch}]")
+    if q.device != dev or block_table.device != dev or seq_lens.device != dev:
+        raise ValueError("q, block_table and seq_lens must be on the cache's GPU")
+    cu = None
+    if cu_seqlens_q is not None:
+        if (cu_seqlens_q.dtype != torch.int32 or tuple(cu_seqlens_q.shape) != (batch + 1,) or not cu_seqlens_q.is_contiguous()
+                or cu_seqlens_q.device != dev):
+            raise ValueError(f"cu_seqlens_q must be contiguous int32 [{batch + 1}] on the cache's GPU")
+        cu = cu_seqlens_q.data_ptr()
+    max_q = total if max_seqlen_q is None else int(max_seqlen_q)
+    max_k = cols * shape[2] if max_seqlen_k is None else int(max_seqlen_k)
+    if out is None:
+        out = torch.empty((total, hq, d), dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or out.stride(2) != 1 or out.device != dev:
+        raise ValueError("out must be bfloat16 of q's shape, contiguous along the last dimension, on the cache's GPU")
+    lse = torch.empty((total, hq), dtype=torch.float32, device=dev) if return_lse else None
+    handle = lib()
+    need = handle.dg_fp8_paged_attention_workspace(batch, total, hq, hk, d, int(cu is None), max_q, max_k, window, sinks)
+    if need < 0:
+        _check(need)
+    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    qs, os_ = q.stride(), out.stride()
+    _check(handle.dg_fp8_paged_attention(
+        ctypes.byref(c), batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(),
+        max(block_table.stride(0), cols), cols, seq_lens.data_ptr(), max_k, d ** -0.5 if sm_scale is None else sm_scale,
+        window, sinks, out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
+        None if work is None else work.data_ptr(), need, torch.cuda.current_stream(dev).cuda_stream))
+    return (out, lse) if return_lse else out

@@ -92,8 +92,14 @@ def build(verbose=False, jobs=None):
                   "-o", os.path.join(bdir, "dg_transform.o")])
     steps.append([HIPCC, *FLAGS, "-c", os.path.join(CSRC, "dg_quant.hip"),
                   "-o", os.path.join(bdir, "dg_quant.o")])
-    steps.append([HIPCC, "-O2", "-std=c++20", "-fPIC", f"--offload-arch={ARCH}", "-c", os.path.join(CSRC, "dg_api.cpp"),
-                  "-o", os.path.join(bdir, "dg_api.o")])
+    # (dg_attention: MFMA results in VGPRs here too, where the softmax reads them; without it the
+    # compiler moves them through accumulation registers and spills at head_dim 256)
+    for name in ("dg_kv_cache", "dg_attention"):
+        steps.append([HIPCC, *FLAGS, "-mllvm", "-amdgpu-mfma-vgpr-form", "-Rpass-analysis=kernel-resource-usage", "-c", os.path.join(CSRC, name + ".hip"),
+                      "-o", os.path.join(bdir, name + ".o")])
+    for name in ("dg_api", "dg_api_kv"):
+        steps.append([HIPCC, "-O2", "-std=c++20", "-fPIC", f"--offload-arch={ARCH}", "-c", os.path.join(CSRC, name + ".cpp"),
+                      "-o", os.path.join(bdir, name + ".o")])
     jobs = jobs or min(16, os.cpu_count() or 4)
     reports = []
     with ThreadPoolExecutor(max_workers=jobs) as ex:

@@ -10,6 +10,7 @@
 
 #include "../../include/dg.h"
 #include "dg_internal.h"
+#include "dg_kv.h"
 
 namespace {
 
@@ -30,6 +31,25 @@ int ok() {
   g_last_error.clear();
   return DG_OK;
 }
+
+}  // namespace
+
+// for the other host files
+namespace dg {
+int api_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return code;
+}
+int api_ok() { return ok(); }
+int api_num_sms() { return dg_get_num_sms(); }
+}  // namespace dg
+
+namespace {
 
 int64_t align4(int64_t x) { return (x + 3) / 4 * 4; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

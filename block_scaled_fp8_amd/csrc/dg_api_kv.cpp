@@ -1,0 +1,231 @@
+// C ABI of the FP8 key/value cache: argument validation, the split of the work, and launch.
+// Validation runs before any HIP call.
+#include <cmath>
+
+#include "../../include/dg.h"
+#include "dg_kv.h"
+
+namespace {
+
+using dg::api_fail;
+using dg::api_ok;
+
+constexpr int64_t kMaxIndex = int64_t(1) << 30;  // tokens, rows and keys are 32-bit numbers with room to subtract
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Checks of a cache; `empty`: nothing will be read or written, so its pointers may be NULL.
+int check_cache(const dg_fp8_kv_cache* c, bool empty) {
+  if (!c) return api_fail(DG_ERR_NULL, "cache must not be NULL");
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return api_fail(DG_ERR_UNSUPPORTED, "head_dim = %d: 64, 128 and 256 are supported", c->head_dim);
+  if (c->num_heads <= 0 || c->num_heads > 65535) return api_fail(DG_ERR_SHAPE, "num_heads = %d must be in [1, 65535]", c->num_heads);
+  if (c->page_size <= 0 || c->num_pages < 0) return api_fail(DG_ERR_SHAPE, "page_size = %d must be positive and num_pages = %d not negative", c->page_size, c->num_pages);
+  if (int64_t(c->num_pages) * c->page_size > kMaxIndex) return api_fail(DG_ERR_SHAPE, "the cache has more than 2^30 slots");
+  if (empty) return DG_OK;
+  if (c->num_pages == 0) return api_fail(DG_ERR_SHAPE, "the cache has no pages");
+  if (!c->k || !c->v || !c->k_sf || !c->v_sf) return api_fail(DG_ERR_NULL, "the cache's k, v, k_sf and v_sf must not be NULL");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return api_fail(DG_ERR_LAYOUT, "the cache's k and v must be 16-byte aligned");
+  if (c->page_stride % 16 || c->head_stride % 16 || c->token_stride % 16)
+    return api_fail(DG_ERR_LAYOUT, "the cache's page, head and token strides must be multiples of 16 bytes");
+  if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < c->head_dim)
+    return api_fail(DG_ERR_LAYOUT, "the cache's strides must not be negative, and token_stride at least head_dim");
+  if (c->sf_page_stride < 0 || c->sf_head_stride < 0 || c->sf_token_stride < 0)
+    return api_fail(DG_ERR_LAYOUT, "the cache's scale strides must not be negative");
+  return DG_OK;
+}
+
+dg::KvCache kernel_cache(const dg_fp8_kv_cache* c) {
+  dg::KvCache k{};
+  k.k = static_cast<uint8_t*>(c->k);
+  k.v = static_cast<uint8_t*>(c->v);
+  k.k_sf = c->k_sf;
+  k.v_sf = c->v_sf;
+  k.page_stride = c->page_stride;
+  k.head_stride = c->head_stride;
+  k.token_stride = c->token_stride;
+  k.sf_page_stride = c->sf_page_stride;
+  k.sf_head_stride = c->sf_head_stride;
+  k.sf_token_stride = c->sf_token_stride;
+  k.num_pages = c->num_pages;
+  k.num_heads = c->num_heads;
+  k.page = dg::fast_div(c->page_size);
+  return k;
+}
+
+// Rows [tokens, heads, head_dim] that are read or written with 16-byte accesses.
+int check_rows(const char* name, const void* p, int64_t token_stride, int64_t head_stride, int esz) {
+  if (!p) return api_fail(DG_ERR_NULL, "%s must not be NULL", name);
+  if (!aligned(p, 16) || (token_stride * esz) % 16 || (head_stride * esz) % 16)
+    return api_fail(DG_ERR_LAYOUT, "%s must have 16-byte aligned rows (start, token stride and head stride)", name);
+  if (token_stride < 0 || head_stride < 0) return api_fail(DG_ERR_LAYOUT, "%s's strides must not be negative", name);
+  return DG_OK;
+}
+
+int move(bool write, const dg_fp8_kv_cache* cache, int32_t num_tokens, const void* k, int64_t k_token_stride,
+         int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride, int32_t dtype,
+         const int64_t* slots, hipStream_t stream) {
+  if (dtype != DG_IN_BF16 && dtype != DG_IN_F32) return api_fail(DG_ERR_DTYPE, "dtype %d is not DG_IN_BF16 or DG_IN_F32", dtype);
+  if (num_tokens < 0 || num_tokens > kMaxIndex) return api_fail(DG_ERR_SHAPE, "num_tokens = %d must be in [0, 2^30]", num_tokens);
+  if (int s = check_cache(cache, num_tokens == 0)) return s;
+  if (num_tokens == 0) return api_ok();
+  const int esz = dtype == DG_IN_BF16 ? 2 : 4;
+  if (int s = check_rows("k", k, k_token_stride, k_head_stride, esz)) return s;
+  if (int s = check_rows("v", v, v_token_stride, v_head_stride, esz)) return s;
+  if (!slots) return api_fail(DG_ERR_NULL, "slots must not be NULL");
+  if (!aligned(slots, 8)) return api_fail(DG_ERR_LAYOUT, "slots must be 8-byte aligned");
+  dg::KvMoveParams p{};
+  p.c = kernel_cache(cache);
+  p.k = const_cast<void*>(k);
+  p.v = const_cast<void*>(v);
+  p.k_token_stride = k_token_stride;
+  p.k_head_stride = k_head_stride;
+  p.v_token_stride = v_token_stride;
+  p.v_head_stride = v_head_stride;
+  p.slots = slots;
+  p.num_tokens = num_tokens;
+  const bool bf16 = dtype == DG_IN_BF16;
+  const hipError_t e = write ? dg::launch_kv_write(p, cache->head_dim, bf16, stream) : dg::launch_kv_read(p, cache->head_dim, bf16, stream);
+  if (e != hipSuccess) return api_fail(DG_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  return api_ok();
+}
+
+// ---------------------------------------------------------------- attention
+struct AttnPlan {
+  bool wide = false;
+  int q_tiles = 1, splits = 1;
+};
+
+// keys: the most keys that a row can see (from the host's bounds).
+AttnPlan plan_attention(int64_t batch, int kv_heads, int64_t rows, int64_t keys, int num_sms) {
+  AttnPlan pl;
+  pl.wide = rows > 2 * dg::kAttnNarrowRows;
+  const int tile = pl.wide ? dg::kAttnWideRows : dg::kAttnNarrowRows;
+  pl.q_tiles = int((rows + tile - 1) / tile);
+  const int64_t blocks = batch * kv_heads * pl.q_tiles;
+  const int64_t want = (2 * int64_t(num_sms) + blocks - 1) / blocks;
+  const int64_t most = keys / 256;  // at least 256 keys in a part
+  int64_t s = want < most ? want : most;
+  if (pl.wide && blocks >= num_sms) s = 1;
+  pl.splits = int(s < 1 ? 1 : s > 256 ? 256 : s);
+  return pl;
+}
+
+struct AttnShape {
+  int32_t batch, total_q, num_q_heads, max_seqlen_q, max_seqlen_k, window, sinks;
+  bool equal;
+};
+
+int check_shape(const AttnShape& a, int32_t num_kv_heads) {
+  if (a.batch < 0 || a.total_q < 0) return api_fail(DG_ERR_SHAPE, "batch = %d and total_q = %d must not be negative", a.batch, a.total_q);
+  if (num_kv_heads <= 0 || a.num_q_heads <= 0 || a.num_q_heads % num_kv_heads)
+    return api_fail(DG_ERR_SHAPE, "num_q_heads = %d must be a positive multiple of the cache's %d heads", a.num_q_heads, num_kv_heads);
+  if (int64_t(a.total_q) * a.num_q_heads > kMaxIndex) return api_fail(DG_ERR_SHAPE, "total_q * num_q_heads must be at most 2^30");
+  if (a.window < 0 || a.sinks < 0) return api_fail(DG_ERR_SHAPE, "window = %d and sinks = %d must not be negative", a.window, a.sinks);
+  if (a.max_seqlen_q < 0 || a.max_seqlen_k < 0) return api_fail(DG_ERR_SHAPE, "max_seqlen_q = %d and max_seqlen_k = %d must not be negative", a.max_seqlen_q, a.max_seqlen_k);
+  if (a.equal && a.batch > 0 && a.total_q % a.batch) return api_fail(DG_ERR_SHAPE, "without cu_seqlens_q, total_q = %d must be a multiple of batch = %d", a.total_q, a.batch);
+  return DG_OK;
+}
+
+AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int num_sms) {
+  const int64_t per_seq = a.equal ? a.total_q / a.batch : a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+  int64_t keys = a.max_seqlen_k;
+  if (a.window && a.window < keys - a.sinks) keys = int64_t(a.window) + a.sinks;
+  return plan_attention(a.batch, num_kv_heads, per_seq * (a.num_q_heads / num_kv_heads), keys, num_sms);
+}
+
+int64_t workspace_of(const AttnShape& a, const AttnPlan& pl, int32_t head_dim) {
+  return pl.splits == 1 ? 0 : int64_t(pl.splits) * a.total_q * a.num_q_heads * (head_dim + 2) * int64_t(sizeof(float));
+}
+
+}  // namespace
+
+extern "C" {
+
+int dg_fp8_kv_cache_write(const dg_fp8_kv_cache* cache, int32_t num_tokens, const void* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                          int32_t dtype, const int64_t* slots, hipStream_t stream) {
+  return move(true, cache, num_tokens, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, dtype, slots, stream);
+}
+
+int dg_fp8_kv_cache_read(const dg_fp8_kv_cache* cache, int32_t num_tokens, void* k, int64_t k_token_stride,
+                         int64_t k_head_stride, void* v, int64_t v_token_stride, int64_t v_head_stride,
+                         int32_t dtype, const int64_t* slots, hipStream_t stream) {
+  return move(false, cache, num_tokens, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, dtype, slots, stream);
+}
+
+int64_t dg_fp8_paged_attention_workspace(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t equal_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                         int32_t window, int32_t sinks) {
+  const AttnShape a{batch, total_q, num_q_heads, max_seqlen_q, max_seqlen_k, window, sinks, equal_q != 0};
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return api_fail(DG_ERR_UNSUPPORTED, "head_dim = %d: 64, 128 and 256 are supported", head_dim);
+  if (int s = check_shape(a, num_kv_heads)) return s;
+  if (batch == 0 || total_q == 0 || (!a.equal && max_seqlen_q == 0)) return 0;
+  const int num_sms = dg::api_num_sms();
+  if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
+  return workspace_of(a, plan_of(a, num_kv_heads, num_sms), head_dim);
+}
+
+int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t total_q, int32_t num_q_heads,
+                           const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                           const int32_t* cu_seqlens_q, int32_t max_seqlen_q,
+                           const int32_t* block_table, int64_t table_stride, int32_t table_cols,
+                           const int32_t* seq_lens, int32_t max_seqlen_k, float sm_scale, int32_t window, int32_t sinks,
+                           void* out, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                           void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  const AttnShape a{batch, total_q, num_q_heads, max_seqlen_q, max_seqlen_k, window, sinks, cu_seqlens_q == nullptr};
+  const bool empty = batch == 0 || total_q == 0 || (cu_seqlens_q && max_seqlen_q == 0);
+  if (int s = check_cache(cache, empty)) return s;
+  if (int s = check_shape(a, cache->num_heads)) return s;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return api_fail(DG_ERR_SHAPE, "sm_scale must be positive and finite");
+  if (table_cols < 0 || table_stride < table_cols) return api_fail(DG_ERR_LAYOUT, "table_cols = %d must not be negative, and table_stride = %lld at least as large", table_cols, (long long)table_stride);
+  if (int64_t(table_cols) * cache->page_size > kMaxIndex) return api_fail(DG_ERR_SHAPE, "table_cols * page_size must be at most 2^30");
+  if (empty) return api_ok();
+  if (!block_table && table_cols > 0) return api_fail(DG_ERR_NULL, "block_table must not be NULL");
+  if (!seq_lens) return api_fail(DG_ERR_NULL, "seq_lens must not be NULL");
+  if (int s = check_rows("q", q, q_token_stride, q_head_stride, 2)) return s;
+  if (int s = check_rows("out", out, o_token_stride, o_head_stride, 2)) return s;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_seqlens_q, 4) || !aligned(lse, 4))
+    return api_fail(DG_ERR_LAYOUT, "block_table, seq_lens, cu_seqlens_q and lse must be 4-byte aligned");
+  const int num_sms = dg::api_num_sms();
+  if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
+  const AttnPlan pl = plan_of(a, cache->num_heads, num_sms);
+  const int64_t need = workspace_of(a, pl, cache->head_dim);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);
+  if (need > 0 && !aligned(workspace, 16)) return api_fail(DG_ERR_LAYOUT, "workspace must be 16-byte aligned");
+
+  dg::AttnParams p{};
+  p.c = kernel_cache(cache);
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_token_stride = q_token_stride;
+  p.q_head_stride = q_head_stride;
+  p.out = static_cast<uint16_t*>(out);
+  p.o_token_stride = o_token_stride;
+  p.o_head_stride = o_head_stride;
+  p.lse = lse;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_seqlens_q;
+  p.table_cols = table_cols;
+  p.batch = batch;
+  p.total_q = total_q;
+  p.q_per_seq = cu_seqlens_q ? 0 : total_q / batch;
+  p.num_q_heads = num_q_heads;
+  p.group = dg::fast_div(num_q_heads / cache->num_heads);
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  // (a window that holds every possible key hides nothing)
+  p.window = window < int64_t(table_cols) * cache->page_size ? window : 0;
+  p.sinks = p.window ? sinks : 0;
+  p.q_tiles = pl.q_tiles;
+  p.splits = pl.splits;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = pl.splits > 1 ? p.part_o + int64_t(pl.splits) * total_q * num_q_heads * cache->head_dim : nullptr;
+  const hipError_t e = dg::launch_attention(p, cache->head_dim, pl.wide, stream);
+  if (e != hipSuccess) return api_fail(DG_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  return api_ok();
+}
+
+}  // extern "C"

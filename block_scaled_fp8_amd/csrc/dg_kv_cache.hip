@@ -1,0 +1,181 @@
+// FP8 key/value cache for gfx950 (MI355X): quantising tokens' keys and values into their slots,
+// and reading them back.
+//
+// A row is one token and head: D values (64, 128 or 256), stored as E4M3 codes with one
+// power-of-two scale, s = amax / 448 raised to the next power of two (1 for a row of zeros), kept
+// as its exponent code sf (UE8M0): value = code * 2^(sf - 127).  A power of two costs E4M3 no
+// relative precision (both the quotient and the product with it are exact) and lets a reader
+// widen codes to BF16 exactly in one conversion.
+//
+// Both directions are bound by memory: D * (input size + 1) + 1 bytes a row.  A row is D / 8
+// lanes of 8 values (16 bytes of BF16), a lane handles the key and the value row of its token
+// and head, and a workgroup takes consecutive tokens of one head, whose cache rows and scale
+// bytes are neighbours when their slots are.
+#include "dg_kv.h"
+
+namespace dg {
+namespace {
+
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+constexpr int THREADS = 256;
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t at, float (&x)[8]) {
+  if constexpr (BF16) {
+    const v4u r = *(const v4u*)((const uint16_t*)base + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(r[i] << 16);
+      x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+    }
+  } else {
+    const v4u r0 = *(const v4u*)((const float*)base + at), r1 = *(const v4u*)((const float*)base + at + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __uint_as_float(r0[i]);
+      x[4 + i] = __uint_as_float(r1[i]);
+    }
+  }
+}
+
+// Codes of a lane's 8 values and the row's scale code.  The row's lanes are L consecutive ones.
+// An infinite value does not count for the scale and saturates; a NaN becomes the NaN code.
+template <int L>
+__device__ __forceinline__ v2u encode8(const float (&x)[8], uint32_t& sf) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(x[i]);
+    amax = a < __builtin_inff() ? fmaxf(amax, a) : amax;
+  }
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+  // 448 = 1.75 * 2^8: the smallest power of two >= amax / 448 has amax's exponent minus 8, plus
+  // one when amax's mantissa is above 1.75
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  // (up to 224 of FP32's smallest steps, amax / 448 is zero in FP32, as for a row of zeros)
+  sf = b <= 224u ? 127u : (uint32_t)max(e, 1);
+  const float inv = __uint_as_float((254u - sf) << 23);  // 1 / s, exact (s <= 2^120)
+  float c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = fminf(fmaxf(x[i] * inv, -448.f), 448.f);
+    c[i] = x[i] == x[i] ? y : x[i];
+  }
+  v2u r;
+  r.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+  r.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], (int)r.x, true);
+  r.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
+  r.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], (int)r.y, true);
+  return r;
+}
+
+struct Place {
+  int64_t code, sf;  // byte offsets of the row
+};
+__device__ __forceinline__ bool place_of(const KvCache& c, int64_t slot, int head, Place& at) {
+  const int64_t slots = (int64_t)c.num_pages * c.page.d;
+  if (slot < 0 || slot >= slots) return false;
+  // (the host keeps num_pages * page size below 2^31)
+  const int32_t page = div((int32_t)slot, c.page), off = (int32_t)slot - page * c.page.d;
+  at.code = page * c.page_stride + head * c.head_stride + off * c.token_stride;
+  at.sf = page * c.sf_page_stride + head * c.sf_head_stride + off * c.sf_token_stride;
+  return true;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(THREADS) kv_write_kernel(const KvMoveParams p) {
+  constexpr int L = D / 8;
+  const int token = blockIdx.x * (THREADS / L) + threadIdx.x / L, head = blockIdx.y, l = threadIdx.x % L;
+  // (a whole row's lanes leave together, so the shuffles below stay within live lanes)
+  if (token >= p.num_tokens) return;
+  Place at;
+  if (!place_of(p.c, p.slots[token], head, at)) return;
+  float k[8], v[8];
+  load8<BF16>(p.k, token * p.k_token_stride + head * p.k_head_stride + 8 * l, k);
+  load8<BF16>(p.v, token * p.v_token_stride + head * p.v_head_stride + 8 * l, v);
+  uint32_t ksf, vsf;
+  const v2u kc = encode8<L>(k, ksf), vc = encode8<L>(v, vsf);
+  *(v2u*)(p.c.k + at.code + 8 * l) = kc;
+  *(v2u*)(p.c.v + at.code + 8 * l) = vc;
+  if (l == 0) {
+    p.c.k_sf[at.sf] = (uint8_t)ksf;
+    p.c.v_sf[at.sf] = (uint8_t)vsf;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, int64_t at, v2u codes, uint32_t sf) {
+  const float s = __uint_as_float(sf << 23);
+  if constexpr (BF16) {
+    v4u r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, false));
+      r[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, true));
+    }
+    *(v4u*)((uint16_t*)base + at) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes[i], s, false);
+      const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes[i], s, true);
+      *(v4u*)((float*)base + at + 4 * i) =
+          (v4u){__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)};
+    }
+  }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(THREADS) kv_read_kernel(const KvMoveParams p) {
+  constexpr int L = D / 8;
+  const int token = blockIdx.x * (THREADS / L) + threadIdx.x / L, head = blockIdx.y, l = threadIdx.x % L;
+  if (token >= p.num_tokens) return;
+  v2u kc = {0, 0}, vc = {0, 0};
+  uint32_t ksf = 127, vsf = 127;  // a skipped slot reads as zeros
+  Place at;
+  if (place_of(p.c, p.slots[token], head, at)) {
+    kc = *(const v2u*)(p.c.k + at.code + 8 * l);
+    vc = *(const v2u*)(p.c.v + at.code + 8 * l);
+    ksf = p.c.k_sf[at.sf];
+    vsf = p.c.v_sf[at.sf];
+  }
+  store8<BF16>(p.k, token * p.k_token_stride + head * p.k_head_stride + 8 * l, kc, ksf);
+  store8<BF16>(p.v, token * p.v_token_stride + head * p.v_head_stride + 8 * l, vc, vsf);
+}
+
+dim3 grid_of(const KvMoveParams& p, int head_dim) {
+  const int per = THREADS / (head_dim / 8);
+  return dim3((p.num_tokens + per - 1) / per, p.c.num_heads);
+}
+
+}  // namespace
+
+#define DG_KV_CASES(K)                                                             \
+  if (head_dim == 64 && bf16) hipLaunchKernelGGL((K<64, true>), g, b, 0, stream, p);    \
+  else if (head_dim == 64) hipLaunchKernelGGL((K<64, false>), g, b, 0, stream, p);      \
+  else if (head_dim == 128 && bf16) hipLaunchKernelGGL((K<128, true>), g, b, 0, stream, p); \
+  else if (head_dim == 128) hipLaunchKernelGGL((K<128, false>), g, b, 0, stream, p);    \
+  else if (head_dim == 256 && bf16) hipLaunchKernelGGL((K<256, true>), g, b, 0, stream, p); \
+  else if (head_dim == 256) hipLaunchKernelGGL((K<256, false>), g, b, 0, stream, p);    \
+  else return hipErrorInvalidValue;
+
+hipError_t launch_kv_write(const KvMoveParams& p, int head_dim, bool bf16, hipStream_t stream) {
+  const dim3 g = grid_of(p, head_dim), b(THREADS);
+  DG_KV_CASES(kv_write_kernel)
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const KvMoveParams& p, int head_dim, bool bf16, hipStream_t stream) {
+  const dim3 g = grid_of(p, head_dim), b(THREADS);
+  DG_KV_CASES(kv_read_kernel)
+  return hipGetLastError();
+}
+#undef DG_KV_CASES
+
+}  // namespace dg

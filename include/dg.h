@@ -353,6 +353,104 @@ int dg_transform_sf(const float* sf_in, int32_t num_groups, int32_t mn, int32_t 
                     int32_t gran_mn, int32_t pack_ue8m0, void* sf_out,
                     int32_t* nonpow2_count, hipStream_t stream);
 
+/*
+ * FP8 key/value cache in pages.
+ *
+ * A row is one token and head: head_dim values, held as E4M3 codes with ONE power-of-two scale,
+ *   s = max|x| / 448 (FP32) raised to the next power of two (1 where that quotient is zero, at least 2^-126),
+ * kept as its UE8M0 code sf: value = code * 2^(sf - 127).  (The recipe of
+ * dg_per_token_group_cast_fp8 with DG_SF_UE8M0X4, the group being the head.)  A power of two costs
+ * E4M3 no relative precision, and codes times scale are exact in BF16.
+ *
+ *  k, v             : E4M3 codes [num_pages, num_heads, page_size, head_dim]; element d of a row at
+ *                     k[page*page_stride + head*head_stride + place*token_stride + d].  Strides in
+ *                     bytes, the same for k and v, multiples of 16; k and v 16-byte aligned.  Any order
+ *                     of pages, heads and tokens is allowed; the rows must not overlap.
+ *  k_sf, v_sf       : UE8M0 codes [num_pages, num_heads, page_size] (sf_*_stride in bytes).  Codes 1 to
+ *                     254 are meant; 0 and 255 give unspecified values.
+ *  head_dim         : 64, 128 or 256.  page_size: any positive number of tokens.
+ *                     num_pages * page_size <= 2^30.
+ * A token's slot is page * page_size + place.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_sf;
+  uint8_t* v_sf;
+  int32_t num_pages, num_heads, page_size, head_dim;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t sf_page_stride, sf_head_stride, sf_token_stride;
+} dg_fp8_kv_cache;
+
+/*
+ * Quantise num_tokens tokens' keys and values into their slots.
+ *  k, v          : BF16 or FP32 (dtype: DG_IN_BF16, DG_IN_F32) [num_tokens, num_heads, head_dim], strides in
+ *                  elements; rows (start, token and head strides) 16-byte aligned.
+ *  slots         : device int64 [num_tokens].  A slot that is negative or past the cache is skipped.
+ *                  Precondition (not checked): no slot is given twice.
+ * Codes are rounded to nearest, ties to even.  Infinities do not count for the scale and saturate to
+ * +-448 s; a NaN is stored as the NaN code 0x7f or 0xff.  num_tokens == 0 is a no-op.
+ */
+int dg_fp8_kv_cache_write(const dg_fp8_kv_cache* cache, int32_t num_tokens, const void* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                          int32_t dtype, const int64_t* slots, hipStream_t stream);
+
+/*
+ * Read slots back: k and v [num_tokens, num_heads, head_dim] as BF16 or FP32, both exact (the smallest
+ * scales apart, where BF16 or FP32 runs out of exponent).  A slot that is negative or past the cache gives zeros.
+ * Arguments as in dg_fp8_kv_cache_write; a slot may be given more than once.
+ */
+int dg_fp8_kv_cache_read(const dg_fp8_kv_cache* cache, int32_t num_tokens, void* k, int64_t k_token_stride,
+                         int64_t k_head_stride, void* v, int64_t v_token_stride, int64_t v_head_stride,
+                         int32_t dtype, const int64_t* slots, hipStream_t stream);
+
+/*
+ * Causal attention of each sequence's newest tokens over its cache (single tokens, a few speculated
+ * ones, or a chunk of a prompt; the new tokens' keys and values are already in the cache):
+ *
+ *   out = sum_j softmax_j(sm_scale * q . k_j) v_j    over the keys j that the query sees.
+ *
+ * Query i of the n new tokens of a sequence with seq_len tokens in all stands at place
+ * x = seq_len - n + i and sees the keys j <= x; with window > 0 only those with j > x - window or
+ * j < sinks (the first tokens, which stay visible).  A query that sees no key (x < 0) gives zeros
+ * and lse = -infinity.  Query head h reads key head h / (num_q_heads / num_heads).
+ *
+ *  q             : BF16 [total_q, num_q_heads, head_dim], the sequences' new tokens one after the other; strides
+ *                  in elements, rows 16-byte aligned.
+ *  cu_seqlens_q  : device int32 [batch + 1], first row of each sequence (non-decreasing; [0] and [batch] bound the
+ *                  rows that are written), or NULL: every sequence has total_q / batch.
+ *  max_seqlen_q  : with cu_seqlens_q, at least the most new tokens of a sequence (rows past it are not
+ *                  computed); not read without.
+ *  block_table   : device int32 [batch, table_cols] with row stride table_stride: the pages of each
+ *                  sequence in order.  Entries for places that no query sees are not used; a used entry
+ *                  outside the cache reads page 0.  table_cols * page_size <= 2^30.
+ *  seq_lens      : device int32 [batch]; clamped to [0, table_cols * page_size].
+ *  max_seqlen_k  : the host's bound of seq_lens, used only to split the work; it never changes which keys count.
+ *  sm_scale      : positive and finite.
+ *  out           : BF16 [total_q, num_q_heads, head_dim], strides in elements, rows 16-byte aligned.
+ *  lse           : NULL, or FP32 [total_q, num_q_heads] contiguous: log sum_j exp(sm_scale * q . k_j).
+ *  workspace     : device memory of at least dg_fp8_paged_attention_workspace() bytes for the same
+ *                  arguments, 16-byte aligned; contents on entry do not matter.  NULL where that is 0.
+ * Products take BF16 operands (the cache's values exactly; the softmax weights rounded to BF16) and
+ * accumulate in FP32; maxima and sums are FP32.  Results do not depend on the run (no atomics), but
+ * the split, and with it the last bits, depends on batch, max_seqlen_q and max_seqlen_k.
+ * A NaN in the cache at a place that some query sees may also reach the other queries of its call
+ * and sequence.  batch == 0 or total_q == 0 is a no-op.
+ */
+int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t total_q, int32_t num_q_heads,
+                           const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                           const int32_t* cu_seqlens_q, int32_t max_seqlen_q,
+                           const int32_t* block_table, int64_t table_stride, int32_t table_cols,
+                           const int32_t* seq_lens, int32_t max_seqlen_k, float sm_scale, int32_t window, int32_t sinks,
+                           void* out, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                           void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Workspace of dg_fp8_paged_attention in bytes (0: none), or a negative dg_status.  equal_q: 1 where
+ * cu_seqlens_q is NULL. */
+int64_t dg_fp8_paged_attention_workspace(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t equal_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                         int32_t window, int32_t sinks);
+
 /* align(mn, 16 / elem_bytes): the padded MN extent of an MN-major scale tensor whose
  * K slices start on 16-byte boundaries (page "02 · DeepGEMM 技术解析" §3.1, ALIGN_MN).
  * elem_bytes must be 1, 2, 4, 8 or 16; returns -1 otherwise. */

@@ -27,14 +27,16 @@ Modules:
              M-grouped forms, and the nn / tn / tt operand layouts (operands stored
              transposed)
   quant   -- the per-token-group FP8 cast (E4M3 codes and 1x128 FP32 scales)
+  kv_cache -- the FP8 key/value cache (encode, write, read) and causal attention over its pages,
+             with a window and first tokens that stay visible
 
 Parity pins: every function here is pinned by a `-m "not gpu"` test in
-``tests/test_oracle_pins.py`` against something other than itself (closed
+``tests/test_oracle_pins.py`` or ``tests/test_kv_host.py`` against something other than itself (closed
 forms, worked examples printed on the pages, exact rational brute force,
 library routines on special cases).  No function is "parity unpinned"; the
 comparison with the original CUDA library itself cannot be made here.
 """
-from . import codecs, layout, gemm, quant  # noqa: F401
+from . import codecs, layout, gemm, quant, kv_cache  # noqa: F401
 from .codecs import (e4m3_decode_table, e4m3_decode, ue8m0_encode, ue8m0_decode,
                      bf16_rne, bf16_bits_to_f64, pow2_violation, e2m1_decode_table, e2m1_decode,
                      unpack_fp4)  # noqa: F401
@@ -44,3 +46,4 @@ from .gemm import (gemm_nt, gemm_nt_points, grouped_contiguous, grouped_masked, 
                    grouped_masked_fp8_fp4, LAYOUTS, as_mk, as_nk, gemm_layout, gemm_layout_points,
                    grouped_contiguous_nn, k_grouped_tn, gemm_fp8_fp4_tt)  # noqa: F401
 from .quant import e4m3_encode_rne, per_token_group_cast  # noqa: F401
+from .kv_cache import kv_encode, kv_decode, kv_write, kv_read, visible, paged_attention  # noqa: F401

@@ -1,0 +1,350 @@
+"""GPU parity of the FP8 key/value cache (write, read back) and of the attention that reads it, through
+the binding, against the float64 oracle."""
+import contextlib
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp8_amd as dg
+import oracle
+from tests import kv_gen
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def cuda(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def bits(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def same(a, b):
+    """Arrays equal, NaN for NaN (says where not, not what)."""
+    a, b = np.asarray(a), np.asarray(b)
+    ok = (a == b) | ((a != a) & (b != b))
+    if not ok.all():
+        at = np.argwhere(~ok)
+        say("differ at", len(at), "places, first", at[:4].tolist(), a[~ok][:4], b[~ok][:4])
+    return bool(ok.all())
+
+
+@contextlib.contextmanager
+def num_sms(n):
+    """Plan for n compute units: more of them split the keys into more parts."""
+    dg.set_num_sms(n)
+    try:
+        yield
+    finally:
+        dg.set_num_sms(0)
+
+
+# ---------------------------------------------------------------- write
+def rand_cache(rng, pages, heads, page, dim):
+    return (rng.integers(0, 0x7F, (pages, heads, page, dim)).astype(np.uint8), rng.integers(100, 140, (pages, heads, page)).astype(np.uint8))
+
+
+def tricky_rows(rng, tokens, heads, dim):
+    """Rows whose scale or rounding sits on an edge: zeros, amax at and beside 448 * 2^e, halfway values,
+    FP32 subnormals, the largest numbers."""
+    x = kv_gen.rows(rng, tokens, heads, dim, wide=True)
+    f = x.reshape(-1, dim)
+    f[0] = 0.0
+    f[1] = -0.0
+    for i, e in enumerate((-130, -126, -100, -3, 0, 5, 100)):
+        top = np.float32(448.0) * np.float32(2.0 ** e) if e > -127 else np.float32(2.0 ** -125)
+        for j, t in enumerate((np.nextafter(top, np.float32(0)), top, np.nextafter(top, np.float32(np.inf)))):
+            r = 2 + 3 * i + j
+            f[r] = rng.uniform(-1, 1, dim).astype(np.float32) * t
+            f[r, r % dim] = t * (-1 if j == 1 else 1)
+    f[23] = np.float32(2.0 ** -149)
+    f[24] = np.finfo(np.float32).max
+    f[25] = (rng.integers(8, 16, dim) + 0.5).astype(np.float32) * 2.0 ** rng.integers(-6, 5, dim)  # ties
+    f[25, 0] = 448.0
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim,heads,page,order", [(64, 5, 16, "hpt"), (128, 8, 64, "hpt"), (128, 3, 48, "thd"), (256, 2, 7, "thd"),
+                                                  (64, 1, 1, "hpt")])
+def test_write_is_bitwise(dtype, dim, heads, page, order):
+    rng = np.random.default_rng(dim + heads + page)
+    tokens = 61
+    x = [tricky_rows(rng, tokens, heads, dim) for _ in range(2)]
+    if dtype == torch.bfloat16:
+        x = [oracle.bf16_bits_to_f64(oracle.bf16_rne(np.clip(v, -3e38, 3e38))).astype(np.float32) for v in x]
+    pages = -(-tokens // page) + 3
+    slots = rng.permutation(pages * page)[:tokens].astype(np.int64)
+    slots[[3, 17]] = [-1, -(2 ** 40)]
+    slots[[5, 20]] = [pages * page, 2 ** 40]
+    before = [rand_cache(rng, pages, heads, page, dim) for _ in range(2)]
+    say("kv write", dtype, dim, heads, page, order)
+    # new tokens' keys and values as slices of one projection's output
+    qkv = torch.empty((tokens, 3 * heads, dim), dtype=dtype, device=DEV)
+    k, v = qkv[:, heads:2 * heads], qkv[:, 2 * heads:]
+    k.copy_(cuda(x[0]))
+    v.copy_(cuda(x[1]))
+    if order == "hpt":
+        caches = [(cuda(c), cuda(s)) for c, s in before]
+    else:  # tokens outermost within a page
+        caches = [(cuda(c.swapaxes(1, 2)).transpose(1, 2), cuda(s.swapaxes(1, 2)).transpose(1, 2)) for c, s in before]
+    dg.fp8_kv_cache_write(k, v, caches[0], caches[1], cuda(slots))
+    torch.cuda.synchronize()
+    for i in range(2):
+        codes, sf = oracle.kv_write(before[i], x[i], slots)
+        assert same(caches[i][1].cpu().numpy(), sf), i
+        assert same(caches[i][0].cpu().numpy(), codes), i
+
+
+def test_write_infinities_and_nans():
+    """An infinity saturates and does not count for the scale; a NaN becomes the NaN code; neighbours are not touched."""
+    rng = np.random.default_rng(0)
+    x = kv_gen.rows(rng, 3, 2, 64)
+    want = [oracle.kv_encode(x), None]
+    y = x.copy()
+    at = np.abs(y).argmin(axis=-1)  # (an element that does not set the scale)
+    y[0, 0, at[0, 0]], y[0, 1, at[0, 1]] = np.inf, -np.inf
+    y[1, 0, at[1, 0]] = np.nan
+    k_cache, v_cache = dg.fp8_kv_cache_empty(1, 2, 4, 64, device=DEV)
+    say("kv write, non-finite values")
+    dg.fp8_kv_cache_write(cuda(y), cuda(x), k_cache, v_cache, torch.arange(3, device=DEV))
+    torch.cuda.synchronize()
+    codes, sf = want[0][0].copy(), want[0][1]
+    codes[0, 0, at[0, 0]], codes[0, 1, at[0, 1]] = 0x7E, 0xFE
+    got = k_cache[0][0].cpu().numpy().swapaxes(0, 1)[:3]
+    assert got[1, 0, at[1, 0]] & 0x7F == 0x7F
+    codes[1, 0, at[1, 0]] = got[1, 0, at[1, 0]]
+    assert same(got, codes) and same(k_cache[1][0].cpu().numpy().T[:3], sf)
+    assert same(v_cache[0][0].cpu().numpy().swapaxes(0, 1)[:3], want[0][0])
+    allinf = torch.full((1, 2, 64), float("inf"), device=DEV)
+    dg.fp8_kv_cache_write(allinf, allinf, k_cache, v_cache, torch.tensor([3], device=DEV))
+    torch.cuda.synchronize()
+    assert (k_cache[0][0, :, 3].cpu() == 0x7E).all() and (k_cache[1][0, :, 3].cpu() == 127).all()
+
+
+def test_write_and_read_of_nothing():
+    k_cache, v_cache = dg.fp8_kv_cache_empty(2, 2, 4, 64, device=DEV)
+    x = torch.empty((0, 2, 64), device=DEV)
+    slots = torch.empty((0,), dtype=torch.int64, device=DEV)
+    dg.fp8_kv_cache_write(x, x, k_cache, v_cache, slots)
+    k, v = dg.fp8_kv_cache_read(k_cache, v_cache, slots)
+    assert k.shape == (0, 2, 64) and v.dtype == torch.bfloat16
+
+
+# ---------------------------------------------------------------- read
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim,heads,page", [(64, 3, 16), (128, 8, 64), (256, 1, 5)])
+def test_read_is_exact(dtype, dim, heads, page):
+    rng = np.random.default_rng(dim)
+    pages = 6
+    cache = [(rng.integers(0, 256, (pages, heads, page, dim)).astype(np.uint8), rng.integers(20, 230, (pages, heads, page)).astype(np.uint8))
+             for _ in range(2)]
+    slots = rng.integers(-2, pages * page + 2, 77).astype(np.int64)
+    say("kv read", dtype, dim, heads, page)
+    out = tuple(torch.full((77, heads + 1, dim), 5.0, dtype=dtype, device=DEV)[:, :heads] for _ in range(2))
+    got = dg.fp8_kv_cache_read(*[(cuda(c).view(torch.float8_e4m3fn), cuda(s).view(torch.float8_e8m0fnu)) for c, s in cache], cuda(slots),
+                               out_dtype=dtype, out=out)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert same(got[i].double().cpu().numpy(), oracle.kv_read(cache[i], slots))
+
+
+# ---------------------------------------------------------------- attention
+def run(p, window=0, sinks=0, lse=True, scale=None, **kw):
+    caches = [(cuda(p[x][0]), cuda(p[x][1])) for x in "kv"]
+    q = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
+    r = dg.fp8_paged_attention(q, caches[0], caches[1], cuda(p["table"]), cuda(p["lens"]), cu_seqlens_q=cuda(p["cu"]),
+                               max_seqlen_q=max(p["news"]), sm_scale=scale, window=window, sinks=sinks, return_lse=lse, **kw)
+    torch.cuda.synchronize()
+    return r
+
+
+def check(p, got, window=0, sinks=0, scale=None):
+    o = oracle.paged_attention(p["q"], p["k"], p["v"], p["table"], p["lens"], p["cu"],
+                               scale if scale is not None else p["dim"] ** -0.5, window, sinks)
+    tol, tol_lse = kv_gen.bounds(o, p["dim"])
+    out, lse = got[0].double().cpu().numpy(), got[1].double().cpu().numpy()
+    err = np.abs(out - o["out"])
+    say("largest error / bound", float((err / tol).max()) if err.size else 0.0)
+    assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(~(err <= tol))[:5])
+    blind = np.isneginf(o["lse"])
+    assert same(np.isneginf(lse), blind) and (out[blind] == 0).all()
+    with np.errstate(invalid="ignore"):
+        assert (np.abs(lse - o["lse"])[~blind] <= tol_lse[~blind]).all()
+
+
+# lengths (tokens in the cache) and new tokens; heads, key heads, head dim, page size
+CASES = {
+    "one_token": ([1], [1], 4, 1, 128, 16),
+    "single_tokens": ([0, 1, 31, 32, 33, 64, 65, 127, 300], [1] * 9, 16, 2, 128, 16),
+    "single_tokens_64": ([5, 0, 700], [1] * 3, 5, 5, 64, 1),
+    "single_tokens_256": ([130, 63, 1], [1] * 3, 8, 2, 256, 32),
+    "groups_of_seven": ([100, 37, 64], [3, 5, 4], 14, 2, 64, 16),
+    "forty_heads_one_key_head": ([90, 17], [1, 2], 40, 1, 128, 100),
+    "more_new_than_held": ([3, 0, 40], [5, 2, 41], 4, 2, 128, 16),
+    "chunks": ([200, 129, 64, 1], [130, 129, 1, 1], 4, 2, 128, 48),
+    "chunks_64": ([300, 100, 65], [64, 100, 33], 12, 4, 64, 7),
+    "chunks_256": ([190, 70], [140, 70], 2, 1, 256, 64),
+    "long": ([1500, 1027], [70, 2], 8, 2, 128, 64),
+}
+
+
+@pytest.mark.parametrize("mask", [(0, 0), (1, 0), (40, 0), (70, 4), (33, 100), (5, 1)])
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_attention(name, mask):
+    lens, news, *shape = CASES[name]
+    p = kv_gen.problem(lens, news, *shape, seed=len(name))
+    say("attention", name, mask)
+    check(p, run(p, *mask), *mask)
+
+
+@pytest.mark.parametrize("mask", [(0, 0), (300, 5)])
+@pytest.mark.parametrize("name", ["chunks", "long", "single_tokens", "more_new_than_held", "single_tokens_256"])
+def test_attention_in_parts(name, mask):
+    """As many parts of the keys as the planner ever makes, some of them without a key for a row."""
+    lens, news, *shape = CASES[name]
+    p = kv_gen.problem(lens, news, *shape, seed=3)
+    say("attention in parts", name, mask)
+    with num_sms(1 << 14):
+        # (a host bound far above the lengths asks for parts that have no tile)
+        got = run(p, *mask, max_seqlen_k=1 << 16)
+    check(p, got, *mask)
+
+
+def test_attention_scale_and_large_scores():
+    """Scores of hundreds: the running maximum moves far, weights underflow."""
+    p = kv_gen.problem([200, 77], [70, 1], 4, 2, 128, 16, seed=9)
+    say("attention, large scores")
+    for scale in (1e-3, 3.0):
+        check(p, run(p, scale=scale), scale=scale)
+
+
+def test_attention_strides_and_rows_of_no_sequence():
+    """q and out as slices, cache with tokens outermost in a page; rows outside the sequences stay as they were."""
+    p = kv_gen.problem([70, 33], [40, 1], 6, 3, 64, 16, seed=4)
+    caches = [(cuda(p[x][0].swapaxes(1, 2)).transpose(1, 2), cuda(p[x][1].swapaxes(1, 2)).transpose(1, 2)) for x in "kv"]
+    big = torch.full((45, 12, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    big[2:43, 3:9] = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
+    table = torch.full((2, p["table"].shape[1] + 3), -7, dtype=torch.int32, device=DEV)
+    table[:, :-3] = cuda(p["table"])
+    for sms in (0, 4096):
+        out = torch.full((45, 9, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        say("attention, strided", sms)
+        with num_sms(sms):
+            got, lse = dg.fp8_paged_attention(big[:, 3:9], *caches, table[:, :-3], cuda(p["lens"]), cu_seqlens_q=cuda(p["cu"] + 2),
+                                              max_seqlen_q=40, max_seqlen_k=1 << 16 if sms else 70, out=out[:, 1:7], return_lse=True)
+        torch.cuda.synchronize()
+        check(p, (got[2:43], lse[2:43]))
+        keep = torch.ones(45, 9, dtype=torch.bool, device=DEV)
+        keep[2:43, 1:7] = False
+        assert (out[keep] == 7.0).all()
+
+
+def test_attention_equal_lengths_without_cu():
+    p = kv_gen.problem([50, 51, 100], [2, 2, 2], 8, 2, 128, 16, seed=5)
+    a = run(p)
+    caches = [(cuda(p[x][0]), cuda(p[x][1])) for x in "kv"]
+    q = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
+    b = dg.fp8_paged_attention(q, *caches, cuda(p["table"]), cuda(p["lens"]), return_lse=True)
+    torch.cuda.synchronize()
+    check(p, b)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_attention_is_deterministic_on_another_stream_and_in_a_graph():
+    p = kv_gen.problem([900, 33, 0, 500], [1, 1, 1, 1], 8, 2, 128, 16, seed=6)
+    caches = [(cuda(p[x][0]), cuda(p[x][1])) for x in "kv"]
+    q = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
+    table, lens = cuda(p["table"]), cuda(p["lens"])
+    out = torch.empty_like(q)
+
+    def call():
+        return dg.fp8_paged_attention(q, *caches, table, lens, max_seqlen_k=900, out=out)
+
+    say("attention, stream and graph")
+    first = call().clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out.zero_()
+        again = call().clone()
+    torch.cuda.synchronize()
+    assert torch.equal(first, again)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for step in range(3):  # (lengths change between replays, as in a decode loop)
+        lens.copy_(cuda(np.maximum(p["lens"] - step, 0)))
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        out.fill_(4.0)
+        assert torch.equal(call(), got), step
+        torch.cuda.synchronize()
+
+
+def test_cache_past_4_gib():
+    """Pages whose byte offsets pass 32 bits: written, attended, read back."""
+    heads, page, dim, pages = 2, 16, 128, 9
+    stride = (1 << 29) + 16  # 8 * stride > 2^32
+    buf = torch.empty((8 * stride + 2 * heads * page * dim,), dtype=torch.uint8, device=DEV)
+    shape, st = (pages, heads, page, dim), (stride, page * dim, dim, 1)
+    say("cache past 4 GiB")
+    k_codes, v_codes = buf.as_strided(shape, st), buf[heads * page * dim:].as_strided(shape, st)
+    sf = torch.full((2, pages, heads, page), 127, dtype=torch.uint8, device=DEV)
+    rng = np.random.default_rng(1)
+    n = 50
+    x = [kv_gen.rows(rng, n, heads, dim) for _ in range(2)]
+    table = np.array([[8, 0, 7, 5]], np.int32)
+    slots = table[0][np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+    caches = (k_codes, sf[0]), (v_codes, sf[1])
+    dg.fp8_kv_cache_write(cuda(x[0]), cuda(x[1]), *caches, cuda(slots))
+    back = dg.fp8_kv_cache_read(*caches, cuda(slots), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert same(back[i].double().cpu().numpy(), oracle.kv_decode(*oracle.kv_encode(x[i])))
+    p = {"dim": dim, "page": page, "table": table, "lens": np.array([n], np.int32)}
+    host = [(np.zeros(shape, np.uint8), np.full(shape[:3], 127, np.uint8)) for _ in range(2)]
+    p["k"], p["v"] = (oracle.kv_write(host[i], x[i], slots) for i in range(2))
+    for new in (1, 50):
+        q = rng.standard_normal((new, 4, dim))
+        p["q_bits"] = oracle.bf16_rne(q)
+        p["q"], p["cu"], p["news"] = oracle.bf16_bits_to_f64(p["q_bits"]), np.array([0, new], np.int32), [new]
+        got = dg.fp8_paged_attention(cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16), *caches, cuda(table), cuda(p["lens"]),
+                                     return_lse=True)
+        torch.cuda.synchronize()
+        check(p, got)
+
+
+def test_write_then_attend_matches_unquantised_attention():
+    """End to end through the library's own cache: within E4M3's step of attention over the keys and values themselves."""
+    rng = np.random.default_rng(8)
+    n, heads, dim, page = 90, 2, 128, 16
+    x = [rng.standard_normal((n, heads, dim)).astype(np.float32) for _ in range(2)]
+    k_cache, v_cache = dg.fp8_kv_cache_empty(8, heads, page, dim, device=DEV)
+    table = torch.tensor([[7, 2, 5, 0, 1, 3]], dtype=torch.int32, device=DEV)
+    i = torch.arange(n, device=DEV)
+    slots = table[0, i // page].long() * page + i % page
+    dg.fp8_kv_cache_write(cuda(x[0]), cuda(x[1]), k_cache, v_cache, slots)
+    q = torch.randn((3, 4, dim), device=DEV, generator=torch.Generator(DEV).manual_seed(1)).bfloat16()
+    out = dg.fp8_paged_attention(q, k_cache, v_cache, table, torch.tensor([n], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    k, v = (torch.from_numpy(a).double().repeat_interleave(2, 1) for a in x)
+    s = torch.einsum("qhd,khd->hqk", q.double().cpu(), k) / dim ** 0.5
+    s = s.masked_fill(torch.arange(n)[None, None] > torch.arange(n - 3, n)[None, :, None], float("-inf"))
+    want = torch.einsum("hqk,khd->qhd", s.softmax(-1), v)
+    rel = float((out.double().cpu() - want).norm() / want.norm())
+    # E4M3 rounds values by up to 2^-4; errors of different keys average out
+    assert rel < 2.0 ** -4, rel
