@@ -32,6 +32,10 @@ int check_cache(const dg_fp8_kv_cache* c, bool empty) {
     return api_fail(DG_ERR_LAYOUT, "the cache's strides must not be negative, and token_stride at least head_dim");
   if (c->sf_page_stride < 0 || c->sf_head_stride < 0 || c->sf_token_stride < 0)
     return api_fail(DG_ERR_LAYOUT, "the cache's scale strides must not be negative");
+  // (an offset within a head's page, and within 16 rows, is a 32-bit number)
+  if (c->token_stride >= (1 << 24) || c->sf_token_stride >= (1 << 24) || c->token_stride * c->page_size >= (int64_t(1) << 31) ||
+      c->sf_token_stride * c->page_size >= (int64_t(1) << 31))
+    return api_fail(DG_ERR_LAYOUT, "the cache's token strides must be less than 2^24 bytes, and page_size times them less than 2^31");
   return DG_OK;
 }
 
@@ -97,10 +101,10 @@ struct AttnPlan {
 };
 
 // keys: the most keys that a row can see (from the host's bounds).
-AttnPlan plan_attention(int64_t batch, int kv_heads, int64_t rows, int64_t keys, int num_sms) {
+AttnPlan plan_attention(int64_t batch, int kv_heads, int64_t rows, int64_t keys, int head_dim, int num_sms) {
   AttnPlan pl;
   pl.wide = rows > 2 * dg::kAttnNarrowRows;
-  const int tile = pl.wide ? dg::kAttnWideRows : dg::kAttnNarrowRows;
+  const int tile = pl.wide ? dg::attn_wide_rows(head_dim) : dg::kAttnNarrowRows;
   pl.q_tiles = int((rows + tile - 1) / tile);
   const int64_t blocks = batch * kv_heads * pl.q_tiles;
   const int64_t want = (2 * int64_t(num_sms) + blocks - 1) / blocks;
@@ -127,11 +131,11 @@ int check_shape(const AttnShape& a, int32_t num_kv_heads) {
   return DG_OK;
 }
 
-AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int num_sms) {
+AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int num_sms) {
   const int64_t per_seq = a.equal ? a.total_q / a.batch : a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
   int64_t keys = a.max_seqlen_k;
   if (a.window && a.window < keys - a.sinks) keys = int64_t(a.window) + a.sinks;
-  return plan_attention(a.batch, num_kv_heads, per_seq * (a.num_q_heads / num_kv_heads), keys, num_sms);
+  return plan_attention(a.batch, num_kv_heads, per_seq * (a.num_q_heads / num_kv_heads), keys, head_dim, num_sms);
 }
 
 int64_t workspace_of(const AttnShape& a, const AttnPlan& pl, int32_t head_dim) {
@@ -164,7 +168,7 @@ int64_t dg_fp8_paged_attention_workspace(int32_t batch, int32_t total_q, int32_t
   if (batch == 0 || total_q == 0 || (!a.equal && max_seqlen_q == 0)) return 0;
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
-  return workspace_of(a, plan_of(a, num_kv_heads, num_sms), head_dim);
+  return workspace_of(a, plan_of(a, num_kv_heads, head_dim, num_sms), head_dim);
 }
 
 int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t total_q, int32_t num_q_heads,
@@ -190,7 +194,7 @@ int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t 
     return api_fail(DG_ERR_LAYOUT, "block_table, seq_lens, cu_seqlens_q and lse must be 4-byte aligned");
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
-  const AttnPlan pl = plan_of(a, cache->num_heads, num_sms);
+  const AttnPlan pl = plan_of(a, cache->num_heads, cache->head_dim, num_sms);
   const int64_t need = workspace_of(a, pl, cache->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);

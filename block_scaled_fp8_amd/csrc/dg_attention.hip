@@ -35,6 +35,11 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 constexpr float NEG_INF = -__builtin_inff();
 constexpr int ROWS = 32;  // query rows of one wave: the columns of its matrix instructions
 // The running maximum is raised only when a score passes it by this much (log2 units): until then
@@ -69,14 +74,15 @@ __device__ __forceinline__ v4u widen8(unsigned lo, unsigned hi, float s) {
 
 // LDS tiles hold BF16 rows of D values (2 D bytes) in 16-byte chunks, permuted within a row so
 // that the reads below hit all banks.  K: 16 lanes read one chunk of 16 consecutive rows.  V: 16
-// lanes read 4 rows x 32 bytes, and the next 16 lanes the 32 bytes beside them.
+// lanes read 4 rows x 32 bytes, and the next 16 lanes the 32 bytes beside them; the lowest bit
+// keeps neighbouring rows' writes apart (a lane writes its two chunks of a row one after the other).
 template <int D>
 __device__ __forceinline__ int k_chunk(int row, int c) {
   return c ^ (D == 64 ? (row >> 1) & 7 : row & 15);
 }
 template <int D>
 __device__ __forceinline__ int v_chunk(int row, int c) {
-  return c ^ (D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2);
+  return c ^ (D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2) ^ (row & 1);
 }
 
 // What a workgroup works on: a tile of query rows of one (sequence, key head), and a part of the
@@ -97,16 +103,17 @@ struct Work {
 // KEYS: keys of a tile.  Returns false if there is no row.
 template <int KEYS>
 __device__ __forceinline__ bool get_work(const AttnParams& p, int tile_rows, Work& w) {
-  // Workgroups are dealt to the eight XCDs in turn; renumber them so that each XCD takes a
-  // contiguous run, and with it all parts of the same keys: they share its L2.
-  const unsigned nb = gridDim.x, per = nb >> 3, extra = nb & 7, xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  unsigned id = xcd < extra ? xcd * (per + 1) + idx : extra * (per + 1) + (xcd - extra) * per + idx;
+  // Workgroups are dealt to the eight XCDs in turn.  With the (sequence, key head) pair as the
+  // fastest index, and a multiple of eight pairs, all workgroups of a pair land on one XCD and share
+  // its L2, and the pairs of one sequence, as long as each other, spread over the XCDs.  Later rows
+  // see more keys: they start first.
+  const unsigned pairs = p.batch * p.c.num_heads;
+  const unsigned pair = blockIdx.x % pairs;
+  unsigned id = blockIdx.x / pairs;
   w.split = id % p.splits;
-  id /= p.splits;
-  const int qt = p.q_tiles - 1 - (int)(id % p.q_tiles);  // (later rows see more keys: they start first)
-  id /= p.q_tiles;
-  w.kv_head = id % p.c.num_heads;
-  w.seq = id / p.c.num_heads;
+  const int qt = p.q_tiles - 1 - (int)(id / p.splits);
+  w.kv_head = pair % p.c.num_heads;
+  w.seq = pair / p.c.num_heads;
   int n;
   if (p.cu_q) {
     const int a = min(max(p.cu_q[w.seq], 0), p.total_q), b = min(max(p.cu_q[w.seq + 1], a), p.total_q);
@@ -180,23 +187,44 @@ __device__ __forceinline__ void init(State<D>& st) {
   st.z = 0.f;
 }
 
-// Scores of NB blocks of 32 keys -> weights (as B operands of the second product), updating the
-// running maximum, sum and, where the maximum rises, the outputs.  key0: first key.
-// A lane's register i of a block is key 8 (i / 4) + 4 (lane / 32) + i % 4.
-template <int D, int NB, bool MASK>
-__device__ __forceinline__ void softmax(const AttnParams& p, State<D>& st, v16f (&s)[NB], v8bf (&w)[NB][2], int key0, int place,
-                                        int h) {
-  if constexpr (MASK) {
-    const int from = p.window ? place - p.window : INT32_MIN;
+// Scores of keys that the lane's query does not see become -infinity.  key0: first key; a lane's
+// register i of a block is key key0 + 4 (lane / 32) + c with c = 32 block + 8 (i / 4) + i % 4, so
+// each bound is a number of the lane against constants.  late, early (uniform): whether some row of the
+// wave may lack the tile's last keys, or its first ones (by its window).
+template <int NB>
+__device__ __forceinline__ void mask(const AttnParams& p, v16f (&s)[NB], int key0, int place, int h, bool late, bool early) {
+  const int first = key0 + 4 * h;
+  if (late) {
+    const int end = place - first;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = key0 + 32 * b + 8 * (i / 4) + 4 * h + i % 4;
-        const bool seen = j <= place && (j > from || j < p.sinks);
-        s[b][i] = seen ? s[b][i] : NEG_INF;
-      }
+      for (int i = 0; i < 16; ++i) s[b][i] = 32 * b + 8 * (i / 4) + i % 4 <= end ? s[b][i] : NEG_INF;
   }
+  if (early) {
+    const int from = place - p.window - first;
+    if (key0 >= p.sinks) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = 32 * b + 8 * (i / 4) + i % 4 > from ? s[b][i] : NEG_INF;
+    } else {
+      const int sinks = p.sinks - first;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int c = 32 * b + 8 * (i / 4) + i % 4;
+          s[b][i] = c > from || c < sinks ? s[b][i] : NEG_INF;
+        }
+    }
+  }
+}
+
+// Scores of NB blocks of 32 keys -> weights (as B operands of the second product), updating the
+// running maximum, sum and, where the maximum rises, the outputs.
+template <int D, int NB>
+__device__ __forceinline__ void softmax(const AttnParams& p, State<D>& st, v16f (&s)[NB], v8bf (&w)[NB][2]) {
   float top = s[0][0];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -289,21 +317,54 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, co
 }
 
 // ---------------------------------------------------------------- many rows: chunks of a prompt
-// Four waves of 32 query rows share tiles of 64 keys.  A tile's codes are loaded into registers
-// while the one before is computed, widened once, and written to the other of two LDS buffers.
+// NW waves of 32 query rows share tiles of KEYS keys.  What bounds it: a wave's tile of 64 keys takes 32
+// matrix instructions of 32 cycles at D = 128 (1024 cycles; half of that at D = 64) and about as long on
+// the vector unit, where 32 exponentials at a quarter of the rate are half of it.  Both units have to be
+// kept busy by different waves.
+//
+// D = 128: eight waves, two on each SIMD, and the two halves of the workgroup take turns: while waves
+// 0-3 are in the matrix phase of a tile (O^T += V^T P^T of the tile before, S^T of this one), waves 4-7
+// are in the vector phase (the softmax) of theirs, half a tile behind, with a barrier after each phase.
+// Measured on 2048 queries (32 heads, 8 key heads) over 8192 keys: 236 us; 269 us without turns; 300 us
+// with turns but LDS reads one matrix instruction ahead instead of four.  D = 64 is bound by the vector
+// unit, which a single half cannot fill: four waves without turns and three such workgroups a CU
+// (61 us on 2 x 2048 queries in a window of 1024; with turns 74, eight waves without 70).  D = 256
+// fills the registers with one wave a SIMD.
+//
+// Tiles lie widened in LDS.  With turns, in rings of three: stage i brings K of tile i + 2 and V of tile
+// i + 1; a wave issues its loads at the end of its matrix phase of tile i, when its LDS reads are out
+// (255 us when issued before them), and widens and stores them at the end of the vector phase, to slots
+// last read in the matrix phases of tile i - 1.  Without turns, two slots, loads a whole tile ahead.
+// A load unit is GR rows of K or of V (one 16-byte load a lane), dealt to the waves; where GR divides
+// the page size and every row of a unit is seen, its address is scalar arithmetic on a page number out
+// of 64 that the lanes hold, else it is found lane by lane.
 template <int D>
-__global__ void __launch_bounds__(256) wide_kernel(const AttnParams p) {
-  constexpr int KEYS = D == 256 ? 32 : 64, NB = KEYS / 32, TILE = KEYS * D * 2;  // bytes of a widened tile
-  constexpr int CH = D / 16, PASS = 256 / CH, NP = KEYS / PASS;  // 16-code chunks; rows and number of load passes
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
+struct Wide {
+  static constexpr int NW = D == 128 ? 8 : 4, KEYS = D == 256 ? 32 : 64, NB = KEYS / 32;
+  static constexpr bool TURNS = D == 128;
+  static constexpr int ROWS_ALL = NW * ROWS, THREADS = NW * 64, TILE = KEYS * D * 2;  // TILE: bytes of a widened K or V tile
+};
+
+// The end of a phase; no instruction is moved from one phase to another.
+__device__ __forceinline__ void phase_end() {
+  __builtin_amdgcn_sched_barrier(0);
+  __syncthreads();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) wide_kernel(const AttnParams p) {
+  constexpr int NW = Wide<D>::NW, KEYS = Wide<D>::KEYS, NB = Wide<D>::NB, TILE = Wide<D>::TILE;
+  constexpr int CH = D / 16, GR = 64 / CH, GROUPS = KEYS / GR, NU = 2 * GROUPS / NW;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][Wide<D>::TURNS ? 3 : 2][TILE];  // [K, V][slot]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   Work w;
-  if (!get_work<KEYS>(p, kAttnWideRows, w)) return;
+  if (!get_work<KEYS>(p, Wide<D>::ROWS_ALL, w)) return;
   const Row row = get_row(p, w, w.row0 + wave * ROWS + (lane & 31));
   // the places of this wave's rows, for whole-tile decisions
   const int wr0 = w.row0 + wave * ROWS;
   const int place_lo = w.place0 + div(min(wr0, w.rows - 1), p.group);
-  const int place_hi = wr0 < w.rows ? w.place0 + div(min(wr0 + ROWS, w.rows) - 1, p.group) : INT32_MIN / 2;
+  const int place_hi = w.place0 + div(min(wr0 + ROWS, w.rows) - 1, p.group);
 
   v8bf q[D / 16];
   {
@@ -312,75 +373,191 @@ __global__ void __launch_bounds__(256) wide_kernel(const AttnParams p) {
     for (int i = 0; i < D / 16; ++i) q[i] = *(const v8bf*)(src + 16 * i);
   }
   const int32_t* table = p.table + w.seq * p.table_stride;
-  const int c = threadIdx.x % CH, r0 = threadIdx.x / CH;
-  v4u kr[NP], vr[NP];
-  uint32_t ks[NP], vs[NP];
-  auto fetch = [&](int i) {
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int j = key_to_load(w, p.sinks, w.tile_key(i, KEYS) + r0 + n * PASS);
+  const bool page_whole = p.c.page.d % GR == 0;
+  const int c = lane % CH, r = lane / CH;
+  const int64_t head_at = w.kv_head * p.c.head_stride, head_sf = w.kv_head * p.c.sf_head_stride;
+  const uint32_t lane_at = (uint32_t)(r * p.c.token_stride) + 16 * c, lane_sf = (uint32_t)(r * p.c.sf_token_stride);
+  // Where a lane finds its part of GR rows from key j0 on: byte offsets into codes and scales.
+  struct At {
+    int64_t code, sf;
+  };
+  // 64 entries of the block table, one a lane, from column table_from
+  int table_from = INT32_MIN / 2, entries = 0;
+  auto place_rows = [&](int j0) {
+    At a;
+    const int j1 = j0 + GR - 1;
+    if (page_whole && j1 < w.key_end && (j0 >= w.key_from || j1 < p.sinks)) {
+      const int col = div(j0, p.c.page);
+      if ((unsigned)(col - table_from) >= 64u) {
+        table_from = col;
+        entries = table[min(col + lane, p.table_cols - 1)];
+        entries = (unsigned)entries < (unsigned)p.c.num_pages ? entries : 0;
+      }
+      const uint32_t pg = __builtin_amdgcn_readlane(entries, col - table_from), off = j0 - col * p.c.page.d;
+      a.code = (int64_t)(pg * (uint64_t)p.c.page_stride + head_at + off * (uint32_t)p.c.token_stride) + lane_at;
+      a.sf = (int64_t)(pg * (uint64_t)p.c.sf_page_stride + head_sf + off * (uint32_t)p.c.sf_token_stride) + lane_sf;
+    } else {
+      const int j = key_to_load(w, p.sinks, j0 + r);
       const int col = div(j, p.c.page), off = j - col * p.c.page.d, pg = page_entry(p, table, col);
-      const int64_t at = pg * p.c.page_stride + w.kv_head * p.c.head_stride + off * p.c.token_stride + 16 * c;
-      const int64_t sf = pg * p.c.sf_page_stride + w.kv_head * p.c.sf_head_stride + off * p.c.sf_token_stride;
-      kr[n] = *(const v4u*)(p.c.k + at);
-      vr[n] = *(const v4u*)(p.c.v + at);
-      ks[n] = p.c.k_sf[sf];
-      vs[n] = p.c.v_sf[sf];
+      a.code = pg * p.c.page_stride + head_at + off * p.c.token_stride + 16 * c;
+      a.sf = pg * p.c.sf_page_stride + head_sf + off * p.c.sf_token_stride;
+    }
+    return a;
+  };
+  // With turns, a wave's V rows of a stage are its K rows of the stage before (except where it loads
+  // only one of the two); without, they are of the same tile.
+  constexpr bool TURNS = Wide<D>::TURNS;
+  constexpr int NK = NU > 1 ? NU / 2 : 1;
+  const bool only_v = NU == 1 && wave >= GROUPS;
+  At at[NK];
+  v4u raw[NU];      // a stage's codes
+  uint32_t sf[NU];  // and their rows' scale codes
+  auto fetch = [&](int i) {
+    // (tiles past the list repeat its ends and are not read)
+    const int key0 = w.tile_key(min(max(TURNS && only_v ? i + 1 : i + 2, w.t0), w.t1 - 1), KEYS);
+    auto get_v = [&](int n) {
+      raw[NU - NK + n] = *(const v4u*)(p.c.v + at[n].code);
+      sf[NU - NK + n] = p.c.v_sf[at[n].sf];
+    };
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      if (NU > 1 && TURNS) get_v(n);
+      at[n] = place_rows(key0 + (wave + n * NW) % GROUPS * GR);
+      if (NU > 1 && !TURNS) get_v(n);
+      raw[n] = *(const v4u*)((only_v ? p.c.v : p.c.k) + at[n].code);
+      sf[n] = (only_v ? p.c.v_sf : p.c.k_sf)[at[n].sf];
     }
   };
-  auto put = [&](int buf) {
+  auto put = [&](uint8_t* k, uint8_t* v) {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int r = r0 + n * PASS;
-      const float a = __uint_as_float(ks[n] << 23), b = __uint_as_float(vs[n] << 23);
-      uint8_t* k = lds[buf][0] + r * 2 * D;
-      uint8_t* v = lds[buf][1] + r * 2 * D;
-      *(v4u*)(k + k_chunk<D>(r, 2 * c) * 16) = widen8(kr[n].x, kr[n].y, a);
-      *(v4u*)(k + k_chunk<D>(r, 2 * c + 1) * 16) = widen8(kr[n].z, kr[n].w, a);
-      *(v4u*)(v + v_chunk<D>(r, 2 * c) * 16) = widen8(vr[n].x, vr[n].y, b);
-      *(v4u*)(v + v_chunk<D>(r, 2 * c + 1) * 16) = widen8(vr[n].z, vr[n].w, b);
+    for (int n = 0; n < NU; ++n) {
+      const bool is_v = NU > 1 ? n >= NK : only_v;
+      const int rr = (wave + n * NW) % GROUPS * GR + r;
+      uint8_t* dst = (is_v ? v : k) + rr * 2 * D;
+      const int c0 = is_v ? v_chunk<D>(rr, 2 * c) : k_chunk<D>(rr, 2 * c), c1 = is_v ? v_chunk<D>(rr, 2 * c + 1) : k_chunk<D>(rr, 2 * c + 1);
+      const float s = __uint_as_float(sf[n] << 23);
+      *(v4u*)(dst + c0 * 16) = widen8(raw[n].x, raw[n].y, s);
+      *(v4u*)(dst + c1 * 16) = widen8(raw[n].z, raw[n].w, s);
     }
   };
 
   State<D> st;
   init(st);
-  if (w.t0 < w.t1) {
-    fetch(w.t0);
-    put(0);
-    if (w.t0 + 1 < w.t1) fetch(w.t0 + 1);
-  }
-  __syncthreads();
-  for (int i = w.t0; i < w.t1; ++i) {
-    const int buf = (i - w.t0) & 1, key0 = w.tile_key(i, KEYS);
-    // a tile that none of the wave's rows sees is left out (tiles above the diagonal, and tiles
-    // between the first keys and the window)
-    const bool none = key0 > place_hi || (p.window && key0 + KEYS - 1 <= place_lo - p.window && key0 >= p.sinks);
-    if (!none) {
-      v16f s[NB];
+  v8bf wt[NB][2];  // (zero weights go with the first matrix phase, which has no tile before it)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
+  for (int b = 0; b < NB; ++b) wt[b][0] = wt[b][1] = __builtin_bit_cast(v8bf, (v4u){0, 0, 0, 0});
+  auto scores = [&](v16f (&s)[NB], const uint8_t* k) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) s[b][x] = 0.f;
-        const int r = 32 * b + (lane & 31);
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const v8bf a = *(const v8bf*)(lds[buf][0] + r * 2 * D + k_chunk<D>(r, 2 * x + h) * 16);
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[x], s[b], 0, 0, 0);
-        }
+      for (int x = 0; x < 16; ++x) s[b][x] = 0.f;
+      const int kr = 32 * b + (lane & 31);
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const v8bf a = *(const v8bf*)(k + kr * 2 * D + k_chunk<D>(kr, 2 * x + h) * 16);
+        s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[x], s[b], 0, 0, 0);
       }
-      v8bf wt[NB][2];
-      const bool all = key0 + KEYS - 1 <= place_lo && (!p.window || key0 > place_hi - p.window || key0 + KEYS <= p.sinks);
-      if (all)
-        softmax<D, NB, false>(p, st, s, wt, key0, row.place, h);
-      else
-        softmax<D, NB, true>(p, st, s, wt, key0, row.place, h);
-      product_v<D, NB>(st, wt, lds[buf][1], lane);
     }
-    if (i + 1 < w.t1) {
-      put(buf ^ 1);
-      if (i + 2 < w.t1) fetch(i + 2);
+  };
+  auto weights = [&](int i, v16f (&s)[NB]) {
+    const int key0 = w.tile_key(i, KEYS);
+    const bool late = key0 + KEYS - 1 > place_lo, early = p.window && key0 <= place_hi - p.window && key0 + KEYS > p.sinks;
+    if (late || early) mask<NB>(p, s, key0, row.place, h, late, early);
+    softmax<D, NB>(p, st, s, wt);
+  };
+  // With turns: tile i of the list, number X of three: its K is in slot X, V of the tile before in slot X - 1.
+  auto step = [&](int i, auto number) {
+    constexpr int X = decltype(number)::value, NEXT = (X + 1) % 3, LAST = (X + 2) % 3;
+    product_v<D, NB>(st, wt, lds[1][LAST], lane);
+    v16f s[NB];
+    scores(s, lds[0][X]);
+    // Four fragments are read ahead of the matrix instruction that takes them.
+    constexpr int NVF = D / 32 * NB * 2, NKF = D / 16 * NB, AHEAD = 4;  // V and K fragments (and matrix instructions)
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
+#pragma unroll
+    for (int x = 0; x < NVF - AHEAD; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
+#pragma unroll
+    for (int x = 0; x < NKF; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(i);
+    phase_end();
+    weights(i, s);
+    // (the weights are wanted here: left to itself, the compiler computes some in the next phase)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) asm volatile("" : "+v"(wt[b][0]), "+v"(wt[b][1]));
+    asm volatile("" : "+v"(st.z));
+    __builtin_amdgcn_sched_barrier(0);
+    put(lds[0][LAST], lds[1][NEXT]);
+    phase_end();
+  };
+  // Without turns: tile i with K and V in slot X; leaves tile i + 1 in the other slot and tile i + 2 on its way.
+  auto plain_step = [&](int i, auto slot) {
+    constexpr int X = decltype(slot)::value, AHEAD = 3;
+    v16f s[NB];
+    scores(s, lds[0][X]);
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int x = 0; x < D / 16 * NB - AHEAD; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    weights(i, s);
+    __builtin_amdgcn_sched_barrier(0);
+    product_v<D, NB>(st, wt, lds[1][X], lane);
+    put(lds[0][1 - X], lds[1][1 - X]);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 1);
+#pragma unroll
+    for (int x = 0; x < D / 16 * NB - AHEAD; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(i);
     __syncthreads();
+  };
+  if (w.t0 < w.t1) {
+#pragma unroll
+    for (int n = 0; n < NK; ++n) at[n] = place_rows(w.tile_key(w.t0, KEYS) + (wave + n * NW) % GROUPS * GR);
+    fetch(w.t0 - 2);
+    if constexpr (TURNS) {
+      put(lds[0][0], lds[1][2]);
+      fetch(w.t0 - 1);
+      put(lds[0][1], lds[1][0]);
+      __syncthreads();
+      if (wave >= 4) __syncthreads();
+      int last = 0;  // slot of the last tile
+      for (int i = w.t0;; i += 3) {
+        step(i, Int<0>{});
+        last = 0;
+        if (i + 1 == w.t1) break;
+        step(i + 1, Int<1>{});
+        last = 1;
+        if (i + 2 == w.t1) break;
+        step(i + 2, Int<2>{});
+        last = 2;
+        if (i + 3 == w.t1) break;
+      }
+      product_v<D, NB>(st, wt, lds[1][last], lane);
+      if (wave < 4) __syncthreads();
+    } else {
+      put(lds[0][0], lds[1][0]);
+      fetch(w.t0 - 1);
+      __syncthreads();
+      for (int i = w.t0; i < w.t1; i += 2) {
+        plain_step(i, Int<0>{});
+        if (i + 1 < w.t1) plain_step(i + 1, Int<1>{});
+      }
+    }
   }
   store_row<D>(p, w, row, st.o, st.m, both_sum(st.z), h);
 }
@@ -458,11 +635,9 @@ __global__ void __launch_bounds__(256) narrow_kernel(const AttnParams p) {
     }
     if (i + NW < w.t1) fetch(i + NW);
     v8bf wt[1][2];
-    const bool all = key0 + KEYS - 1 <= place_lo && (!p.window || key0 > place_hi - p.window || key0 + KEYS <= p.sinks);
-    if (all)
-      softmax<D, 1, false>(p, st, s, wt, key0, row.place, h);
-    else
-      softmax<D, 1, true>(p, st, s, wt, key0, row.place, h);
+    const bool late = key0 + KEYS - 1 > place_lo, early = p.window && key0 <= place_hi - p.window && key0 + KEYS > p.sinks;
+    if (late || early) mask<1>(p, s, key0, row.place, h, late, early);
+    softmax<D, 1>(p, st, s, wt);
     // the wave reads what its other lanes wrote: its LDS operations complete in order, so only the
     // compiler has to keep theirs
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -570,7 +745,7 @@ hipError_t launch(const AttnParams& p, bool wide, hipStream_t stream) {
   const int64_t grid = (int64_t)p.batch * p.c.num_heads * p.q_tiles * p.splits;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   if (wide)
-    hipLaunchKernelGGL((wide_kernel<D>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((wide_kernel<D>), dim3((unsigned)grid), dim3(Wide<D>::THREADS), 0, stream, p);
   else
     hipLaunchKernelGGL((narrow_kernel<D>), dim3((unsigned)grid), dim3(256), 0, stream, p);
   hipError_t e = hipGetLastError();

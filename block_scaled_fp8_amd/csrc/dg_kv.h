@@ -71,6 +71,7 @@ struct AttnParams {
 hipError_t launch_attention(const AttnParams& p, int head_dim, bool wide, hipStream_t stream);
 
 // Query rows (token, head of the group) of one workgroup's tile.
-constexpr int kAttnWideRows = 128, kAttnNarrowRows = 32;
+inline int attn_wide_rows(int head_dim) { return head_dim == 128 ? 256 : 128; }
+constexpr int kAttnNarrowRows = 32;
 
 }  // namespace dg

@@ -364,8 +364,8 @@ int dg_transform_sf(const float* sf_in, int32_t num_groups, int32_t mn, int32_t 
  *
  *  k, v             : E4M3 codes [num_pages, num_heads, page_size, head_dim]; element d of a row at
  *                     k[page*page_stride + head*head_stride + place*token_stride + d].  Strides in
- *                     bytes, the same for k and v, multiples of 16; k and v 16-byte aligned.  Any order
- *                     of pages, heads and tokens is allowed; the rows must not overlap.
+ *                     bytes, the same for k and v, multiples of 16; k and v 16-byte aligned; token
+ *                     strides (scales' too) below 2^24.  Any order of pages, heads and tokens is allowed; the rows must not overlap.
  *  k_sf, v_sf       : UE8M0 codes [num_pages, num_heads, page_size] (sf_*_stride in bytes).  Codes 1 to
  *                     254 are meant; 0 and 255 give unspecified values.
  *  head_dim         : 64, 128 or 256.  page_size: any positive number of tokens.

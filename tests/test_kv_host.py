@@ -30,6 +30,7 @@ CACHE_FAULTS = [
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(k_sf=None), NULL), (dict(v_sf=None), NULL),
     (dict(k=P_MIS), LAYOUT), (dict(v=P_MIS), LAYOUT), (dict(page_stride=8200), LAYOUT), (dict(head_stride=2056), LAYOUT),
     (dict(token_stride=136), LAYOUT), (dict(token_stride=64), LAYOUT), (dict(page_stride=-8192), LAYOUT), (dict(sf_head_stride=-1), LAYOUT),
+    (dict(token_stride=1 << 24), LAYOUT), (dict(sf_token_stride=1 << 24), LAYOUT),
 ]
 
 
