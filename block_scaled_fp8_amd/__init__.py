@@ -37,6 +37,17 @@ DG_SF_F32, DG_SF_UE8M0X4 = 0, 1
 DG_IN_BF16, DG_IN_F32 = 1, 2
 
 _i32, _i64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+
+
+class _KvCache(ctypes.Structure):
+    """dg_fp8_kv_cache (include/dg.h)."""
+    _fields_ = [("k", _p), ("v", _p), ("k_sf", _p), ("v_sf", _p),
+                ("num_pages", _i32), ("num_heads", _i32), ("page_size", _i32), ("head_dim", _i32),
+                ("page_stride", _i64), ("head_stride", _i64), ("token_stride", _i64),
+                ("sf_page_stride", _i64), ("sf_head_stride", _i64), ("sf_token_stride", _i64)]
+
+
+_c = ctypes.POINTER(_KvCache)
 _SIGS = {
     **{f"dg_fp8_gemm_{lay}": (_i32, [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _i32,
                                      _p, _i64, _p, _i64, _i32, _p]) for lay in ("nt", "nn", "tn", "tt")},
@@ -58,9 +69,9 @@ _SIGS = {
     "dg_k_grouped_fp8_gemm_nt_contiguous": (_i32, [_i32, _i32, _i32, _p, _p, _i64, _p, _p, _i64, _p, _p, _p, _p]),
     "dg_k_grouped_fp8_gemm_tn_contiguous": (_i32, [_i32, _i32, _i32, _p, _p, _i64, _p, _p, _i64, _p, _p, _p, _p]),
     "dg_per_token_group_cast_fp8": (_i32, [_i32, _i32, _p, _i64, _i32, _p, _i64, _p, _i64, _i32, _p]),
-    "dg_fp8_kv_cache_write": (_i32, [_p, _i32, _p, _i64, _i64, _p, _i64, _i64, _i32, _p, _p]),
-    "dg_fp8_kv_cache_read": (_i32, [_p, _i32, _p, _i64, _i64, _p, _i64, _i64, _i32, _p, _p]),
-    "dg_fp8_paged_attention": (_i32, [_p, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32,
+    "dg_fp8_kv_cache_write": (_i32, [_c, _i32, _p, _i64, _i64, _p, _i64, _i64, _i32, _p, _p]),
+    "dg_fp8_kv_cache_read": (_i32, [_c, _i32, _p, _i64, _i64, _p, _i64, _i64, _i32, _p, _p]),
+    "dg_fp8_paged_attention": (_i32, [_c, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32,
                                       ctypes.c_float, _i32, _i32, _p, _i64, _i64, _p, _p, _i64, _p]),
     "dg_fp8_paged_attention_workspace": (_i64, [_i32] * 10),
     "dg_get_tma_aligned_size": (_i64, [_i64, _i32]),
@@ -558,14 +569,6 @@ def m_grouped_fp8_fp4_gemm_nt_masked(a, b, d, masked_m, expected_m=0):
 
 
 # ---------------------------------------------------------------- FP8 key/value cache
-class _KvCache(ctypes.Structure):
-    """dg_fp8_kv_cache (include/dg.h)."""
-    _fields_ = [("k", _p), ("v", _p), ("k_sf", _p), ("v_sf", _p),
-                ("num_pages", _i32), ("num_heads", _i32), ("page_size", _i32), ("head_dim", _i32),
-                ("page_stride", _i64), ("head_stride", _i64), ("token_stride", _i64),
-                ("sf_page_stride", _i64), ("sf_head_stride", _i64), ("sf_token_stride", _i64)]
-
-
 _CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
 _SF_TYPES = (torch.uint8, torch.float8_e8m0fnu)
 
@@ -580,23 +583,30 @@ def fp8_kv_cache_empty(num_pages, num_kv_heads, page_size, head_dim, device="cud
 
 
 def _kv_cache(k_cache, v_cache):
-    """The C struct of a cache, and its shape."""
+    """The C struct of a cache, and its shape and device."""
     (kc, ks), (vc, vs) = k_cache, v_cache
+    shape, st, sf, dev = kc.shape, kc.stride(), ks.stride(), kc.device
     if kc.dtype not in _CODE_TYPES or vc.dtype not in _CODE_TYPES:
         raise TypeError(f"cache codes must be uint8 or float8_e4m3fn, got {kc.dtype} and {vc.dtype}")
     if ks.dtype not in _SF_TYPES or vs.dtype not in _SF_TYPES:
         raise TypeError(f"cache scales must be uint8 or float8_e8m0fnu, got {ks.dtype} and {vs.dtype}")
-    shape, st, sf = kc.shape, kc.stride(), ks.stride()
     if len(shape) != 4 or st[3] != 1 or vc.shape != shape or vc.stride() != st:
         raise ValueError("cache codes must be [pages, heads, page size, head dim], contiguous along the last "
                          "dimension, keys and values with the same shape and strides")
-    if ks.shape != shape[:3] or vs.shape != shape[:3] or vs.stride() != sf:
+    rows = shape[:3]
+    if ks.shape != rows or vs.shape != rows or vs.stride() != sf:
         raise ValueError("cache scales must be [pages, heads, page size], keys' and values' with the same strides")
-    dev = kc.device
-    if not kc.is_cuda or vc.device != dev or ks.device != dev or vs.device != dev:
+    if dev.type != "cuda" or vc.device != dev or ks.device != dev or vs.device != dev:
         raise ValueError("the cache must be on one GPU")
-    return _KvCache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2], shape[3],
-                    st[0], st[1], st[2], sf[0], sf[1], sf[2]), shape, dev
+    return _KvCache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), *shape, *st[:3], *sf), shape, dev
+
+
+# The current stream's handle without building a torch.cuda.Stream, which takes 2 us of a 5 us call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(dev):
+    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 _IN_TYPES = {torch.bfloat16: DG_IN_BF16, torch.float32: DG_IN_F32}
@@ -614,8 +624,8 @@ def _kv_move(fn, c, k, v, slots, shape, dev):
         raise ValueError("slots must be a contiguous int64 vector")
     if k.device != dev or v.device != dev or slots.device != dev:
         raise ValueError("k, v and slots must be on the cache's GPU")
-    _check(fn(ctypes.byref(c), n, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _IN_TYPES[k.dtype],
-              slots.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
+    _check(fn(c, n, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _IN_TYPES[k.dtype],
+              slots.data_ptr(), _current_stream(dev)))
 
 
 def fp8_kv_cache_write(k, v, k_cache, v_cache, slots):
@@ -655,39 +665,42 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
     ``sinks`` tokens.  Returns ``out`` BF16 [total tokens, query heads, head dim], with ``return_lse`` also the
     FP32 log sum of exponentials [total tokens, query heads]; a query that sees nothing gives zeros and -inf."""
     c, shape, dev = _kv_cache(k_cache, v_cache)
-    hk, d = shape[1], shape[3]
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d or q.stride(2) != 1:
+    _, hk, page, d = shape
+    qshape, qs = q.shape, q.stride()
+    if q.dtype != torch.bfloat16 or len(qshape) != 3 or qshape[2] != d or qs[2] != 1:
         raise ValueError(f"q must be bfloat16 [tokens, heads, {d}], contiguous along the last dimension")
-    total, hq = q.shape[0], q.shape[1]
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [batch, columns], contiguous along its columns")
+    total, hq, _ = qshape
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch, columns]")
     batch, cols = block_table.shape
-    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (batch,) or not seq_lens.is_contiguous():
+    ts = block_table.stride()
+    if cols > 1 and ts[1] != 1:
+        raise ValueError("block_table must be contiguous along its columns")
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_contiguous():
         raise ValueError(f"seq_lens must be contiguous int32 [{batch}]")
     if q.device != dev or block_table.device != dev or seq_lens.device != dev:
         raise ValueError("q, block_table and seq_lens must be on the cache's GPU")
     cu = None
     if cu_seqlens_q is not None:
-        if (cu_seqlens_q.dtype != torch.int32 or tuple(cu_seqlens_q.shape) != (batch + 1,) or not cu_seqlens_q.is_contiguous()
+        if (cu_seqlens_q.dtype != torch.int32 or cu_seqlens_q.shape != (batch + 1,) or not cu_seqlens_q.is_contiguous()
                 or cu_seqlens_q.device != dev):
             raise ValueError(f"cu_seqlens_q must be contiguous int32 [{batch + 1}] on the cache's GPU")
         cu = cu_seqlens_q.data_ptr()
     max_q = total if max_seqlen_q is None else int(max_seqlen_q)
-    max_k = cols * shape[2] if max_seqlen_k is None else int(max_seqlen_k)
+    max_k = cols * page if max_seqlen_k is None else int(max_seqlen_k)
     if out is None:
-        out = torch.empty((total, hq, d), dtype=torch.bfloat16, device=dev)
-    elif out.dtype != torch.bfloat16 or out.shape != q.shape or out.stride(2) != 1 or out.device != dev:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.dtype != torch.bfloat16 or out.shape != qshape or out.stride(2) != 1 or out.device != dev:
         raise ValueError("out must be bfloat16 of q's shape, contiguous along the last dimension, on the cache's GPU")
     lse = torch.empty((total, hq), dtype=torch.float32, device=dev) if return_lse else None
     handle = lib()
-    need = handle.dg_fp8_paged_attention_workspace(batch, total, hq, hk, d, int(cu is None), max_q, max_k, window, sinks)
+    need = handle.dg_fp8_paged_attention_workspace(batch, total, hq, hk, d, cu is None, max_q, max_k, window, sinks)
     if need < 0:
         _check(need)
     work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    qs, os_ = q.stride(), out.stride()
+    os_ = out.stride()
     _check(handle.dg_fp8_paged_attention(
-        ctypes.byref(c), batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(),
-        max(block_table.stride(0), cols), cols, seq_lens.data_ptr(), max_k, d ** -0.5 if sm_scale is None else sm_scale,
-        window, sinks, out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
-        None if work is None else work.data_ptr(), need, torch.cuda.current_stream(dev).cuda_stream))
+        c, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts[0] if ts[0] > cols else cols, cols,
+        seq_lens.data_ptr(), max_k, d ** -0.5 if sm_scale is None else sm_scale, window, sinks, out.data_ptr(), os_[0], os_[1],
+        None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(), need, _current_stream(dev)))
     return (out, lse) if return_lse else out

@@ -46,7 +46,6 @@ int api_fail(int code, const char* fmt, ...) {
   return code;
 }
 int api_ok() { return ok(); }
-int api_num_sms() { return dg_get_num_sms(); }
 }  // namespace dg
 
 namespace {
@@ -61,6 +60,25 @@ int device_cu_count() {
   if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return -1;
   return n;
 }
+
+}  // namespace
+
+namespace dg {
+int api_num_sms() {
+  const int o = g_num_sms_override.load();
+  if (o > 0) return o;
+  // a device's CU count does not change: asked once for each of the first 64
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return -1;
+  if (dev < 0 || dev >= 64) return device_cu_count();
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n <= 0) known[dev].store(n = device_cu_count(), std::memory_order_relaxed);
+  return n;
+}
+}  // namespace dg
+
+namespace {
 
 int env_int(const char* name, int dflt) {
   const char* s = getenv(name);

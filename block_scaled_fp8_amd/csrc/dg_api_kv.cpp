@@ -95,26 +95,6 @@ int move(bool write, const dg_fp8_kv_cache* cache, int32_t num_tokens, const voi
 }
 
 // ---------------------------------------------------------------- attention
-struct AttnPlan {
-  bool wide = false;
-  int q_tiles = 1, splits = 1;
-};
-
-// keys: the most keys that a row can see (from the host's bounds).
-AttnPlan plan_attention(int64_t batch, int kv_heads, int64_t rows, int64_t keys, int head_dim, int num_sms) {
-  AttnPlan pl;
-  pl.wide = rows > 2 * dg::kAttnNarrowRows;
-  const int tile = pl.wide ? dg::attn_wide_rows(head_dim) : dg::kAttnNarrowRows;
-  pl.q_tiles = int((rows + tile - 1) / tile);
-  const int64_t blocks = batch * kv_heads * pl.q_tiles;
-  const int64_t want = (2 * int64_t(num_sms) + blocks - 1) / blocks;
-  const int64_t most = keys / 256;  // at least 256 keys in a part
-  int64_t s = want < most ? want : most;
-  if (pl.wide && blocks >= num_sms) s = 1;
-  pl.splits = int(s < 1 ? 1 : s > 256 ? 256 : s);
-  return pl;
-}
-
 struct AttnShape {
   int32_t batch, total_q, num_q_heads, max_seqlen_q, max_seqlen_k, window, sinks;
   bool equal;
@@ -131,15 +111,55 @@ int check_shape(const AttnShape& a, int32_t num_kv_heads) {
   return DG_OK;
 }
 
+struct AttnPlan {
+  int form = 0, q_tiles = 1, head_aim = 0, least_tiles = 1, max_cut = 1, join_rows = 1, waves = 4;
+  int64_t items = 0, most_parts = 0;
+};
+
 AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int num_sms) {
   const int64_t per_seq = a.equal ? a.total_q / a.batch : a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
-  int64_t keys = a.max_seqlen_k;
-  if (a.window && a.window < keys - a.sinks) keys = int64_t(a.window) + a.sinks;
-  return plan_attention(a.batch, num_kv_heads, per_seq * (a.num_q_heads / num_kv_heads), keys, head_dim, num_sms);
+  const int64_t group = a.num_q_heads / num_kv_heads, rows = per_seq * group;
+  AttnPlan pl;
+  // The few-rows kernel reads the keys once for every 32 rows (from L2 after the first), the many-rows kernel
+  // spends whole tiles of 128 or 256: 33.1 against 30.6 us at 4 x 8 x 120 rows over 4000 keys.
+  pl.form = rows <= 16 ? dg::ATTN_NARROW_16 : rows <= 128 ? dg::ATTN_NARROW_32 : dg::ATTN_WIDE;
+  const int tile = dg::attn_tile_rows(pl.form, head_dim), keys = dg::attn_tile_keys(pl.form, head_dim);
+  pl.q_tiles = int((rows + tile - 1) / tile);
+  pl.join_rows = int(rows < tile ? rows : tile);
+  pl.items = int64_t(a.batch) * pl.q_tiles;
+  // Key tiles of an item at most, from the host's bound of the lengths (rounded up at both ends of a window).
+  int64_t tiles = (a.max_seqlen_k + int64_t(keys) - 1) / keys;
+  if (a.window) {
+    const int64_t seen = (int64_t(a.window) + (tile - 1) / group + keys - 1) / keys + 1 + (int64_t(a.sinks) + keys - 1) / keys;
+    if (seen < tiles) tiles = seen;
+  }
+  // Cutting items along the keys costs a second kernel and the parts' way through memory.  It is for items
+  // that are too few for the chip; where they would fill half of it, only for long ones, whose lengths
+  // it also evens out.  128 sequences in a window of 1024 (512 items of 35 tiles for 768 places): 32 us whole,
+  // 52 cut; 64 sequences of up to 8192 keys (512 items of up to 256 tiles): 128 whole, 123 cut.  For many
+  // rows a part's sums weigh more: 1024 queries over 4024 keys (128 items for 256 places) 104 us whole, 81
+  // cut; 2048 over 8192 (256 items) 250 whole, 255 cut.
+  const int64_t slots = int64_t(num_sms) * dg::attn_per_cu(pl.form, head_dim), work = pl.items * num_kv_heads;
+  const bool few = pl.form == dg::ATTN_WIDE ? work < slots : 2 * work <= slots || (work < 2 * slots && tiles >= 128);
+  pl.least_tiles = 4;
+  // Short contexts of few items: eight waves instead of the second kernel, whose launch costs the host more
+  // than it saves the device (1001 keys of 8 key heads: 11.6 against 9.1 us on the device, 8.5 against 12.9 on
+  // the host; 2000 keys: 17.1 against 9.9).  (At 256 values a head eight waves run out of registers.)
+  if (pl.form == dg::ATTN_NARROW_16 && head_dim != 256 && work <= num_sms && tiles > pl.least_tiles && tiles <= 40)
+    pl.waves = 8;
+  else if (few && pl.items <= 1024 && tiles > pl.least_tiles) {
+    pl.head_aim = int(slots < num_kv_heads ? 1 : slots / num_kv_heads);
+    pl.max_cut = int((tiles + pl.least_tiles - 1) / pl.least_tiles);
+    const int64_t by_aim = int64_t(pl.head_aim) * num_kv_heads + work, by_cut = work * pl.max_cut;
+    pl.most_parts = by_aim < by_cut ? by_aim : by_cut;
+  }
+  return pl;
 }
 
-int64_t workspace_of(const AttnShape& a, const AttnPlan& pl, int32_t head_dim) {
-  return pl.splits == 1 ? 0 : int64_t(pl.splits) * a.total_q * a.num_q_heads * (head_dim + 2) * int64_t(sizeof(float));
+int64_t part_rows(const AttnPlan& pl, int32_t head_dim) { return pl.most_parts * dg::attn_tile_rows(pl.form, head_dim); }
+
+int64_t workspace_of(const AttnPlan& pl, int32_t head_dim) {
+  return pl.head_aim ? part_rows(pl, head_dim) * (head_dim + 2) * int64_t(sizeof(float)) + (pl.items + 3) / 4 * 16 : 0;
 }
 
 }  // namespace
@@ -168,7 +188,7 @@ int64_t dg_fp8_paged_attention_workspace(int32_t batch, int32_t total_q, int32_t
   if (batch == 0 || total_q == 0 || (!a.equal && max_seqlen_q == 0)) return 0;
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
-  return workspace_of(a, plan_of(a, num_kv_heads, head_dim, num_sms), head_dim);
+  return workspace_of(plan_of(a, num_kv_heads, head_dim, num_sms), head_dim);
 }
 
 int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t total_q, int32_t num_q_heads,
@@ -195,7 +215,7 @@ int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t 
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
   const AttnPlan pl = plan_of(a, cache->num_heads, cache->head_dim, num_sms);
-  const int64_t need = workspace_of(a, pl, cache->head_dim);
+  const int64_t need = workspace_of(pl, cache->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);
   if (need > 0 && !aligned(workspace, 16)) return api_fail(DG_ERR_LAYOUT, "workspace must be 16-byte aligned");
@@ -223,11 +243,19 @@ int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t 
   // (a window that holds every possible key hides nothing)
   p.window = window < int64_t(table_cols) * cache->page_size ? window : 0;
   p.sinks = p.window ? sinks : 0;
-  p.q_tiles = pl.q_tiles;
-  p.splits = pl.splits;
+  p.q_tiles = dg::fast_div(pl.q_tiles);
+  p.tile_rows = dg::attn_tile_rows(pl.form, cache->head_dim);
+  p.items = int(pl.items);
+  p.waves = pl.waves;
+  p.head_aim = pl.head_aim;
+  p.max_cut = pl.max_cut;
+  p.join_rows = pl.join_rows;
+  p.most_parts = int(pl.most_parts);
+  p.least_tiles = pl.least_tiles;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = pl.splits > 1 ? p.part_o + int64_t(pl.splits) * total_q * num_q_heads * cache->head_dim : nullptr;
-  const hipError_t e = dg::launch_attention(p, cache->head_dim, pl.wide, stream);
+  p.part_mz = p.part_o + part_rows(pl, cache->head_dim) * cache->head_dim;
+  p.item_end = reinterpret_cast<int32_t*>(p.part_mz + part_rows(pl, cache->head_dim) * 2);
+  const hipError_t e = dg::launch_attention(p, cache->head_dim, pl.form, stream);
   if (e != hipSuccess) return api_fail(DG_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   return api_ok();
 }

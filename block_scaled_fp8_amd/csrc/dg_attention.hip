@@ -30,6 +30,7 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -85,60 +86,139 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
   return c ^ (D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2) ^ (row & 1);
 }
 
-// What a workgroup works on: a tile of query rows of one (sequence, key head), and a part of the
-// tiles of keys that these rows see.
+// An item: a tile of query rows of one sequence (and, for each key head, the tiles of keys that these
+// rows see).
 struct Work {
-  int seq, kv_head, split;
+  int seq, kv_head;
   int q_first;           // first packed query row (token) of the sequence
   int row0, rows;        // first row of the tile; rows of the sequence in all
   int place0;            // place of the sequence's first query (negative where queries exceed the context)
   int key_end;           // one past the last key that some row of the tile sees
   int key_from;          // first key of the window of the tile's first query
-  int sink_tiles, first_tile;
-  int t0, t1;            // key tiles [t0, t1) of this part, as list indices
+  int sink_tiles, first_tile, tiles;
+  int t0, t1;            // key tiles [t0, t1) of this piece of work, as list indices
+  int slot;              // where a part of an item goes; -1 for a whole item
 
   __device__ __forceinline__ int tile_key(int i, int keys) const { return (i < sink_tiles ? i : first_tile + i - sink_tiles) * keys; }
 };
 
-// KEYS: keys of a tile.  Returns false if there is no row.
-template <int KEYS>
-__device__ __forceinline__ bool get_work(const AttnParams& p, int tile_rows, Work& w) {
-  // Workgroups are dealt to the eight XCDs in turn.  With the (sequence, key head) pair as the
-  // fastest index, and a multiple of eight pairs, all workgroups of a pair land on one XCD and share
-  // its L2, and the pairs of one sequence, as long as each other, spread over the XCDs.  Later rows
-  // see more keys: they start first.
-  const unsigned pairs = p.batch * p.c.num_heads;
-  const unsigned pair = blockIdx.x % pairs;
-  unsigned id = blockIdx.x / pairs;
-  w.split = id % p.splits;
-  const int qt = p.q_tiles - 1 - (int)(id / p.splits);
-  w.kv_head = pair % p.c.num_heads;
-  w.seq = pair / p.c.num_heads;
+// A value that is the same for all lanes, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
+}
+
+// KEYS: keys of a tile.  SAME: the item is the same for all lanes.  Returns the item's weight: its key tiles, one where its rows see no key (they
+// are still to be written), 0 without rows.
+template <int KEYS, bool SAME>
+__device__ __forceinline__ int describe(const AttnParams& p, int item, Work& w) {
+  w.seq = p.q_tiles.d == 1 ? item : div(item, p.q_tiles);
+  const int qt = p.q_tiles.d == 1 ? 0 : item - w.seq * p.q_tiles.d;
   int n;
   if (p.cu_q) {
-    const int a = min(max(p.cu_q[w.seq], 0), p.total_q), b = min(max(p.cu_q[w.seq + 1], a), p.total_q);
-    w.q_first = a;
-    n = b - a;
+    int a = p.cu_q[w.seq], b = p.cu_q[w.seq + 1];
+    if (SAME) a = uniform(a), b = uniform(b);
+    w.q_first = min(max(a, 0), p.total_q);
+    n = min(max(b, w.q_first), p.total_q) - w.q_first;
   } else {
     w.q_first = w.seq * p.q_per_seq;
     n = p.q_per_seq;
   }
-  const int g = p.group.d;
-  w.rows = n * g;
-  w.row0 = qt * tile_rows;
-  if (w.row0 >= w.rows) return false;
-  const int64_t held = (int64_t)p.table_cols * p.c.page.d;
-  const int ctx = (int)min((int64_t)max(p.seq_lens[w.seq], 0), held);
+  int ctx = p.seq_lens[w.seq];
+  if (SAME) ctx = uniform(ctx);
+  ctx = min(max(ctx, 0), p.table_cols * p.c.page.d);
+  w.rows = n * p.group.d;
+  w.row0 = qt * p.tile_rows;
   w.place0 = ctx - n;
   const int first = w.place0 + div(w.row0, p.group);
-  const int last = w.place0 + div(min(w.row0 + tile_rows, w.rows) - 1, p.group);
+  const int last = w.place0 + div(max(min(w.row0 + p.tile_rows, w.rows) - 1, 0), p.group);
   w.key_end = max(last + 1, 0);
   w.key_from = p.window ? max(first - p.window + 1, 0) : 0;
   w.first_tile = w.key_from / KEYS;
   w.sink_tiles = min((min(p.sinks, w.key_end) + KEYS - 1) / KEYS, w.first_tile);
-  const int tiles = w.key_end > 0 ? w.sink_tiles + (w.key_end + KEYS - 1) / KEYS - w.first_tile : 0;
-  w.t0 = (int)((int64_t)tiles * w.split / p.splits);
-  w.t1 = (int)((int64_t)tiles * (w.split + 1) / p.splits);
+  w.tiles = w.key_end > 0 ? w.sink_tiles + (w.key_end + KEYS - 1) / KEYS - w.first_tile : 0;
+  return w.row0 < w.rows ? max(w.tiles, 1) : 0;
+}
+
+// Sum over the lanes up to and with one's own.
+__device__ __forceinline__ int scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // from 1, 2, 4, 8 lanes before, in rows of 16
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // the last lane of row 0 (2) into row 1 (3)
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // lane 31 into rows 2 and 3
+  return x;
+}
+
+// How the work is dealt where items are cut: into parts of about as many key tiles, a number that follows
+// from the lengths, and so is known to the device only.  A head's parts are numbered item after item, and
+// heads follow each other.  A part of an item that is not cut writes the item; else it leaves its sums
+// in the slot of its number, and join_kernel adds them up.
+//
+// With t_i the items' weights (up to 2^20: 1024 items' sum stays a 32-bit number), T their sum and
+// n = head_aim, an item is cut into t_i / s parts, to the nearest, with s = max(least_tiles, ceil(T / n)), raised to a
+// multiple of four (the few-rows kernel's waves), so there are at most n + items of them.
+// The host's bound of the lengths, which may be wrong, enters as max_cut, the most parts of an item, alone.
+struct Cut {
+  unsigned size, max_cut;
+  __device__ __forceinline__ int parts(int weight) const { return weight ? (int)min(max(((unsigned)weight + size / 2) / size, 1u), max_cut) : 0; }
+};
+
+// The workgroup's piece of work; false if there is none.
+template <int KEYS>
+__device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
+  if (p.head_aim == 0) {
+    // One workgroup for each item and key head.  Workgroups are dealt to the eight XCDs in turn: with the
+    // (sequence, key head) pair as the fastest index, and a multiple of eight pairs, those of a pair land on
+    // one XCD and share its L2, and the pairs of a sequence spread over the XCDs.  Later rows see more
+    // keys: they start first.
+    const int pairs = p.batch * p.c.num_heads, pair = blockIdx.x % pairs;
+    w.kv_head = pair % p.c.num_heads;
+    if (!describe<KEYS, true>(p, pair / p.c.num_heads * p.q_tiles.d + p.q_tiles.d - 1 - blockIdx.x / pairs, w)) return false;
+    w.t0 = 0;
+    w.t1 = w.tiles;
+    w.slot = -1;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  auto weight = [&](int item) { return item < p.items ? min(describe<KEYS, false>(p, item, w), 1 << 20) : 0; };
+  const int mine = weight(lane);  // (kept for the search among the first 64 items)
+  int per_head = __builtin_amdgcn_readlane(scan(mine), 63);
+  for (int base = 64; base < p.items; base += 64) per_head += __builtin_amdgcn_readlane(scan(weight(base + lane)), 63);
+  if (per_head == 0) return false;
+  const Cut cut{(max((unsigned)p.least_tiles, ((unsigned)per_head + p.head_aim - 1) / (unsigned)p.head_aim) + 3) & ~3u, (unsigned)p.max_cut};
+  int sums = scan(cut.parts(mine)), all = __builtin_amdgcn_readlane(sums, 63);
+  if (blockIdx.x == 0 && threadIdx.x < 64 && lane < p.items) p.item_end[lane] = sums;
+  for (int base = 64; base < p.items; base += 64) {
+    const int x = scan(cut.parts(weight(base + lane)));
+    if (blockIdx.x == 0 && threadIdx.x < 64 && base + lane < p.items) p.item_end[base + lane] = all + x;
+    all += __builtin_amdgcn_readlane(x, 63);
+  }
+  // renumbered, each XCD takes a contiguous run, so the parts of a (sequence, key head) pair share an L2
+  const int nb = all * p.c.num_heads;
+  if ((int)blockIdx.x >= nb) return false;
+  const int per = nb >> 3, extra = nb & 7, xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+  const int id = xcd < extra ? xcd * (per + 1) + idx : extra * (per + 1) + (xcd - extra) * per + idx;
+  const int kv_head = uniform((int)((unsigned)id / (unsigned)all));
+  int want = id - kv_head * all, item = 0;
+  for (int base = 0;; base += 64) {
+    if (base) sums = scan(cut.parts(weight(base + lane)));
+    const uint64_t later = __ballot(sums > want);
+    if (later) {
+      const int l = __builtin_ctzll(later);
+      item = base + l;
+      want -= l ? __builtin_amdgcn_readlane(sums, l - 1) : 0;
+      break;
+    }
+    want -= __builtin_amdgcn_readlane(sums, 63);
+  }
+  const int n = uniform(cut.parts(min(describe<KEYS, true>(p, item, w), 1 << 20)));
+  const int share = uniform((int)((unsigned)w.tiles / (unsigned)n)), more = w.tiles - share * n;
+  w.kv_head = kv_head;
+  w.t0 = want * share + min(want, more);
+  w.t1 = w.t0 + share + (want < more ? 1 : 0);
+  w.slot = n == 1 ? -1 : id;
   return true;
 }
 
@@ -159,10 +239,12 @@ __device__ __forceinline__ int page_entry(const AttnParams& p, const int32_t* ro
 struct Row {
   int place;        // its place in the sequence; very low for rows that do not exist
   int token, head;  // packed query row and query head
+  int r;            // number among the sequence's rows
   bool live;
 };
 __device__ __forceinline__ Row get_row(const AttnParams& p, const Work& w, int r) {
   Row o;
+  o.r = r;
   o.live = r < w.rows;
   const int t = div(min(r, w.rows - 1), p.group);
   o.head = w.kv_head * p.group.d + min(r, w.rows - 1) - t * p.group.d;
@@ -284,15 +366,19 @@ __device__ __forceinline__ void product_v(State<D>& st, const v8bf (&w)[NB][2], 
     }
 }
 
-// A part's result, or the final one where there is a single part.  Register i of 16-group d is
-// value 32 d + 8 (i / 4) + 4 (lane / 32) + i % 4.  z: summed over the half waves.
+__device__ __forceinline__ float inverse(float z) { return z > 0.f ? 1.f / z : (z == z ? 0.f : z); }
+__device__ __forceinline__ float log_sum(float m, float z) {
+  return z > 0.f ? (m + __log2f(z)) * 0.6931471805599453f : (z == z ? NEG_INF : z);
+}
+
+// An item's result, or a part's.  Register i of 16-group d is value 32 d + 8 (i / 4) + 4 (lane / 32) + i % 4.
+// z: summed over the half waves.
 template <int D>
 __device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, const Row& row, const v16f (&o)[D / 32],
                                           float m, float z, int h) {
   if (!row.live) return;
-  const int64_t idx = (int64_t)row.token * p.num_q_heads + row.head;
-  if (p.splits == 1) {
-    const float f = z > 0.f ? 1.f / z : (z == z ? 0.f : z);
+  if (w.slot < 0) {
+    const float f = inverse(z);
     uint16_t* dst = p.out + row.token * p.o_token_stride + row.head * p.o_head_stride;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -300,19 +386,16 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, co
       for (int j = 0; j < 4; ++j)
         *(v2u*)(dst + 32 * d + 8 * j + 4 * h) = (v2u){pack2(o[d][4 * j] * f, o[d][4 * j + 1] * f),
                                                       pack2(o[d][4 * j + 2] * f, o[d][4 * j + 3] * f)};
-    if (p.lse && h == 0) p.lse[idx] = z > 0.f ? (m + __log2f(z)) * 0.6931471805599453f : (z == z ? NEG_INF : z);
+    if (p.lse && h == 0) p.lse[(int64_t)row.token * p.num_q_heads + row.head] = log_sum(m, z);
   } else {
-    const int64_t at = (int64_t)w.split * p.total_q * p.num_q_heads + idx;
+    const int64_t at = (int64_t)w.slot * p.tile_rows + row.r - w.row0;
     float* dst = p.part_o + at * D;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *(v4f*)(dst + 32 * d + 8 * j + 4 * h) = (v4f){o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
-    if (h == 0) {
-      p.part_ml[2 * at] = m;
-      p.part_ml[2 * at + 1] = z;
-    }
+    if (h == 0) *(v2f*)(p.part_mz + 2 * at) = (v2f){m, z};
   }
 }
 
@@ -357,9 +440,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
   constexpr int NW = Wide<D>::NW, KEYS = Wide<D>::KEYS, NB = Wide<D>::NB, TILE = Wide<D>::TILE;
   constexpr int CH = D / 16, GR = 64 / CH, GROUPS = KEYS / GR, NU = 2 * GROUPS / NW;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][Wide<D>::TURNS ? 3 : 2][TILE];  // [K, V][slot]
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   Work w;
-  if (!get_work<KEYS>(p, Wide<D>::ROWS_ALL, w)) return;
+  if (!get_work<KEYS>(p, w)) return;
   const Row row = get_row(p, w, w.row0 + wave * ROWS + (lane & 31));
   // the places of this wave's rows, for whole-tile decisions
   const int wr0 = w.row0 + wave * ROWS;
@@ -499,7 +582,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
   };
   // Without turns: tile i with K and V in slot X; leaves tile i + 1 in the other slot and tile i + 2 on its way.
   auto plain_step = [&](int i, auto slot) {
-    constexpr int X = decltype(slot)::value, AHEAD = 3;
+    constexpr int X = decltype(slot)::value, AHEAD = 2;
     v16f s[NB];
     scores(s, lds[0][X]);
     __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
@@ -563,204 +646,416 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
 }
 
 // ---------------------------------------------------------------- few rows: single tokens
-// The four waves share up to 32 query rows and take the key tiles (32 keys) in turn.  A wave reads
-// K straight into operand registers (the order of D within the contraction is free: half wave h
-// takes bytes 16 h.. of every 32), stages V in its own LDS slice for the transposing reads, and
-// keeps the next tile's loads in flight.  The waves' sums are joined at the end.
+// Bound by reading the cache once.  The four waves share 16 RB query rows and take the item's key tiles
+// (32 keys) in turn, each by itself: no barrier until their sums are joined.  A wave reads K straight
+// into operand registers (the order of D within the contraction is free: lane group g takes bytes
+// 16 g.. of every 64), stages V in its own LDS slice for the transposing reads, and has the next
+// tile's loads on their way before the softmax.  16 x 16 matrix instructions: with 32 columns, single
+// tokens of 8 heads a key head left registers for half as many waves.
+//
+// S^T in blocks of 16 keys: lane group g (lane / 16) holds keys 4 g + i of query lane % 16.  In the second
+// product's step of 32 keys, group g's eight operand places are keys 4 g + i and 16 + 4 g + i.
+// Without a common page for each 16 keys, rows are addressed lane by lane.
 template <int D>
-__global__ void __launch_bounds__(256) narrow_kernel(const AttnParams p) {
-  constexpr int KEYS = 32, NW = 4, TILE = KEYS * D * 2;
-  constexpr int CH = D / 16, PASS = 64 / CH, NP = KEYS / PASS;
+__device__ __forceinline__ int narrow_chunk(int row, int c) {
+  // 32-byte pieces of a row move by its number, so that 16 lanes' 4 rows, and the next groups', differ in
+  // banks; within a piece the 16-byte halves change places on odd rows, for the writes
+  return c ^ (D == 64 ? ((row >> 1) & 3) << 1 : (row & 7) << 1) ^ (row & 1);
+}
+
+// Maximum and sum over the four lane groups.
+__device__ __forceinline__ float groups_max(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return both_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float groups_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return both_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// Buffer descriptor from a scalar address on, 2^31 - 1 bytes long (the host keeps a head's page below that).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((int64_t)base), (short)0, 0x7FFFFFFF, 0x00020000);
+}
+
+template <int D, int RB, int NW>
+__global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const AttnParams p) {
+  constexpr int KEYS = 32, TILE = KEYS * D * 2;
+  constexpr int CH = D / 16, PASS = 64 / CH, NP = KEYS / PASS;  // V: 16-code chunks of a row, rows of a load, loads
+  constexpr int ROWS_ALL = 16 * RB;
   constexpr int JD = 64;  // values of D joined at once
-  constexpr int JOIN = NW * ROWS * (JD + 4) * 4;
+  constexpr int JOIN = NW * ROWS_ALL * (JD + 4) * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[NW * TILE > JOIN ? NW * TILE : JOIN];
-  __shared__ float ml[NW][2][ROWS];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  __shared__ float mz[NW][2][ROWS_ALL];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), g = lane >> 4, col = lane & 15;
+  uint8_t* vt = lds + wave * TILE;
+  const bool halves_whole = p.c.page.d % 16 == 0;
+  const uint32_t k_at = (uint32_t)(col * p.c.token_stride) + 16 * g, k_sf_at = (uint32_t)(col * p.c.sf_token_stride);
+  const uint32_t v_at = (uint32_t)(lane / CH * p.c.token_stride) + 16 * (lane % CH), v_sf_at = (uint32_t)(lane / CH * p.c.sf_token_stride);
+  const uint32_t v_step = (uint32_t)(PASS * p.c.token_stride), v_sf_step = (uint32_t)(PASS * p.c.sf_token_stride);
+
   Work w;
-  if (!get_work<KEYS>(p, kAttnNarrowRows, w)) return;
-  const Row row = get_row(p, w, w.row0 + (lane & 31));
-  const int place_lo = w.place0 + div(w.row0, p.group);
-  const int place_hi = w.place0 + div(min(w.row0 + ROWS, w.rows) - 1, p.group);
-  v8bf q[D / 16];
-  {
-    const uint16_t* src = p.q + row.token * p.q_token_stride + row.head * p.q_head_stride + 16 * h;
+  if (!get_work<KEYS>(p, w)) return;
+  Row row[RB];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      q[2 * i] = *(const v8bf*)(src + 32 * i);
-      q[2 * i + 1] = *(const v8bf*)(src + 32 * i + 8);
+  for (int b = 0; b < RB; ++b) row[b] = get_row(p, w, w.row0 + 16 * b + col);
+  const int place_lo = w.place0 + div(w.row0, p.group);
+  const int place_hi = w.place0 + div(min(w.row0 + ROWS_ALL, w.rows) - 1, p.group);
+  v8bf q[RB][D / 32];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const uint16_t* src = p.q + row[b].token * p.q_token_stride + row[b].head * p.q_head_stride + 16 * g;
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) {
+      q[b][2 * x] = *(const v8bf*)(src + 64 * x);
+      q[b][2 * x + 1] = *(const v8bf*)(src + 64 * x + 8);
     }
   }
   const int32_t* table = p.table + w.seq * p.table_stride;
-  const int64_t head_at = w.kv_head * p.c.head_stride;
-  uint8_t* vt = lds + wave * TILE;
-  v4u kr[D / 32], vr[NP];
-  uint32_t ks, vs[NP];
-  auto fetch = [&](int i) {
-    // lane and lane + 32 look the page of key lane % 32 up; V's rows take it from there
-    const int j = key_to_load(w, p.sinks, w.tile_key(i, KEYS) + (lane & 31));
-    const int col = div(j, p.c.page), off = j - col * p.c.page.d, pg = page_entry(p, table, col);
-    const uint8_t* k = p.c.k + pg * p.c.page_stride + head_at + off * p.c.token_stride + 16 * h;
+  const int64_t head_at = w.kv_head * p.c.head_stride, head_sf = w.kv_head * p.c.sf_head_stride;
+  // 128 entries of the block table, two a lane, from column table_from; the second 64 are loaded when
+  // the first come into use
+  int table_from = INT32_MIN / 2, entries = 0, entries_next = 0;
+  auto load_entries = [&](int c) {
+    const int e = table[min(max(c, 0) + lane, p.table_cols - 1)];
+    return (unsigned)e < (unsigned)p.c.num_pages ? e : 0;
+  };
+  // Byte offsets of the tile's two halves (16 keys) where that will do.
+  struct Half {
+    int64_t code, sf;
+  };
+  Half half[2];
+  bool fast = false;
+  int next_key = 0;
+  auto place = [&](int i) {
+    const int key0 = w.tile_key(i, KEYS);
+    next_key = key0;
+    fast = halves_whole && key0 + KEYS <= w.key_end && (key0 >= w.key_from || key0 + KEYS <= p.sinks);
+    if (!fast) return;
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) kr[x] = *(const v4u*)(k + 32 * x);
-    ks = p.c.k_sf[pg * p.c.sf_page_stride + w.kv_head * p.c.sf_head_stride + off * p.c.sf_token_stride];
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int r = lane / CH + n * PASS;
-      const int vpg = __shfl(pg, r), voff = __shfl(off, r);
-      vr[n] = *(const v4u*)(p.c.v + vpg * p.c.page_stride + head_at + voff * p.c.token_stride + 16 * (lane % CH));
-      vs[n] = p.c.v_sf[vpg * p.c.sf_page_stride + w.kv_head * p.c.sf_head_stride + voff * p.c.sf_token_stride];
+    for (int x = 0; x < 2; ++x) {
+      const int c = div(key0 + 16 * x, p.c.page);
+      if ((unsigned)(c - table_from) >= 64u) {
+        entries = (unsigned)(c - table_from) < 128u ? entries_next : load_entries(c);
+        table_from = (unsigned)(c - table_from) < 128u ? table_from + 64 : c;
+        entries_next = load_entries(table_from + 64);
+      }
+      const uint32_t pg = __builtin_amdgcn_readlane(entries, c - table_from), off = key0 + 16 * x - c * p.c.page.d;
+      half[x].code = (int64_t)(pg * (uint64_t)p.c.page_stride + head_at + off * (uint32_t)p.c.token_stride);
+      half[x].sf = (int64_t)(pg * (uint64_t)p.c.sf_page_stride + head_sf + off * (uint32_t)p.c.sf_token_stride);
     }
   };
-  State<D> st;
-  init(st);
+  auto slow_row = [&](int j) {
+    j = key_to_load(w, p.sinks, j);
+    const int c = div(j, p.c.page), off = j - c * p.c.page.d, pg = page_entry(p, table, c);
+    return Half{pg * p.c.page_stride + head_at + off * p.c.token_stride, pg * p.c.sf_page_stride + head_sf + off * p.c.sf_token_stride};
+  };
+  v4u kr[2][D / 64], vr[NP];
+  uint32_t ks[2], vs[NP];
+  // (Where the rows' addresses are scalar, through buffer descriptors of the halves; lane by lane, the
+  // scale bytes are widened at once, so that the two ways' values meet as words: as bytes they would be
+  // widened where they meet, and waited for there.)
+  auto fetch_k = [&]() {
+    if (fast) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const __amdgpu_buffer_rsrc_t codes = rsrc(p.c.k + half[x].code), sf = rsrc(p.c.k_sf + half[x].sf);
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y) kr[x][y] = __builtin_amdgcn_raw_buffer_load_b128(codes, k_at + 64 * y, 0, 0);
+        ks[x] = __builtin_amdgcn_raw_buffer_load_b8(sf, k_sf_at, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const Half a = slow_row(next_key + 16 * x + col);
+#pragma unroll
+        for (int y = 0; y < D / 64; ++y) kr[x][y] = *(const v4u*)(p.c.k + a.code + 16 * g + 64 * y);
+        ks[x] = p.c.k_sf[a.sf];
+        asm volatile("" : "+v"(ks[x]));
+      }
+    }
+  };
+  auto fetch_v = [&]() {
+    if (fast) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const __amdgpu_buffer_rsrc_t codes = rsrc(p.c.v + half[x].code), sf = rsrc(p.c.v_sf + half[x].sf);
+#pragma unroll
+        for (int n = 0; n < NP / 2; ++n) {
+          vr[x * (NP / 2) + n] = __builtin_amdgcn_raw_buffer_load_b128(codes, v_at, n * v_step, 0);
+          vs[x * (NP / 2) + n] = __builtin_amdgcn_raw_buffer_load_b8(sf, v_sf_at, n * v_sf_step, 0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        const Half a = slow_row(next_key + n * PASS + lane / CH);
+        vr[n] = *(const v4u*)(p.c.v + a.code + 16 * (lane % CH));
+        vs[n] = p.c.v_sf[a.sf];
+        asm volatile("" : "+v"(vs[n]));
+      }
+    }
+  };
+
+  v4f o[RB][D / 16];
+  float m[RB], z[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    m[b] = NEG_INF;
+    z[b] = 0.f;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) o[b][d] = (v4f){0.f, 0.f, 0.f, 0.f};
+  }
   int i = w.t0 + wave;
-  if (i < w.t1) fetch(i);
+  if (i < w.t1) {
+    place(i);
+    fetch_k();
+    fetch_v();
+    // (keeps the compiler from carrying these through the loop as bytes, which it would widen, and so
+    // wait for, where they are loaded)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) asm volatile("" : "+v"(ks[x]));
+#pragma unroll
+    for (int n = 0; n < NP; ++n) asm volatile("" : "+v"(vs[n]));
+  }
   for (; i < w.t1; i += NW) {
     const int key0 = w.tile_key(i, KEYS);
-    v16f s[1];
+    const bool more = i + NW < w.t1;
+    if (more) place(i + NW);
+    v4f s[RB][2];
 #pragma unroll
-    for (int x = 0; x < 16; ++x) s[0][x] = 0.f;
-    const float a = __uint_as_float(ks << 23);
+    for (int b = 0; b < RB; ++b) s[b][0] = s[b][1] = (v4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) {
-      s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, widen8(kr[x].x, kr[x].y, a)), q[2 * x], s[0], 0, 0, 0);
-      s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, widen8(kr[x].z, kr[x].w, a)), q[2 * x + 1], s[0], 0, 0, 0);
+    for (int x = 0; x < 2; ++x) {
+      const float scale = __uint_as_float(ks[x] << 23);
+#pragma unroll
+      for (int y = 0; y < D / 64; ++y) {
+        const v8bf lo = __builtin_bit_cast(v8bf, widen8(kr[x][y].x, kr[x][y].y, scale));
+        const v8bf hi = __builtin_bit_cast(v8bf, widen8(kr[x][y].z, kr[x][y].w, scale));
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          s[b][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, q[b][2 * y], s[b][x], 0, 0, 0);
+          s[b][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, q[b][2 * y + 1], s[b][x], 0, 0, 0);
+        }
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) fetch_k();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       const int r = lane / CH + n * PASS, c = lane % CH;
-      const float b = __uint_as_float(vs[n] << 23);
-      *(v4u*)(vt + r * 2 * D + v_chunk<D>(r, 2 * c) * 16) = widen8(vr[n].x, vr[n].y, b);
-      *(v4u*)(vt + r * 2 * D + v_chunk<D>(r, 2 * c + 1) * 16) = widen8(vr[n].z, vr[n].w, b);
+      const float scale = __uint_as_float(vs[n] << 23);
+      *(v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c) * 16) = widen8(vr[n].x, vr[n].y, scale);
+      *(v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c + 1) * 16) = widen8(vr[n].z, vr[n].w, scale);
     }
-    if (i + NW < w.t1) fetch(i + NW);
-    v8bf wt[1][2];
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) fetch_v();
+    __builtin_amdgcn_sched_barrier(0);
     const bool late = key0 + KEYS - 1 > place_lo, early = p.window && key0 <= place_hi - p.window && key0 + KEYS > p.sinks;
-    if (late || early) mask<1>(p, s, key0, row.place, h, late, early);
-    softmax<D, 1>(p, st, s, wt);
+    v8bf wt[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      if (late || early) {
+        const int first = key0 + 4 * g, end = row[b].place - first, from = p.window ? end - p.window : INT32_MIN, sinks = p.sinks - first;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = 16 * x + e;
+            s[b][x][e] = c <= end && (c > from || c < sinks) ? s[b][x][e] : NEG_INF;
+          }
+      }
+      float top = s[b][0][0];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[b][x][e]);
+      top = groups_max(top) * p.scale_log2;  // (the scale is positive)
+      if (__any(top > m[b] + SLACK)) {
+        const float raised = fmaxf(m[b], top);
+        const float f = raised == NEG_INF ? 1.f : exp2_hw(m[b] - raised);
+        m[b] = raised;
+        z[b] *= f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[b][d] *= f;
+      }
+      const float sub = m[b] == NEG_INF ? 0.f : -m[b];  // nothing seen yet: every weight is 2^-inf = 0
+      v4u x4;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[b][x][e] = exp2_hw(__builtin_fmaf(s[b][x][e], p.scale_log2, sub));
+          z[b] += s[b][x][e];
+        }
+        x4[2 * x] = pack2(s[b][x][0], s[b][x][1]);
+        x4[2 * x + 1] = pack2(s[b][x][2], s[b][x][3]);
+      }
+      wt[b] = __builtin_bit_cast(v8bf, x4);
+    }
     // the wave reads what its other lanes wrote: its LDS operations complete in order, so only the
     // compiler has to keep theirs
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    product_v<D, 1>(st, wt, vt, lane);
+    const int r = 4 * g + (col >> 2);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const int at = r * 2 * D + narrow_chunk<D>(r, 2 * d + ((lane & 3) >> 1)) * 16 + (lane & 1) * 8;
+      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LDS v4s*)(vt + at));
+      const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LDS v4s*)(vt + at + 16 * 2 * D));
+      const v8s a = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        o[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), wt[b], o[b][d], 0, 0, 0);
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
-  // join: rescale to the common maximum, add up through LDS
-  const float z = both_sum(st.z);
-  if (h == 0) {
-    ml[wave][0][lane] = st.m;
-    ml[wave][1][lane] = z;
+
+  // join the waves: rescale to the common maximum and add up through LDS, JD values of D at a time
+  float f[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    z[b] = groups_sum(z[b]);
+    if (g == 0) {
+      mz[wave][0][16 * b + col] = m[b];
+      mz[wave][1][16 * b + col] = z[b];
+    }
   }
   __syncthreads();
-  float m = NEG_INF, zz = 0.f;
 #pragma unroll
-  for (int x = 0; x < NW; ++x) m = fmaxf(m, ml[x][0][lane & 31]);
+  for (int b = 0; b < RB; ++b) {
+    float all = NEG_INF;
 #pragma unroll
-  for (int x = 0; x < NW; ++x) {
-    const float mx = ml[x][0][lane & 31];
-    zz += (m == NEG_INF ? 1.f : exp2_hw(mx - m)) * ml[x][1][lane & 31];
+    for (int x = 0; x < NW; ++x) all = fmaxf(all, mz[x][0][16 * b + col]);
+    f[b] = all == NEG_INF ? 1.f : exp2_hw(m[b] - all);
   }
-  const float f = m == NEG_INF ? 1.f : exp2_hw(st.m - m);
   float* jo = (float*)lds;
-  // JD values of D at a time: every wave puts its part, wave x adds up and keeps 32-value group x
-  const int64_t idx = (int64_t)row.token * p.num_q_heads + row.head;
+  // this thread (of the first 256) adds up row jr (and jr + 16), values jd.. of JD
+  const int jr = threadIdx.x >> 4, jd = 4 * (threadIdx.x & 15);
 #pragma unroll
-  for (int d0 = 0; d0 < D / 32; d0 += JD / 32) {
+  for (int d0 = 0; d0 < D; d0 += JD) {
+    if (d0) __syncthreads();
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int d = 0; d < JD / 16; ++d)
+        *(v4f*)(jo + (wave * ROWS_ALL + 16 * b + col) * (JD + 4) + 16 * d + 4 * g) = o[b][d0 / 16 + d] * f[b];
     __syncthreads();
 #pragma unroll
-    for (int d = 0; d < JD / 32; ++d)
+    for (int b = 0; b < RB; ++b) {
+      const Row out = get_row(p, w, w.row0 + 16 * b + jr);
+      if (jr >= 16 || !out.live) continue;
+      float all = NEG_INF, sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *(v4f*)(jo + (wave * ROWS + (lane & 31)) * (JD + 4) + 32 * d + 8 * j + 4 * h) =
-            (v4f){st.o[d0 + d][4 * j] * f, st.o[d0 + d][4 * j + 1] * f, st.o[d0 + d][4 * j + 2] * f, st.o[d0 + d][4 * j + 3] * f};
-    __syncthreads();
-    // wave x, half h: values 16 x + 8 h .. + 7 of the JD
-    v4f a[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      for (int x = 0; x < NW; ++x) all = fmaxf(all, mz[x][0][16 * b + jr]);
 #pragma unroll
-    for (int x = 0; x < NW; ++x) {
-      const float* src = jo + (x * ROWS + (lane & 31)) * (JD + 4) + 16 * wave + 8 * h;
-      a[0] += *(const v4f*)src;
-      a[1] += *(const v4f*)(src + 4);
-    }
-    if (row.live) {
-      const int d = 32 * d0 + 16 * wave + 8 * h;
-      if (p.splits == 1) {
-        const float g = zz > 0.f ? 1.f / zz : (zz == zz ? 0.f : zz);
-        *(v4u*)(p.out + row.token * p.o_token_stride + row.head * p.o_head_stride + d) =
-            (v4u){pack2(a[0].x * g, a[0].y * g), pack2(a[0].z * g, a[0].w * g), pack2(a[1].x * g, a[1].y * g),
-                  pack2(a[1].z * g, a[1].w * g)};
+      for (int x = 0; x < NW; ++x) sum += (all == NEG_INF ? 1.f : exp2_hw(mz[x][0][16 * b + jr] - all)) * mz[x][1][16 * b + jr];
+      v4f a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < NW; ++x) a += *(const v4f*)(jo + (x * ROWS_ALL + 16 * b + jr) * (JD + 4) + jd);
+      if (w.slot < 0) {
+        a *= inverse(sum);
+        *(v2u*)(p.out + out.token * p.o_token_stride + out.head * p.o_head_stride + d0 + jd) = (v2u){pack2(a.x, a.y), pack2(a.z, a.w)};
+        if (p.lse && d0 == 0 && jd == 0) p.lse[(int64_t)out.token * p.num_q_heads + out.head] = log_sum(all, sum);
       } else {
-        float* dst = p.part_o + ((int64_t)w.split * p.total_q * p.num_q_heads + idx) * D + d;
-        *(v4f*)dst = a[0];
-        *(v4f*)(dst + 4) = a[1];
+        const int64_t at = (int64_t)w.slot * ROWS_ALL + 16 * b + jr;
+        *(v4f*)(p.part_o + at * D + d0 + jd) = a;
+        if (d0 == 0 && jd == 0) *(v2f*)(p.part_mz + 2 * at) = (v2f){all, sum};
       }
-    }
-  }
-  if (row.live && wave == 0 && h == 0) {
-    if (p.splits > 1) {
-      const int64_t at = (int64_t)w.split * p.total_q * p.num_q_heads + idx;
-      p.part_ml[2 * at] = m;
-      p.part_ml[2 * at + 1] = zz;
-    } else if (p.lse) {
-      p.lse[idx] = zz > 0.f ? (m + __log2f(zz)) * 0.6931471805599453f : (zz == zz ? NEG_INF : zz);
     }
   }
 }
 
 // ---------------------------------------------------------------- joining the parts
-// One wave per (token, head): out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) z_s.
-template <int D>
+// out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) z_s over the parts s of a row's item.  A row is G groups of
+// D / 4 lanes; group x takes parts x, x + G, ..., and the groups' sums are added in their order.  G = 1
+// where rows are many, 256 threads for a row where they are few and their parts many.
+template <int D, bool FEW>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
-  constexpr int E = D / 64;  // values of a lane
-  const int64_t rows = (int64_t)p.total_q * p.num_q_heads;
-  const int64_t idx = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (idx >= rows) return;
-  const int token = (int)(idx / p.num_q_heads), head = (int)(idx - (int64_t)token * p.num_q_heads);
-  if (p.cu_q && (token < p.cu_q[0] || token >= p.cu_q[p.batch])) return;  // rows of no sequence
-  float m = NEG_INF;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_ml[2 * (s * rows + idx)]);
-  float z = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t at = s * rows + idx;
-    const float ms = p.part_ml[2 * at];
-    if (ms == NEG_INF) continue;  // (a part without keys)
-    const float f = exp2_hw(ms - m);
-    z += f * p.part_ml[2 * at + 1];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += f * p.part_o[at * D + E * lane + e];
+  constexpr int L = D / 4, G = FEW ? 256 / L : 1, PER = 256 / (L * G);  // rows of a workgroup
+  const int lanes = threadIdx.x % L, group = threadIdx.x / L % G;
+  const int blocks = (p.join_rows + PER - 1) / PER, part_row = blockIdx.x % blocks * PER + threadIdx.x / (L * G);
+  const int id = blockIdx.x / blocks, kv_head = id % p.c.num_heads, item = id / p.c.num_heads;
+  const int all = p.item_end[p.items - 1], end = p.item_end[item], from = item ? p.item_end[item - 1] : 0, n = end - from;
+  if (n <= 1) return;  // no rows, or written as a whole
+  Work w;
+  describe<32, true>(p, item, w);
+  w.kv_head = kv_head;
+  const Row row = get_row(p, w, w.row0 + part_row);
+  const int64_t at = (int64_t)(kv_head * all + from) * p.tile_rows + part_row;
+  const v2f* mz = (const v2f*)p.part_mz + at;
+  const float* part = p.part_o + at * D + 4 * lanes;
+  const int64_t step = p.tile_rows;
+  float m = NEG_INF, z = 0.f;
+  v4f o = {0.f, 0.f, 0.f, 0.f};
+  if (row.live) {
+    // (each group by its own running maximum)
+    for (int x = group; x < n; x += G) {
+      const v2f a = mz[x * step];
+      const v4f b = *(const v4f*)(part + x * step * D);
+      if (a.x == NEG_INF) continue;  // a part in which the row sees nothing
+      const float top = fmaxf(m, a.x), f = exp2_hw(m - top), g = exp2_hw(a.x - top);
+      z = z * f + a.y * g;
+      o = o * f + b * g;
+      m = top;
+    }
   }
-  const float g = z > 0.f ? 1.f / z : (z == z ? 0.f : z);
-  uint16_t* dst = p.out + token * p.o_token_stride + head * p.o_head_stride + E * lane;
+  if constexpr (FEW) {
+    __shared__ float sums[G][L][4], tops[G][2];
+    *(v4f*)sums[group][lanes] = o;
+    if (lanes == 0) tops[group][0] = m, tops[group][1] = z;
+    __syncthreads();
+    if (group != 0) return;
 #pragma unroll
-  for (int e = 0; e < E; ++e) dst[e] = __builtin_bit_cast(uint16_t, (__bf16)(o[e] * g));
-  if (p.lse && lane == 0) p.lse[idx] = z > 0.f ? (m + __log2f(z)) * 0.6931471805599453f : (z == z ? NEG_INF : z);
+    for (int x = 0; x < G; ++x) m = fmaxf(m, tops[x][0]);
+    z = 0.f;
+    o = 0.f;
+#pragma unroll
+    for (int x = 0; x < G; ++x) {
+      const float f = tops[x][0] == NEG_INF ? 0.f : exp2_hw(tops[x][0] - m);
+      z += f * tops[x][1];
+      o += f * *(const v4f*)sums[x][lanes];
+    }
+  }
+  if (!row.live) return;
+  o *= inverse(z);
+  *(v2u*)(p.out + row.token * p.o_token_stride + row.head * p.o_head_stride + 4 * lanes) = (v2u){pack2(o.x, o.y), pack2(o.z, o.w)};
+  if (p.lse && lanes == 0) p.lse[(int64_t)row.token * p.num_q_heads + row.head] = log_sum(m, z);
 }
 
 template <int D>
-hipError_t launch(const AttnParams& p, bool wide, hipStream_t stream) {
-  const int64_t grid = (int64_t)p.batch * p.c.num_heads * p.q_tiles * p.splits;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  if (wide)
+hipError_t launch(const AttnParams& p, int form, hipStream_t stream) {
+  const int64_t whole = (int64_t)p.items * p.c.num_heads, grid = p.head_aim ? p.most_parts : whole;
+  const bool few = form != ATTN_WIDE;
+  const int64_t blocks = whole * (few ? p.join_rows : (p.join_rows + 1024 / D - 1) / (1024 / D));
+  if (grid > INT32_MAX || blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (form == ATTN_WIDE)
     hipLaunchKernelGGL((wide_kernel<D>), dim3((unsigned)grid), dim3(Wide<D>::THREADS), 0, stream, p);
+  else if (form == ATTN_NARROW_32)
+    hipLaunchKernelGGL((narrow_kernel<D, 2, 4>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+  else if (p.waves == 4)
+    hipLaunchKernelGGL((narrow_kernel<D, 1, 4>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+  else if constexpr (D != 256)
+    hipLaunchKernelGGL((narrow_kernel<D, 1, 8>), dim3((unsigned)grid), dim3(512), 0, stream, p);
   else
-    hipLaunchKernelGGL((narrow_kernel<D>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    return hipErrorInvalidValue;
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t rows = (int64_t)p.total_q * p.num_q_heads;
-  hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+  if (e != hipSuccess || p.head_aim == 0) return e;
+  if (few)
+    hipLaunchKernelGGL((join_kernel<D, true>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((join_kernel<D, false>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
 }  // namespace attn
 
-hipError_t launch_attention(const AttnParams& p, int head_dim, bool wide, hipStream_t stream) {
-  if (head_dim == 64) return attn::launch<64>(p, wide, stream);
-  if (head_dim == 128) return attn::launch<128>(p, wide, stream);
-  if (head_dim == 256) return attn::launch<256>(p, wide, stream);
+hipError_t launch_attention(const AttnParams& p, int head_dim, int form, hipStream_t stream) {
+  if (head_dim == 64) return attn::launch<64>(p, form, stream);
+  if (head_dim == 128) return attn::launch<128>(p, form, stream);
+  if (head_dim == 256) return attn::launch<256>(p, form, stream);
   return hipErrorInvalidValue;
 }
 

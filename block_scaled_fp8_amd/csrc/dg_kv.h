@@ -63,15 +63,34 @@ struct AttnParams {
   FastDiv group;             // query heads per key head
   float scale_log2;          // softmax scale * log2(e)
   int32_t window, sinks;     // window 0: none
-  int32_t q_tiles;           // tiles of query rows per (sequence, key head)
-  int32_t splits;            // parts of the key range, each its own workgroup
-  float* part_o;             // [splits, total_q, heads, head dim] unnormalised sums
-  float* part_ml;            // [splits, total_q, heads, 2] running maximum (log2 units) and sum
+  FastDiv q_tiles;           // tiles of query rows per sequence
+  int32_t tile_rows;         // query rows (token, head of the group) of a tile
+  int32_t items;             // batch * q_tiles
+  int32_t waves;             // of a workgroup of the 16-row kernel: 4 or 8
+  int32_t head_aim;          // cut items so that each key head has about so many parts; 0: one workgroup for each item and key head
+  int32_t least_tiles;       // a part has at least so many key tiles (or all of its item's)
+  int32_t max_cut;           // an item has at most so many parts
+  int32_t most_parts;        // a bound of the number of parts
+  int32_t join_rows;         // a bound of the rows of a tile
+  // workspace (head_aim > 0)
+  float* part_o;             // [most_parts, tile_rows, head dim] parts' unnormalised sums
+  float* part_mz;            // [most_parts, tile_rows, 2] their running maximum (log2 units) and sum of weights
+  int32_t* item_end;         // [items] a head's parts up to and with each item
 };
-hipError_t launch_attention(const AttnParams& p, int head_dim, bool wide, hipStream_t stream);
 
-// Query rows (token, head of the group) of one workgroup's tile.
-inline int attn_wide_rows(int head_dim) { return head_dim == 128 ? 256 : 128; }
-constexpr int kAttnNarrowRows = 32;
+// The kernels: four waves over the same 16 or 32 query rows, or waves of 32 rows each.
+enum AttnForm { ATTN_NARROW_16 = 0, ATTN_NARROW_32 = 1, ATTN_WIDE = 2 };
+inline int attn_tile_rows(int form, int head_dim) {
+  return form == ATTN_NARROW_16 ? 16 : form == ATTN_NARROW_32 ? 32 : head_dim == 128 ? 256 : 128;
+}
+inline int attn_tile_keys(int form, int head_dim) { return form != ATTN_WIDE || head_dim == 256 ? 32 : 64; }
+// workgroups that a compute unit holds at a time
+inline int attn_per_cu(int form, int head_dim) {
+  if (form == ATTN_WIDE) return head_dim == 64 ? 3 : 1;
+  if (head_dim == 256) return 1;
+  if (form == ATTN_NARROW_16) return head_dim == 64 ? 4 : 3;
+  return head_dim == 64 ? 3 : 2;
+}
+hipError_t launch_attention(const AttnParams& p, int head_dim, int form, hipStream_t stream);
 
 }  // namespace dg

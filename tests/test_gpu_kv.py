@@ -218,6 +218,33 @@ def test_attention_in_parts(name, mask):
     check(p, got, *mask)
 
 
+@pytest.mark.parametrize("hint", [0, 1, 40, 1 << 20])
+@pytest.mark.parametrize("name", ["single_tokens", "long"])
+def test_attention_with_a_wrong_bound_of_the_lengths(name, hint):
+    """max_seqlen_k guides the split and nothing else, whatever it says."""
+    lens, news, *shape = CASES[name]
+    p = kv_gen.problem(lens, news, *shape, seed=12)
+    say("attention, bound", name, hint)
+    for sms in (0, 3, 1 << 14):
+        with num_sms(sms):
+            got = run(p, max_seqlen_k=hint)
+        check(p, got)
+
+
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_attention_of_many_sequences(new):
+    """More items than the lanes that look them up, empty sequences among them, whole and in parts."""
+    rng = np.random.default_rng(new)
+    lens = [int(x) for x in rng.integers(0, 400, 75)]
+    lens[0] = lens[64] = lens[74] = 0
+    p = kv_gen.problem(lens, [new if i % 7 else 0 for i in range(75)], 8, 2, 64, 16, seed=new)
+    say("attention, many sequences", new)
+    for sms in (0, 1 << 12):
+        with num_sms(sms):
+            check(p, run(p))
+            check(p, run(p, 50, 3), 50, 3)
+
+
 def test_attention_scale_and_large_scores():
     """Scores of hundreds: the running maximum moves far, weights underflow."""
     p = kv_gen.problem([200, 77], [70, 1], 4, 2, 128, 16, seed=9)
