@@ -375,3 +375,31 @@ def test_write_then_attend_matches_unquantised_attention():
     rel = float((out.double().cpu() - want).norm() / want.norm())
     # E4M3 rounds values by up to 2^-4; errors of different keys average out
     assert rel < 2.0 ** -4, rel
+
+
+@pytest.mark.parametrize("mask", [(0, 0), (50, 4)])
+def test_attention_layer_example(mask):
+    """The library's parts together as a serving layer uses them.  Chunks and single tokens differ from one chunk by
+    the rounding of the attention's output to BF16 (2^-8) and of that to E4M3 (2^-4), where a last bit may flip."""
+    from examples import attention_layer
+    say("attention layer", mask)
+    off, moved = attention_layer.main(*mask)
+    assert moved and off < 2.0 ** -6
+
+
+def test_quantised_values_survive_being_written_again():
+    """Reading back and writing again gives the same values, whatever the scales: E4M3 values times a power of two.
+    (The row of FP32's largest number is rounded up to 2^128, which FP32 does not have: it reads as infinity.)"""
+    rng = np.random.default_rng(3)
+    x = tricky_rows(rng, 30, 2, 128)
+    k_cache, v_cache = dg.fp8_kv_cache_empty(4, 2, 16, 128, device=DEV)
+    slots = torch.arange(30, device=DEV)
+    dg.fp8_kv_cache_write(cuda(x), cuda(x[::-1]), k_cache, v_cache, slots)
+    first = dg.fp8_kv_cache_read(k_cache, v_cache, slots, out_dtype=torch.float32)
+    dg.fp8_kv_cache_write(*first, k_cache, v_cache, slots + 30)
+    again = dg.fp8_kv_cache_read(k_cache, v_cache, slots + 30, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    for a, b in zip(first, again):
+        fine = torch.isfinite(a).all(-1)
+        assert int((~fine).sum()) == 1
+        assert same(a[fine].cpu().numpy(), b[fine].cpu().numpy())
