@@ -108,12 +108,10 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
 }
 
-// KEYS: keys of a tile.  SAME: the item is the same for all lanes.  Returns the item's weight: its key tiles, one where its rows see no key (they
-// are still to be written), 0 without rows.
-template <int KEYS, bool SAME>
-__device__ __forceinline__ int describe(const AttnParams& p, int item, Work& w) {
+// The item's rows.  SAME: the item is the same for all lanes.  Returns the sequence's queries.
+template <bool SAME>
+__device__ __forceinline__ int item_rows(const AttnParams& p, int item, Work& w) {
   w.seq = p.q_tiles.d == 1 ? item : div(item, p.q_tiles);
-  const int qt = p.q_tiles.d == 1 ? 0 : item - w.seq * p.q_tiles.d;
   int n;
   if (p.cu_q) {
     int a = p.cu_q[w.seq], b = p.cu_q[w.seq + 1];
@@ -124,11 +122,19 @@ __device__ __forceinline__ int describe(const AttnParams& p, int item, Work& w) 
     w.q_first = w.seq * p.q_per_seq;
     n = p.q_per_seq;
   }
+  w.rows = n * p.group.d;
+  w.row0 = (item - w.seq * p.q_tiles.d) * p.tile_rows;
+  return n;
+}
+
+// And the keys they see, in tiles of KEYS.  Returns the item's weight: its key tiles, one where its rows see no
+// key (they are still to be written), 0 without rows.
+template <int KEYS, bool SAME>
+__device__ __forceinline__ int describe(const AttnParams& p, int item, Work& w) {
+  const int n = item_rows<SAME>(p, item, w);
   int ctx = p.seq_lens[w.seq];
   if (SAME) ctx = uniform(ctx);
   ctx = min(max(ctx, 0), p.table_cols * p.c.page.d);
-  w.rows = n * p.group.d;
-  w.row0 = qt * p.tile_rows;
   w.place0 = ctx - n;
   const int first = w.place0 + div(w.row0, p.group);
   const int last = w.place0 + div(max(min(w.row0 + p.tile_rows, w.rows) - 1, 0), p.group);
@@ -138,6 +144,20 @@ __device__ __forceinline__ int describe(const AttnParams& p, int item, Work& w) 
   w.sink_tiles = min((min(p.sinks, w.key_end) + KEYS - 1) / KEYS, w.first_tile);
   w.tiles = w.key_end > 0 ? w.sink_tiles + (w.key_end + KEYS - 1) / KEYS - w.first_tile : 0;
   return w.row0 < w.rows ? max(w.tiles, 1) : 0;
+}
+
+// Lane l's item for the whole wave.
+__device__ __forceinline__ void take_from_lane(Work& w, int l) {
+  w.seq = __builtin_amdgcn_readlane(w.seq, l);
+  w.q_first = __builtin_amdgcn_readlane(w.q_first, l);
+  w.row0 = __builtin_amdgcn_readlane(w.row0, l);
+  w.rows = __builtin_amdgcn_readlane(w.rows, l);
+  w.place0 = __builtin_amdgcn_readlane(w.place0, l);
+  w.key_end = __builtin_amdgcn_readlane(w.key_end, l);
+  w.key_from = __builtin_amdgcn_readlane(w.key_from, l);
+  w.first_tile = __builtin_amdgcn_readlane(w.first_tile, l);
+  w.sink_tiles = __builtin_amdgcn_readlane(w.sink_tiles, l);
+  w.tiles = __builtin_amdgcn_readlane(w.tiles, l);
 }
 
 // Sum over the lanes up to and with one's own.
@@ -160,38 +180,83 @@ __device__ __forceinline__ int scan(int x) {
 // n = head_aim, an item is cut into t_i / s parts, to the nearest, with s = max(least_tiles, ceil(T / n)), raised to a
 // multiple of four (the few-rows kernel's waves), so there are at most n + items of them.
 // The host's bound of the lengths, which may be wrong, enters as max_cut, the most parts of an item, alone.
+// Without cuts, the items of several sequences are dealt to the workgroups heaviest first, up to this many
+// (each workgroup finds its item by itself, 64 to a lane's register): the chunks of 5 sequences, 1 to 1537
+// queries after 0 to 4001 keys, take 165 us, 183 us in order of rows.  One sequence's are in order as they
+// are; finding the item costs 1.2 us.
+constexpr int MAX_SORTED = 256;
+
 struct Cut {
   unsigned size, max_cut;
   __device__ __forceinline__ int parts(int weight) const { return weight ? (int)min(max(((unsigned)weight + size / 2) / size, 1u), max_cut) : 0; }
 };
 
-// The workgroup's piece of work; false if there is none.
+// The item of rank `rank` by weight, the heaviest first and equals in their order; false past the last with rows.
 template <int KEYS>
+__device__ __forceinline__ bool item_by_weight(const AttnParams& p, int rank, Work& w) {
+  constexpr int MOST = MAX_SORTED / 64;
+  const int lane = threadIdx.x & 63;
+  int weights[MOST];
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) weights[k] = 64 * k + lane < p.items ? min(describe<KEYS, false>(p, 64 * k + lane, w), 1 << 20) : 0;
+  // the largest threshold that more than `rank` items reach, bit by bit, and how many are above it
+  int t = 0;
+  for (int bit = 1 << 20; bit; bit >>= 1) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) n += __builtin_popcountll(__ballot(weights[k] >= (t | bit)));
+    if (n > rank) t |= bit;
+  }
+  if (t == 0) return false;
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) rank -= __builtin_popcountll(__ballot(weights[k] > t));
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    uint64_t same = __ballot(weights[k] == t);
+    const int n = __builtin_popcountll(same);
+    if (rank < n) {
+      for (; rank; --rank) same &= same - 1;
+      describe<KEYS, true>(p, 64 * k + __builtin_ctzll(same), w);
+      return true;
+    }
+    rank -= n;
+  }
+  return false;
+}
+
+// The workgroup's piece of work; false if there is none.  SORT: without cuts, items go out by weight.
+template <int KEYS, bool SORT>
 __device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
   if (p.head_aim == 0) {
     // One workgroup for each item and key head.  Workgroups are dealt to the eight XCDs in turn: with the
-    // (sequence, key head) pair as the fastest index, and a multiple of eight pairs, those of a pair land on
-    // one XCD and share its L2, and the pairs of a sequence spread over the XCDs.  Later rows see more
-    // keys: they start first.
-    const int pairs = p.batch * p.c.num_heads, pair = blockIdx.x % pairs;
-    w.kv_head = pair % p.c.num_heads;
-    if (!describe<KEYS, true>(p, pair / p.c.num_heads * p.q_tiles.d + p.q_tiles.d - 1 - blockIdx.x / pairs, w)) return false;
+    // key head as the fastest index, and a multiple of eight heads, those of a (sequence, key head) pair
+    // land on one XCD and share its L2.
+    const int kv_head = blockIdx.x % p.c.num_heads, rank = blockIdx.x / p.c.num_heads;
+    if (SORT && p.batch > 1 && p.items <= MAX_SORTED) {
+      if (!item_by_weight<KEYS>(p, rank, w)) return false;
+    } else {
+      // a sequence's later rows, which see more keys, first
+      const int seq = rank % p.batch, item = seq * p.q_tiles.d + p.q_tiles.d - 1 - rank / p.batch;
+      if (!describe<KEYS, true>(p, item, w)) return false;
+    }
+    w.kv_head = kv_head;
     w.t0 = 0;
     w.t1 = w.tiles;
     w.slot = -1;
     return true;
   }
   const int lane = threadIdx.x & 63;
-  auto weight = [&](int item) { return item < p.items ? min(describe<KEYS, false>(p, item, w), 1 << 20) : 0; };
-  const int mine = weight(lane);  // (kept for the search among the first 64 items)
+  auto weight = [&](int item, Work& x) { return item < p.items ? min(describe<KEYS, false>(p, item, x), 1 << 20) : 0; };
+  Work other;
+  const int mine = weight(lane, w);  // (the first 64 items stay in the lanes)
   int per_head = __builtin_amdgcn_readlane(scan(mine), 63);
-  for (int base = 64; base < p.items; base += 64) per_head += __builtin_amdgcn_readlane(scan(weight(base + lane)), 63);
+  for (int base = 64; base < p.items; base += 64) per_head += __builtin_amdgcn_readlane(scan(weight(base + lane, other)), 63);
   if (per_head == 0) return false;
   const Cut cut{(max((unsigned)p.least_tiles, ((unsigned)per_head + p.head_aim - 1) / (unsigned)p.head_aim) + 3) & ~3u, (unsigned)p.max_cut};
   int sums = scan(cut.parts(mine)), all = __builtin_amdgcn_readlane(sums, 63);
   if (blockIdx.x == 0 && threadIdx.x < 64 && lane < p.items) p.item_end[lane] = sums;
   for (int base = 64; base < p.items; base += 64) {
-    const int x = scan(cut.parts(weight(base + lane)));
+    const int x = scan(cut.parts(weight(base + lane, other)));
     if (blockIdx.x == 0 && threadIdx.x < 64 && base + lane < p.items) p.item_end[base + lane] = all + x;
     all += __builtin_amdgcn_readlane(x, 63);
   }
@@ -201,19 +266,23 @@ __device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
   const int per = nb >> 3, extra = nb & 7, xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
   const int id = xcd < extra ? xcd * (per + 1) + idx : extra * (per + 1) + (xcd - extra) * per + idx;
   const int kv_head = uniform((int)((unsigned)id / (unsigned)all));
-  int want = id - kv_head * all, item = 0;
+  int want = id - kv_head * all, n = 0;
   for (int base = 0;; base += 64) {
-    if (base) sums = scan(cut.parts(weight(base + lane)));
+    int parts = 0;
+    if (base) {
+      parts = cut.parts(weight(base + lane, w));
+      sums = scan(parts);
+    }
     const uint64_t later = __ballot(sums > want);
     if (later) {
-      const int l = __builtin_ctzll(later);
-      item = base + l;
-      want -= l ? __builtin_amdgcn_readlane(sums, l - 1) : 0;
+      const int l = __builtin_ctzll(later), before = l ? __builtin_amdgcn_readlane(sums, l - 1) : 0;
+      n = __builtin_amdgcn_readlane(sums, l) - before;
+      want -= before;
+      take_from_lane(w, l);
       break;
     }
     want -= __builtin_amdgcn_readlane(sums, 63);
   }
-  const int n = uniform(cut.parts(min(describe<KEYS, true>(p, item, w), 1 << 20)));
   const int share = uniform((int)((unsigned)w.tiles / (unsigned)n)), more = w.tiles - share * n;
   w.kv_head = kv_head;
   w.t0 = want * share + min(want, more);
@@ -407,17 +476,22 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, co
 //
 // D = 128: eight waves, two on each SIMD, and the two halves of the workgroup take turns: while waves
 // 0-3 are in the matrix phase of a tile (O^T += V^T P^T of the tile before, S^T of this one), waves 4-7
-// are in the vector phase (the softmax) of theirs, half a tile behind, with a barrier after each phase.
-// Measured on 2048 queries (32 heads, 8 key heads) over 8192 keys: 236 us; 269 us without turns; 300 us
-// with turns but LDS reads one matrix instruction ahead instead of four.  D = 64 is bound by the vector
-// unit, which a single half cannot fill: four waves without turns and three such workgroups a CU
-// (61 us on 2 x 2048 queries in a window of 1024; with turns 74, eight waves without 70).  D = 256
-// fills the registers with one wave a SIMD.
+// are in the vector phase (the softmax) of theirs, half a tile behind.  One barrier a tile keeps them
+// there: waves 0-3 come to it between their matrix phase of tile i and their vector phase, waves 4-7
+// when their vector phase of tile i - 1 has ended.  So between two barriers, i and i + 1, waves 0-3 are
+// in vector phase i and matrix phase i + 1, waves 4-7 in matrix phase i and vector phase i; a barrier
+// after each phase measured 1% more.  When chosen, on 2048 queries (32 heads, 8 key heads) over 8192 keys:
+// 236 us with turns, 269 without, 300 with turns but LDS reads one matrix instruction ahead instead of
+// four.  D = 64 is bound by the vector unit, which a single half cannot fill: four waves without turns
+// and three such workgroups a CU (61 us on 2 x 2048 queries in a window of 1024; with turns 74, eight
+// waves without 70).  D = 256 fills the registers with one wave a SIMD.
 //
 // Tiles lie widened in LDS.  With turns, in rings of three: stage i brings K of tile i + 2 and V of tile
 // i + 1; a wave issues its loads at the end of its matrix phase of tile i, when its LDS reads are out
-// (255 us when issued before them), and widens and stores them at the end of the vector phase, to slots
-// last read in the matrix phases of tile i - 1.  Without turns, two slots, loads a whole tile ahead.
+// (255 us when issued before them), and widens and stores them at the end of the vector phase: K to the
+// slot of tile i - 1, V to that of tile i + 1.  Between the barriers around it, K of tiles i and i + 1 and
+// V of tiles i - 1 and i are read: other slots of the three.  Without turns, two slots, loads a whole tile
+// ahead.
 // A load unit is GR rows of K or of V (one 16-byte load a lane), dealt to the waves; where GR divides
 // the page size and every row of a unit is seen, its address is scalar arithmetic on a page number out
 // of 64 that the lanes hold, else it is found lane by lane.
@@ -428,10 +502,11 @@ struct Wide {
   static constexpr int ROWS_ALL = NW * ROWS, THREADS = NW * 64, TILE = KEYS * D * 2;  // TILE: bytes of a widened K or V tile
 };
 
-// The end of a phase; no instruction is moved from one phase to another.
-__device__ __forceinline__ void phase_end() {
+// The end of a phase, with a barrier for those whose turn ends there; no instruction is moved from one
+// phase to another.
+__device__ __forceinline__ void phase_end(bool wait) {
   __builtin_amdgcn_sched_barrier(0);
-  __syncthreads();
+  if (wait) __syncthreads();
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -442,7 +517,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][Wide<D>::TURNS ? 3 : 2][TILE];  // [K, V][slot]
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   Work w;
-  if (!get_work<KEYS>(p, w)) return;
+  if (!get_work<KEYS, true>(p, w)) return;
   const Row row = get_row(p, w, w.row0 + wave * ROWS + (lane & 31));
   // the places of this wave's rows, for whole-tile decisions
   const int wr0 = w.row0 + wave * ROWS;
@@ -493,34 +568,38 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
   constexpr int NK = NU > 1 ? NU / 2 : 1;
   const bool only_v = NU == 1 && wave >= GROUPS;
   At at[NK];
-  v4u raw[NU];      // a stage's codes
-  uint32_t sf[NU];  // and their rows' scale codes
-  auto fetch = [&](int i) {
+  struct Stage {
+    v4u raw[NU];      // codes
+    uint32_t sf[NU];  // and their rows' scale codes
+  };
+  Stage ahead;
+  auto fetch = [&](Stage& to, int i) {
     // (tiles past the list repeat its ends and are not read)
     const int key0 = w.tile_key(min(max(TURNS && only_v ? i + 1 : i + 2, w.t0), w.t1 - 1), KEYS);
     auto get_v = [&](int n) {
-      raw[NU - NK + n] = *(const v4u*)(p.c.v + at[n].code);
-      sf[NU - NK + n] = p.c.v_sf[at[n].sf];
+      to.raw[NU - NK + n] = *(const v4u*)(p.c.v + at[n].code);
+      to.sf[NU - NK + n] = p.c.v_sf[at[n].sf];
     };
 #pragma unroll
     for (int n = 0; n < NK; ++n) {
       if (NU > 1 && TURNS) get_v(n);
       at[n] = place_rows(key0 + (wave + n * NW) % GROUPS * GR);
       if (NU > 1 && !TURNS) get_v(n);
-      raw[n] = *(const v4u*)((only_v ? p.c.v : p.c.k) + at[n].code);
-      sf[n] = (only_v ? p.c.v_sf : p.c.k_sf)[at[n].sf];
+      to.raw[n] = *(const v4u*)((only_v ? p.c.v : p.c.k) + at[n].code);
+      to.sf[n] = (only_v ? p.c.v_sf : p.c.k_sf)[at[n].sf];
     }
   };
-  auto put = [&](uint8_t* k, uint8_t* v) {
+  auto put = [&](const Stage& from, uint8_t* k, uint8_t* v) {
 #pragma unroll
     for (int n = 0; n < NU; ++n) {
       const bool is_v = NU > 1 ? n >= NK : only_v;
       const int rr = (wave + n * NW) % GROUPS * GR + r;
       uint8_t* dst = (is_v ? v : k) + rr * 2 * D;
       const int c0 = is_v ? v_chunk<D>(rr, 2 * c) : k_chunk<D>(rr, 2 * c), c1 = is_v ? v_chunk<D>(rr, 2 * c + 1) : k_chunk<D>(rr, 2 * c + 1);
-      const float s = __uint_as_float(sf[n] << 23);
-      *(v4u*)(dst + c0 * 16) = widen8(raw[n].x, raw[n].y, s);
-      *(v4u*)(dst + c1 * 16) = widen8(raw[n].z, raw[n].w, s);
+      const v4u x = from.raw[n];
+      const float s = __uint_as_float(from.sf[n] << 23);
+      *(v4u*)(dst + c0 * 16) = widen8(x.x, x.y, s);
+      *(v4u*)(dst + c1 * 16) = widen8(x.z, x.w, s);
     }
   };
 
@@ -569,16 +648,16 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
     }
     __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
     __builtin_amdgcn_sched_barrier(0);
-    fetch(i);
-    phase_end();
+    fetch(ahead, i);
+    phase_end(wave < 4);
     weights(i, s);
     // (the weights are wanted here: left to itself, the compiler computes some in the next phase)
 #pragma unroll
     for (int b = 0; b < NB; ++b) asm volatile("" : "+v"(wt[b][0]), "+v"(wt[b][1]));
     asm volatile("" : "+v"(st.z));
     __builtin_amdgcn_sched_barrier(0);
-    put(lds[0][LAST], lds[1][NEXT]);
-    phase_end();
+    put(ahead, lds[0][LAST], lds[1][NEXT]);
+    phase_end(wave >= 4 && i + 1 < w.t1);
   };
   // Without turns: tile i with K and V in slot X; leaves tile i + 1 in the other slot and tile i + 2 on its way.
   auto plain_step = [&](int i, auto slot) {
@@ -596,7 +675,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
     weights(i, s);
     __builtin_amdgcn_sched_barrier(0);
     product_v<D, NB>(st, wt, lds[1][X], lane);
-    put(lds[0][1 - X], lds[1][1 - X]);
+    put(ahead, lds[0][1 - X], lds[1][1 - X]);
     __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 1);
 #pragma unroll
     for (int x = 0; x < D / 16 * NB - AHEAD; ++x) {
@@ -605,17 +684,18 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
     }
     __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 1);
     __builtin_amdgcn_sched_barrier(0);
-    fetch(i);
+    fetch(ahead, i);
     __syncthreads();
   };
   if (w.t0 < w.t1) {
 #pragma unroll
     for (int n = 0; n < NK; ++n) at[n] = place_rows(w.tile_key(w.t0, KEYS) + (wave + n * NW) % GROUPS * GR);
-    fetch(w.t0 - 2);
+    Stage first;
+    fetch(first, w.t0 - 2);
+    fetch(ahead, w.t0 - 1);
     if constexpr (TURNS) {
-      put(lds[0][0], lds[1][2]);
-      fetch(w.t0 - 1);
-      put(lds[0][1], lds[1][0]);
+      put(first, lds[0][0], lds[1][2]);
+      put(ahead, lds[0][1], lds[1][0]);
       __syncthreads();
       if (wave >= 4) __syncthreads();
       int last = 0;  // slot of the last tile
@@ -631,10 +711,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
         if (i + 3 == w.t1) break;
       }
       product_v<D, NB>(st, wt, lds[1][last], lane);
-      if (wave < 4) __syncthreads();
     } else {
-      put(lds[0][0], lds[1][0]);
-      fetch(w.t0 - 1);
+      put(first, lds[0][0], lds[1][0]);
       __syncthreads();
       for (int i = w.t0; i < w.t1; i += 2) {
         plain_step(i, Int<0>{});
@@ -695,7 +773,7 @@ __global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const
   const uint32_t v_step = (uint32_t)(PASS * p.c.token_stride), v_sf_step = (uint32_t)(PASS * p.c.sf_token_stride);
 
   Work w;
-  if (!get_work<KEYS>(p, w)) return;
+  if (!get_work<KEYS, false>(p, w)) return;
   Row row[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) row[b] = get_row(p, w, w.row0 + 16 * b + col);
@@ -981,8 +1059,9 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
   const int all = p.item_end[p.items - 1], end = p.item_end[item], from = item ? p.item_end[item - 1] : 0, n = end - from;
   if (n <= 1) return;  // no rows, or written as a whole
   Work w;
-  describe<32, true>(p, item, w);
+  item_rows<true>(p, item, w);
   w.kv_head = kv_head;
+  w.place0 = 0;  // (places do not matter here)
   const Row row = get_row(p, w, w.row0 + part_row);
   const int64_t at = (int64_t)(kv_head * all + from) * p.tile_rows + part_row;
   const v2f* mz = (const v2f*)p.part_mz + at;
