@@ -112,7 +112,7 @@ int check_shape(const AttnShape& a, int32_t num_kv_heads) {
 }
 
 struct AttnPlan {
-  int form = 0, q_tiles = 1, head_aim = 0, least_tiles = 1, max_cut = 1, join_rows = 1, waves = 4;
+  int form = 0, q_tiles = 1, head_aim = 0, least_tiles = 1, max_cut = 1, join_rows = 1, join_steps = 1, waves = 4;
   int64_t items = 0, most_parts = 0;
 };
 
@@ -134,23 +134,32 @@ AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int
     if (seen < tiles) tiles = seen;
   }
   // Cutting items along the keys costs a second kernel and the parts' way through memory.  It is for items
-  // that are too few for the chip; where they would fill half of it, only for long ones, whose lengths
-  // it also evens out.  128 sequences in a window of 1024 (512 items of 35 tiles for 768 places): 32 us whole,
-  // 52 cut; 64 sequences of up to 8192 keys (512 items of up to 256 tiles): 128 whole, 123 cut.  For many
-  // rows a part's sums weigh more: 1024 queries over 4024 keys (128 items for 256 places) 104 us whole, 81
-  // cut; 2048 over 8192 (256 items) 250 whole, 255 cut.
-  const int64_t slots = int64_t(num_sms) * dg::attn_per_cu(pl.form, head_dim), work = pl.items * num_kv_heads;
-  const bool few = pl.form == dg::ATTN_WIDE ? work < slots : 2 * work <= slots || (work < 2 * slots && tiles >= 128);
+  // that fill at most half of the chip, and for longer ones (whose lengths it also evens out) up to twice it.
+  // Few rows: 128 sequences in a window of 1024 (512 items of 35 tiles for 768 places) 32 us whole, 52 cut;
+  // 64 sequences of up to 8192 keys (512 items of up to 256 tiles) 128 whole, 123 cut.  Many rows, one
+  // sequence: 1024 queries over 4024 keys (128 items for 256 places) 104 whole, 78 cut; 1280 over 7424 (160
+  // items) 182 whole, 209 cut, with 64 values a head 2048 over 8192 (512 items for 768 places) 167 whole,
+  // 180 cut.  Several sequences: 3 x 500 queries after 1000 to 7000 keys 185 whole, 131 cut; 6 x 256 after
+  // 4000 each 117 whole, 118 cut; 12 x 64 to 400 after 100 to 2000 72 whole, 78 cut.
+  const int64_t with_rows = int64_t(a.total_q) * group / tile + a.batch;  // of the items, at most
+  const int64_t work = (with_rows < pl.items ? with_rows : pl.items) * num_kv_heads;
+  const int64_t slots = int64_t(num_sms) * dg::attn_per_cu(pl.form, head_dim);
+  const bool wide = pl.form == dg::ATTN_WIDE, fills_half = 2 * work <= slots;
+  const bool few = fills_half || (work < 2 * slots && (wide ? a.batch > 1 && tiles >= 64 : tiles >= 128));
   pl.least_tiles = 4;
   // Short contexts of few items: eight waves instead of the second kernel, whose launch costs the host more
   // than it saves the device (1001 keys of 8 key heads: 11.6 against 9.1 us on the device, 8.5 against 12.9 on
   // the host; 2000 keys: 17.1 against 9.9).  (At 256 values a head eight waves run out of registers.)
   if (pl.form == dg::ATTN_NARROW_16 && head_dim != 256 && work <= num_sms && tiles > pl.least_tiles && tiles <= 40)
     pl.waves = 8;
-  else if (few && pl.items <= 1024 && tiles > pl.least_tiles) {
+  else if (few && pl.items <= (wide ? dg::MAX_SORTED : 1024) && tiles > pl.least_tiles) {
     pl.head_aim = int(slots < num_kv_heads ? 1 : slots / num_kv_heads);
+    // One row after the other where most items may not be cut (12 x 64 to 400 queries 84 -> 78 us); where
+    // few items have many parts, as many workgroups as rows give (128 queries over 8128 keys 43 us, with two
+    // rows 52).
+    pl.join_steps = fills_half ? 1 : 2;
     pl.max_cut = int((tiles + pl.least_tiles - 1) / pl.least_tiles);
-    const int64_t by_aim = int64_t(pl.head_aim) * num_kv_heads + work, by_cut = work * pl.max_cut;
+    const int64_t by_aim = (int64_t(pl.head_aim) + pl.items) * num_kv_heads, by_cut = pl.items * num_kv_heads * pl.max_cut;
     pl.most_parts = by_aim < by_cut ? by_aim : by_cut;
   }
   return pl;
@@ -250,6 +259,7 @@ int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t 
   p.head_aim = pl.head_aim;
   p.max_cut = pl.max_cut;
   p.join_rows = pl.join_rows;
+  p.join_steps = pl.join_steps;
   p.most_parts = int(pl.most_parts);
   p.least_tiles = pl.least_tiles;
   p.part_o = static_cast<float*>(workspace);

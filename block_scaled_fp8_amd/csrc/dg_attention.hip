@@ -171,6 +171,17 @@ __device__ __forceinline__ int scan(int x) {
   return x;
 }
 
+// The largest of the lanes' values, none negative.
+__device__ __forceinline__ int most(int x) {
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
 // How the work is dealt where items are cut: into parts of about as many key tiles, a number that follows
 // from the lengths, and so is known to the device only.  A head's parts are numbered item after item, and
 // heads follow each other.  A part of an item that is not cut writes the item; else it leaves its sums
@@ -180,66 +191,102 @@ __device__ __forceinline__ int scan(int x) {
 // n = head_aim, an item is cut into t_i / s parts, to the nearest, with s = max(least_tiles, ceil(T / n)), raised to a
 // multiple of four (the few-rows kernel's waves), so there are at most n + items of them.
 // The host's bound of the lengths, which may be wrong, enters as max_cut, the most parts of an item, alone.
-// Without cuts, the items of several sequences are dealt to the workgroups heaviest first, up to this many
-// (each workgroup finds its item by itself, 64 to a lane's register): the chunks of 5 sequences, 1 to 1537
-// queries after 0 to 4001 keys, take 165 us, 183 us in order of rows.  One sequence's are in order as they
-// are; finding the item costs 1.2 us.
-constexpr int MAX_SORTED = 256;
-
+//
+// The many-rows kernel's workgroups take the pieces largest first, whole items of several sequences
+// too: the chunks of 5 sequences, 1 to 1537 queries after 0 to 4001 keys, 159 us (183 in order of rows); 4
+// sequences, 1 to 900 queries after 0 to 4000 keys, cut, 80 us (91 in order of parts; 112 whole).  Each finds
+// its piece by itself, in 1 to 2 us.  One sequence's whole items are in order as they are.
 struct Cut {
   unsigned size, max_cut;
   __device__ __forceinline__ int parts(int weight) const { return weight ? (int)min(max(((unsigned)weight + size / 2) / size, 1u), max_cut) : 0; }
 };
 
-// The item of rank `rank` by weight, the heaviest first and equals in their order; false past the last with rows.
+__device__ __forceinline__ Cut cut_for(const AttnParams& p, int per_head) {
+  return {(max((unsigned)p.least_tiles, ((unsigned)per_head + p.head_aim - 1) / (unsigned)p.head_aim) + 3) & ~3u, (unsigned)p.max_cut};
+}
+
+// Part x of n: as many key tiles as the others, or one more.
+__device__ __forceinline__ void take_part(Work& w, int x, int n) {
+  const int share = uniform((int)((unsigned)w.tiles / (unsigned)n)), more = w.tiles - share * n;
+  w.t0 = x * share + min(x, more);
+  w.t1 = w.t0 + share + (x < more ? 1 : 0);
+}
+
+// Piece number `rank` of a key head's, the largest first and equals in their order; false past the last.  For
+// up to MAX_SORTED items, 64 to a register.
 template <int KEYS>
-__device__ __forceinline__ bool item_by_weight(const AttnParams& p, int rank, Work& w) {
+__device__ __forceinline__ bool piece_by_size(const AttnParams& p, int kv_head, int rank, Work& w) {
   constexpr int MOST = MAX_SORTED / 64;
   const int lane = threadIdx.x & 63;
-  int weights[MOST];
-#pragma unroll
-  for (int k = 0; k < MOST; ++k) weights[k] = 64 * k + lane < p.items ? min(describe<KEYS, false>(p, 64 * k + lane, w), 1 << 20) : 0;
-  // the largest threshold that more than `rank` items reach, bit by bit, and how many are above it
-  int t = 0;
-  for (int bit = 1 << 20; bit; bit >>= 1) {
-    int n = 0;
-#pragma unroll
-    for (int k = 0; k < MOST; ++k) n += __builtin_popcountll(__ballot(weights[k] >= (t | bit)));
-    if (n > rank) t |= bit;
-  }
-  if (t == 0) return false;
-#pragma unroll
-  for (int k = 0; k < MOST; ++k) rank -= __builtin_popcountll(__ballot(weights[k] > t));
+  int parts[MOST], size[MOST], ends[MOST];  // (parts: weights at first)
+  int per_head = 0, all = 0, largest = 0;
+  Work other;
 #pragma unroll
   for (int k = 0; k < MOST; ++k) {
-    uint64_t same = __ballot(weights[k] == t);
-    const int n = __builtin_popcountll(same);
-    if (rank < n) {
-      for (; rank; --rank) same &= same - 1;
-      describe<KEYS, true>(p, 64 * k + __builtin_ctzll(same), w);
+    parts[k] = 0;
+    if (64 * k + lane < p.items) parts[k] = min(describe<KEYS, false>(p, 64 * k + lane, k ? other : w), 1 << 20);
+    per_head += parts[k];
+  }
+  Cut cut{1, 1};
+  if (p.head_aim) cut = cut_for(p, __builtin_amdgcn_readlane(scan(per_head), 63));
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    size[k] = parts[k];
+    if (64 * k >= p.items) continue;
+    parts[k] = cut.parts(size[k]);
+    if (p.head_aim) {
+      if (size[k]) size[k] = (size[k] + parts[k] - 1) / (unsigned)parts[k];
+      ends[k] = all + scan(parts[k]);
+      all = __builtin_amdgcn_readlane(ends[k], 63);
+      if (blockIdx.x == 0 && threadIdx.x < 64 && 64 * k + lane < p.items) p.item_end[64 * k + lane] = ends[k];
+    }
+    largest = max(largest, size[k]);
+  }
+  auto count = [&](auto among) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) n += among(size[k]) ? parts[k] : 0;
+    return __builtin_amdgcn_readlane(scan(n), 63);
+  };
+  // the largest threshold that more than `rank` pieces reach, bit by bit
+  int t = 0;
+  for (int bit = 1 << (31 - __builtin_clz(most(largest) | 1)); bit; bit >>= 1)
+    if (count([&](int x) { return x >= (t | bit); }) > rank) t |= bit;
+  if (t == 0) return false;
+  rank -= count([&](int x) { return x > t; });
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    if (64 * k >= p.items) return false;
+    const int x = scan(size[k] == t ? parts[k] : 0);
+    const uint64_t later = __ballot(x > rank);
+    if (later) {
+      const int l = __builtin_ctzll(later), n = __builtin_amdgcn_readlane(parts[k], l);
+      const int part = rank - (__builtin_amdgcn_readlane(x, l) - n);
+      if (k == 0)
+        take_from_lane(w, l);
+      else
+        describe<KEYS, true>(p, 64 * k + l, w);
+      take_part(w, part, n);
+      w.slot = n == 1 ? -1 : kv_head * all + __builtin_amdgcn_readlane(ends[k], l) - n + part;
       return true;
     }
-    rank -= n;
+    rank -= __builtin_amdgcn_readlane(x, 63);
   }
   return false;
 }
 
-// The workgroup's piece of work; false if there is none.  SORT: without cuts, items go out by weight.
-template <int KEYS, bool SORT>
+// The workgroup's piece of work; false if there is none.
+template <int KEYS, bool WIDE>
 __device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
-  if (p.head_aim == 0) {
-    // One workgroup for each item and key head.  Workgroups are dealt to the eight XCDs in turn: with the
-    // key head as the fastest index, and a multiple of eight heads, those of a (sequence, key head) pair
-    // land on one XCD and share its L2.
+  if (WIDE || p.head_aim == 0) {
+    // Workgroups are dealt to the eight XCDs in turn: with the key head as the fastest index, and a multiple
+    // of eight heads, those of a (sequence, key head) pair land on one XCD and share its L2.
     const int kv_head = blockIdx.x % p.c.num_heads, rank = blockIdx.x / p.c.num_heads;
-    if (SORT && p.batch > 1 && p.items <= MAX_SORTED) {
-      if (!item_by_weight<KEYS>(p, rank, w)) return false;
-    } else {
-      // a sequence's later rows, which see more keys, first
-      const int seq = rank % p.batch, item = seq * p.q_tiles.d + p.q_tiles.d - 1 - rank / p.batch;
-      if (!describe<KEYS, true>(p, item, w)) return false;
-    }
     w.kv_head = kv_head;
+    if (WIDE && p.items <= MAX_SORTED && (p.batch > 1 || p.head_aim)) return piece_by_size<KEYS>(p, kv_head, rank, w);
+    // a sequence's later rows, which see more keys, first
+    const int seq = rank % p.batch, item = seq * p.q_tiles.d + p.q_tiles.d - 1 - rank / p.batch;
+    if (!describe<KEYS, true>(p, item, w)) return false;
     w.t0 = 0;
     w.t1 = w.tiles;
     w.slot = -1;
@@ -252,7 +299,7 @@ __device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
   int per_head = __builtin_amdgcn_readlane(scan(mine), 63);
   for (int base = 64; base < p.items; base += 64) per_head += __builtin_amdgcn_readlane(scan(weight(base + lane, other)), 63);
   if (per_head == 0) return false;
-  const Cut cut{(max((unsigned)p.least_tiles, ((unsigned)per_head + p.head_aim - 1) / (unsigned)p.head_aim) + 3) & ~3u, (unsigned)p.max_cut};
+  const Cut cut = cut_for(p, per_head);
   int sums = scan(cut.parts(mine)), all = __builtin_amdgcn_readlane(sums, 63);
   if (blockIdx.x == 0 && threadIdx.x < 64 && lane < p.items) p.item_end[lane] = sums;
   for (int base = 64; base < p.items; base += 64) {
@@ -283,10 +330,8 @@ __device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
     }
     want -= __builtin_amdgcn_readlane(sums, 63);
   }
-  const int share = uniform((int)((unsigned)w.tiles / (unsigned)n)), more = w.tiles - share * n;
+  take_part(w, want, n);
   w.kv_head = kv_head;
-  w.t0 = want * share + min(want, more);
-  w.t1 = w.t0 + share + (want < more ? 1 : 0);
   w.slot = n == 1 ? -1 : id;
   return true;
 }
@@ -1048,13 +1093,21 @@ __global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const
 
 // ---------------------------------------------------------------- joining the parts
 // out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) z_s over the parts s of a row's item.  A row is G groups of
-// D / 4 lanes; group x takes parts x, x + G, ..., and the groups' sums are added in their order.  G = 1
-// where rows are many, 256 threads for a row where they are few and their parts many.
+// D / 4 lanes; group x takes parts x, x + G, ..., and the groups' sums are added in their order.  256
+// threads for a row where rows are few and their parts many.  Where rows are many, G = 1 and a workgroup
+// has STEPS rows for each lane group: most items may not be cut, and their workgroups' starts are what
+// they cost.
+template <int D, bool FEW>
+struct Join {
+  static constexpr int L = D / 4, G = FEW ? 256 / L : 1, PER = 256 / (L * G);  // PER: rows at a time
+};
+
 template <int D, bool FEW>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
-  constexpr int L = D / 4, G = FEW ? 256 / L : 1, PER = 256 / (L * G);  // rows of a workgroup
+  using J = Join<D, FEW>;
+  constexpr int L = J::L, G = J::G;
   const int lanes = threadIdx.x % L, group = threadIdx.x / L % G;
-  const int blocks = (p.join_rows + PER - 1) / PER, part_row = blockIdx.x % blocks * PER + threadIdx.x / (L * G);
+  const int steps = FEW ? 1 : p.join_steps, blocks = (p.join_rows + J::PER * steps - 1) / (J::PER * steps);
   const int id = blockIdx.x / blocks, kv_head = id % p.c.num_heads, item = id / p.c.num_heads;
   const int all = p.item_end[p.items - 1], end = p.item_end[item], from = item ? p.item_end[item - 1] : 0, n = end - from;
   if (n <= 1) return;  // no rows, or written as a whole
@@ -1062,53 +1115,58 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
   item_rows<true>(p, item, w);
   w.kv_head = kv_head;
   w.place0 = 0;  // (places do not matter here)
-  const Row row = get_row(p, w, w.row0 + part_row);
-  const int64_t at = (int64_t)(kv_head * all + from) * p.tile_rows + part_row;
-  const v2f* mz = (const v2f*)p.part_mz + at;
-  const float* part = p.part_o + at * D + 4 * lanes;
   const int64_t step = p.tile_rows;
-  float m = NEG_INF, z = 0.f;
-  v4f o = {0.f, 0.f, 0.f, 0.f};
-  if (row.live) {
-    // (each group by its own running maximum)
-    for (int x = group; x < n; x += G) {
-      const v2f a = mz[x * step];
-      const v4f b = *(const v4f*)(part + x * step * D);
-      if (a.x == NEG_INF) continue;  // a part in which the row sees nothing
-      const float top = fmaxf(m, a.x), f = exp2_hw(m - top), g = exp2_hw(a.x - top);
-      z = z * f + a.y * g;
-      o = o * f + b * g;
-      m = top;
+  for (int y = 0; y < steps; ++y) {
+    const int part_row = (blockIdx.x % blocks * steps + y) * J::PER + threadIdx.x / (L * G);
+    const Row row = get_row(p, w, w.row0 + part_row);
+    const bool live = row.live && part_row < p.tile_rows;
+    const int64_t at = (int64_t)(kv_head * all + from) * p.tile_rows + part_row;
+    const v2f* mz = (const v2f*)p.part_mz + at;
+    const float* part = p.part_o + at * D + 4 * lanes;
+    float m = NEG_INF, z = 0.f;
+    v4f o = {0.f, 0.f, 0.f, 0.f};
+    if (live) {
+      // (each group by its own running maximum)
+      for (int x = group; x < n; x += G) {
+        const v2f a = mz[x * step];
+        const v4f b = *(const v4f*)(part + x * step * D);
+        if (a.x == NEG_INF) continue;  // a part in which the row sees nothing
+        const float top = fmaxf(m, a.x), f = exp2_hw(m - top), g = exp2_hw(a.x - top);
+        z = z * f + a.y * g;
+        o = o * f + b * g;
+        m = top;
+      }
     }
-  }
-  if constexpr (FEW) {
-    __shared__ float sums[G][L][4], tops[G][2];
-    *(v4f*)sums[group][lanes] = o;
-    if (lanes == 0) tops[group][0] = m, tops[group][1] = z;
-    __syncthreads();
-    if (group != 0) return;
+    if constexpr (FEW) {
+      __shared__ float sums[G][L][4], tops[G][2];
+      *(v4f*)sums[group][lanes] = o;
+      if (lanes == 0) tops[group][0] = m, tops[group][1] = z;
+      __syncthreads();
+      if (group != 0) return;
 #pragma unroll
-    for (int x = 0; x < G; ++x) m = fmaxf(m, tops[x][0]);
-    z = 0.f;
-    o = 0.f;
+      for (int x = 0; x < G; ++x) m = fmaxf(m, tops[x][0]);
+      z = 0.f;
+      o = 0.f;
 #pragma unroll
-    for (int x = 0; x < G; ++x) {
-      const float f = tops[x][0] == NEG_INF ? 0.f : exp2_hw(tops[x][0] - m);
-      z += f * tops[x][1];
-      o += f * *(const v4f*)sums[x][lanes];
+      for (int x = 0; x < G; ++x) {
+        const float f = tops[x][0] == NEG_INF ? 0.f : exp2_hw(tops[x][0] - m);
+        z += f * tops[x][1];
+        o += f * *(const v4f*)sums[x][lanes];
+      }
     }
+    if (!live) continue;
+    o *= inverse(z);
+    *(v2u*)(p.out + row.token * p.o_token_stride + row.head * p.o_head_stride + 4 * lanes) = (v2u){pack2(o.x, o.y), pack2(o.z, o.w)};
+    if (p.lse && lanes == 0) p.lse[(int64_t)row.token * p.num_q_heads + row.head] = log_sum(m, z);
   }
-  if (!row.live) return;
-  o *= inverse(z);
-  *(v2u*)(p.out + row.token * p.o_token_stride + row.head * p.o_head_stride + 4 * lanes) = (v2u){pack2(o.x, o.y), pack2(o.z, o.w)};
-  if (p.lse && lanes == 0) p.lse[(int64_t)row.token * p.num_q_heads + row.head] = log_sum(m, z);
 }
 
 template <int D>
 hipError_t launch(const AttnParams& p, int form, hipStream_t stream) {
   const int64_t whole = (int64_t)p.items * p.c.num_heads, grid = p.head_aim ? p.most_parts : whole;
   const bool few = form != ATTN_WIDE;
-  const int64_t blocks = whole * (few ? p.join_rows : (p.join_rows + 1024 / D - 1) / (1024 / D));
+  const int block_rows = few ? Join<D, true>::PER : Join<D, false>::PER * p.join_steps;
+  const int64_t blocks = whole * ((p.join_rows + block_rows - 1) / block_rows);
   if (grid > INT32_MAX || blocks > INT32_MAX) return hipErrorInvalidValue;
   if (form == ATTN_WIDE)
     hipLaunchKernelGGL((wide_kernel<D>), dim3((unsigned)grid), dim3(Wide<D>::THREADS), 0, stream, p);

@@ -72,6 +72,7 @@ struct AttnParams {
   int32_t max_cut;           // an item has at most so many parts
   int32_t most_parts;        // a bound of the number of parts
   int32_t join_rows;         // a bound of the rows of a tile
+  int32_t join_steps;        // rows that a lane group of the many-rows join has one after the other
   // workspace (head_aim > 0)
   float* part_o;             // [most_parts, tile_rows, head dim] parts' unnormalised sums
   float* part_mz;            // [most_parts, tile_rows, 2] their running maximum (log2 units) and sum of weights
@@ -80,6 +81,9 @@ struct AttnParams {
 
 // The kernels: four waves over the same 16 or 32 query rows, or waves of 32 rows each.
 enum AttnForm { ATTN_NARROW_16 = 0, ATTN_NARROW_32 = 1, ATTN_WIDE = 2 };
+// The many-rows kernel deals the pieces of up to so many items by size, and cuts items of such calls only: a
+// lane holds four of them.
+constexpr int MAX_SORTED = 256;
 inline int attn_tile_rows(int form, int head_dim) {
   return form == ATTN_NARROW_16 ? 16 : form == ATTN_NARROW_32 ? 32 : head_dim == 128 ? 256 : 128;
 }

@@ -245,6 +245,25 @@ def test_attention_of_many_sequences(new):
             check(p, run(p, 50, 3), 50, 3)
 
 
+@pytest.mark.parametrize("seqs,sms", [(1, 1), (2, 2), (5, 5), (5, 12), (128, 100), (130, 100)])
+@pytest.mark.parametrize("dim,group,mask", [(64, 4, (0, 0)), (128, 8, (200, 3)), (256, 4, (0, 0))])
+def test_attention_pieces_by_size(dim, group, mask, seqs, sms):
+    """Many rows of unequal sequences: whole and cut items of all sizes in one call, up to as many as are sorted
+    and more; two rows of a lane group in the join (5 compute units for 5 sequences, say)."""
+    rng = np.random.default_rng(seqs)
+    small = seqs > 8
+    lens = [int(x) for x in rng.integers(0, 120 if small else 1500, seqs)]
+    lens[-1] = 130 if small else 2600
+    news = [int(x) for x in rng.integers(0, 4 if small else 90, seqs)]
+    news[seqs // 2] = 256 // group + 3 if dim == 128 else 128 // group + 3
+    p = kv_gen.problem(lens, news, 2 * group, 2, dim, 16, seed=seqs)
+    say("attention, pieces by size", dim, mask, seqs, sms)
+    for most in (None, 1 << 14):
+        with num_sms(sms):
+            got = run(p, *mask) if most is None else run(p, *mask, max_seqlen_k=most)
+        check(p, got, *mask)
+
+
 def test_attention_scale_and_large_scores():
     """Scores of hundreds: the running maximum moves far, weights underflow."""
     p = kv_gen.problem([200, 77], [70, 1], 4, 2, 128, 16, seed=9)
