@@ -108,6 +108,16 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
 }
 
+// The same for a piece of work: its fields come through branches that the compiler cannot tell are taken by
+// all lanes, and the addresses of every tile hang on them.
+__device__ __forceinline__ void make_uniform(Work& w) {
+  w.seq = uniform(w.seq), w.kv_head = uniform(w.kv_head), w.q_first = uniform(w.q_first);
+  w.row0 = uniform(w.row0), w.rows = uniform(w.rows), w.place0 = uniform(w.place0);
+  w.key_end = uniform(w.key_end), w.key_from = uniform(w.key_from);
+  w.sink_tiles = uniform(w.sink_tiles), w.first_tile = uniform(w.first_tile), w.tiles = uniform(w.tiles);
+  w.t0 = uniform(w.t0), w.t1 = uniform(w.t1), w.slot = uniform(w.slot);
+}
+
 // The item's rows.  SAME: the item is the same for all lanes.  Returns the sequence's queries.
 template <bool SAME>
 __device__ __forceinline__ int item_rows(const AttnParams& p, int item, Work& w) {
@@ -563,6 +573,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   Work w;
   if (!get_work<KEYS, true>(p, w)) return;
+  make_uniform(w);
   const Row row = get_row(p, w, w.row0 + wave * ROWS + (lane & 31));
   // the places of this wave's rows, for whole-tile decisions
   const int wr0 = w.row0 + wave * ROWS;
@@ -597,8 +608,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
         entries = (unsigned)entries < (unsigned)p.c.num_pages ? entries : 0;
       }
       const uint32_t pg = __builtin_amdgcn_readlane(entries, col - table_from), off = j0 - col * p.c.page.d;
-      a.code = (int64_t)(pg * (uint64_t)p.c.page_stride + head_at + off * (uint32_t)p.c.token_stride) + lane_at;
-      a.sf = (int64_t)(pg * (uint64_t)p.c.sf_page_stride + head_sf + off * (uint32_t)p.c.sf_token_stride) + lane_sf;
+      a.code = uniform((int64_t)(pg * (uint64_t)p.c.page_stride + head_at + off * (uint32_t)p.c.token_stride)) + lane_at;
+      a.sf = uniform((int64_t)(pg * (uint64_t)p.c.sf_page_stride + head_sf + off * (uint32_t)p.c.sf_token_stride)) + lane_sf;
     } else {
       const int j = key_to_load(w, p.sinks, j0 + r);
       const int col = div(j, p.c.page), off = j - col * p.c.page.d, pg = page_entry(p, table, col);
@@ -819,6 +830,7 @@ __global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const
 
   Work w;
   if (!get_work<KEYS, false>(p, w)) return;
+  make_uniform(w);
   Row row[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) row[b] = get_row(p, w, w.row0 + 16 * b + col);
