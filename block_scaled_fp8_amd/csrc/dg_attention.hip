@@ -467,9 +467,9 @@ __device__ __forceinline__ void softmax(const AttnParams& p, State<D>& st, v16f 
   st.z += z;
 }
 
-// O^T += V^T P^T over NB blocks of 32 keys of the V tile at `v` (LDS bytes).
-template <int D, int NB>
-__device__ __forceinline__ void product_v(State<D>& st, const v8bf (&w)[NB][2], const uint8_t* v, int lane) {
+// O^T += V^T P^T over NB blocks of 32 keys of the V tile at `v` (LDS bytes), for DO values of D from d0 on.
+template <int D, int DO, int NB>
+__device__ __forceinline__ void product_v(State<DO>& st, const v8bf (&w)[NB][2], const uint8_t* v, int d0, int lane) {
   const int r = (lane & 15) >> 2, h = lane >> 5;
   // lane's 8 bytes within a 4-row, 32-byte group: row r, 8-byte piece lane % 4; the second 16
   // lanes of a half wave take the next 32 bytes
@@ -479,8 +479,8 @@ __device__ __forceinline__ void product_v(State<D>& st, const v8bf (&w)[NB][2], 
     for (int u = 0; u < 2; ++u) {
       const int row = 32 * b + 16 * u + 4 * h + r;
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) {
-        const int chunk = v_chunk<D>(row, 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
+      for (int d = 0; d < DO / 32; ++d) {
+        const int chunk = v_chunk<D>(row, d0 / 8 + 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
         const int at = row * 2 * D + chunk * 16 + (lane & 1) * 8;
         const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LDS v4s*)(v + at));
         const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LDS v4s*)(v + at + 8 * 2 * D));
@@ -496,35 +496,35 @@ __device__ __forceinline__ float log_sum(float m, float z) {
 }
 
 // An item's result, or a part's.  Register i of 16-group d is value 32 d + 8 (i / 4) + 4 (lane / 32) + i % 4.
-// z: summed over the half waves.
-template <int D>
-__device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, const Row& row, const v16f (&o)[D / 32],
-                                          float m, float z, int h) {
+// z: summed over the half waves; the DO values of the row from d0 on.
+template <int D, int DO>
+__device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, const Row& row, const v16f (&o)[DO / 32],
+                                          float m, float z, int d0, int h) {
   if (!row.live) return;
   if (w.slot < 0) {
     const float f = inverse(z);
-    uint16_t* dst = p.out + row.token * p.o_token_stride + row.head * p.o_head_stride;
+    uint16_t* dst = p.out + row.token * p.o_token_stride + row.head * p.o_head_stride + d0;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+    for (int d = 0; d < DO / 32; ++d)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *(v2u*)(dst + 32 * d + 8 * j + 4 * h) = (v2u){pack2(o[d][4 * j] * f, o[d][4 * j + 1] * f),
                                                       pack2(o[d][4 * j + 2] * f, o[d][4 * j + 3] * f)};
-    if (p.lse && h == 0) p.lse[(int64_t)row.token * p.num_q_heads + row.head] = log_sum(m, z);
+    if (p.lse && h == 0 && d0 == 0) p.lse[(int64_t)row.token * p.num_q_heads + row.head] = log_sum(m, z);
   } else {
     const int64_t at = (int64_t)w.slot * p.tile_rows + row.r - w.row0;
-    float* dst = p.part_o + at * D;
+    float* dst = p.part_o + at * D + d0;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+    for (int d = 0; d < DO / 32; ++d)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *(v4f*)(dst + 32 * d + 8 * j + 4 * h) = (v4f){o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
-    if (h == 0) *(v2f*)(p.part_mz + 2 * at) = (v2f){m, z};
+    if (h == 0 && d0 == 0) *(v2f*)(p.part_mz + 2 * at) = (v2f){m, z};
   }
 }
 
 // ---------------------------------------------------------------- many rows: chunks of a prompt
-// NW waves of 32 query rows share tiles of KEYS keys.  What bounds it: a wave's tile of 64 keys takes 32
+// NW waves, each with 32 query rows, share tiles of KEYS keys.  What bounds it: a wave's tile of 64 keys takes 32
 // matrix instructions of 32 cycles at D = 128 (1024 cycles; half of that at D = 64) and about as long on
 // the vector unit, where 32 exponentials at a quarter of the rate are half of it.  Both units have to be
 // kept busy by different waves.
@@ -539,7 +539,10 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, co
 // 236 us with turns, 269 without, 300 with turns but LDS reads one matrix instruction ahead instead of
 // four.  D = 64 is bound by the vector unit, which a single half cannot fill: four waves without turns
 // and three such workgroups a CU (61 us on 2 x 2048 queries in a window of 1024; with turns 74, eight
-// waves without 70).  D = 256 fills the registers with one wave a SIMD.
+// waves without 70).  D = 256: a wave with the queries and outputs of 32 rows has no room beside it on its
+// SIMD, and a single one is bound by how fast it issues.  So two waves, one of each half of the workgroup,
+// share 32 rows: both compute their scores and weights, each half of the outputs (1536 queries, 16 heads, 4
+// key heads, over 7680 keys: 314 us; with four waves, each alone with its rows, 405).
 //
 // Tiles lie widened in LDS.  With turns, in rings of three: stage i brings K of tile i + 2 and V of tile
 // i + 1; a wave issues its loads at the end of its matrix phase of tile i, when its LDS reads are out
@@ -547,14 +550,15 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, co
 // slot of tile i - 1, V to that of tile i + 1.  Between the barriers around it, K of tiles i and i + 1 and
 // V of tiles i - 1 and i are read: other slots of the three.  Without turns, two slots, loads a whole tile
 // ahead.
-// A load unit is GR rows of K or of V (one 16-byte load a lane), dealt to the waves; where GR divides
-// the page size and every row of a unit is seen, its address is scalar arithmetic on a page number out
-// of 64 that the lanes hold, else it is found lane by lane.
+// Each wave loads GR rows of K and of V of a stage (one 16-byte load a lane); where GR divides the page
+// size and every one of them is seen, their address is scalar arithmetic on a page number out of 64 that
+// the lanes hold, else it is found lane by lane.
 template <int D>
 struct Wide {
-  static constexpr int NW = D == 128 ? 8 : 4, KEYS = D == 256 ? 32 : 64, NB = KEYS / 32;
-  static constexpr bool TURNS = D == 128;
-  static constexpr int ROWS_ALL = NW * ROWS, THREADS = NW * 64, TILE = KEYS * D * 2;  // TILE: bytes of a widened K or V tile
+  static constexpr int NW = D == 64 ? 4 : 8, KEYS = D == 256 ? 32 : 64, NB = KEYS / 32;
+  static constexpr int SHARE = D == 256 ? 2 : 1, DO = D / SHARE;  // waves that share 32 rows, a wave's values of the output
+  static constexpr bool TURNS = D != 64;
+  static constexpr int THREADS = NW * 64, TILE = KEYS * D * 2;  // TILE: bytes of a widened K or V tile
 };
 
 // The end of a phase, with a barrier for those whose turn ends there; no instruction is moved from one
@@ -566,17 +570,19 @@ __device__ __forceinline__ void phase_end(bool wait) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) wide_kernel(const AttnParams p) {
-  constexpr int NW = Wide<D>::NW, KEYS = Wide<D>::KEYS, NB = Wide<D>::NB, TILE = Wide<D>::TILE;
-  constexpr int CH = D / 16, GR = 64 / CH, GROUPS = KEYS / GR, NU = 2 * GROUPS / NW;
+__global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel(const AttnParams p) {
+  constexpr int NW = Wide<D>::NW, KEYS = Wide<D>::KEYS, NB = Wide<D>::NB, TILE = Wide<D>::TILE, DO = Wide<D>::DO;
+  constexpr int CH = D / 16, GR = 64 / CH;
+  static_assert(KEYS / GR == NW);
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][Wide<D>::TURNS ? 3 : 2][TILE];  // [K, V][slot]
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   Work w;
   if (!get_work<KEYS, true>(p, w)) return;
   make_uniform(w);
-  const Row row = get_row(p, w, w.row0 + wave * ROWS + (lane & 31));
+  const int rows_of = wave % (NW / Wide<D>::SHARE), d0 = wave / (NW / Wide<D>::SHARE) * DO;
+  const Row row = get_row(p, w, w.row0 + rows_of * ROWS + (lane & 31));
   // the places of this wave's rows, for whole-tile decisions
-  const int wr0 = w.row0 + wave * ROWS;
+  const int wr0 = w.row0 + rows_of * ROWS;
   const int place_lo = w.place0 + div(min(wr0, w.rows - 1), p.group);
   const int place_hi = w.place0 + div(min(wr0 + ROWS, w.rows) - 1, p.group);
 
@@ -618,48 +624,38 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
     }
     return a;
   };
-  // With turns, a wave's V rows of a stage are its K rows of the stage before (except where it loads
-  // only one of the two); without, they are of the same tile.
+  // With turns, a wave's V rows of a stage are its K rows of the stage before; without, they are of the same tile.
   constexpr bool TURNS = Wide<D>::TURNS;
-  constexpr int NK = NU > 1 ? NU / 2 : 1;
-  const bool only_v = NU == 1 && wave >= GROUPS;
-  At at[NK];
+  At at;
   struct Stage {
-    v4u raw[NU];      // codes
-    uint32_t sf[NU];  // and their rows' scale codes
+    v4u k, v;             // codes
+    uint32_t k_sf, v_sf;  // and their rows' scale codes
   };
   Stage ahead;
+  auto place_tile = [&](int i) { return place_rows(w.tile_key(min(max(i, w.t0), w.t1 - 1), KEYS) + wave * GR); };
   auto fetch = [&](Stage& to, int i) {
-    // (tiles past the list repeat its ends and are not read)
-    const int key0 = w.tile_key(min(max(TURNS && only_v ? i + 1 : i + 2, w.t0), w.t1 - 1), KEYS);
-    auto get_v = [&](int n) {
-      to.raw[NU - NK + n] = *(const v4u*)(p.c.v + at[n].code);
-      to.sf[NU - NK + n] = p.c.v_sf[at[n].sf];
+    auto get_v = [&] {
+      to.v = *(const v4u*)(p.c.v + at.code);
+      to.v_sf = p.c.v_sf[at.sf];
     };
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      if (NU > 1 && TURNS) get_v(n);
-      at[n] = place_rows(key0 + (wave + n * NW) % GROUPS * GR);
-      if (NU > 1 && !TURNS) get_v(n);
-      to.raw[n] = *(const v4u*)((only_v ? p.c.v : p.c.k) + at[n].code);
-      to.sf[n] = (only_v ? p.c.v_sf : p.c.k_sf)[at[n].sf];
-    }
+    if (TURNS) get_v();
+    at = place_tile(i + 2);  // (tiles past the list repeat its ends and are not read)
+    if (!TURNS) get_v();
+    to.k = *(const v4u*)(p.c.k + at.code);
+    to.k_sf = p.c.k_sf[at.sf];
   };
   auto put = [&](const Stage& from, uint8_t* k, uint8_t* v) {
-#pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      const bool is_v = NU > 1 ? n >= NK : only_v;
-      const int rr = (wave + n * NW) % GROUPS * GR + r;
-      uint8_t* dst = (is_v ? v : k) + rr * 2 * D;
-      const int c0 = is_v ? v_chunk<D>(rr, 2 * c) : k_chunk<D>(rr, 2 * c), c1 = is_v ? v_chunk<D>(rr, 2 * c + 1) : k_chunk<D>(rr, 2 * c + 1);
-      const v4u x = from.raw[n];
-      const float s = __uint_as_float(from.sf[n] << 23);
-      *(v4u*)(dst + c0 * 16) = widen8(x.x, x.y, s);
-      *(v4u*)(dst + c1 * 16) = widen8(x.z, x.w, s);
-    }
+    const int rr = wave * GR + r;
+    auto widen_row = [&](uint8_t* dst, v4u x, uint32_t sf, int c0, int c1) {
+      const float s = __uint_as_float(sf << 23);
+      *(v4u*)(dst + rr * 2 * D + c0 * 16) = widen8(x.x, x.y, s);
+      *(v4u*)(dst + rr * 2 * D + c1 * 16) = widen8(x.z, x.w, s);
+    };
+    widen_row(k, from.k, from.k_sf, k_chunk<D>(rr, 2 * c), k_chunk<D>(rr, 2 * c + 1));
+    widen_row(v, from.v, from.v_sf, v_chunk<D>(rr, 2 * c), v_chunk<D>(rr, 2 * c + 1));
   };
 
-  State<D> st;
+  State<DO> st;
   init(st);
   v8bf wt[NB][2];  // (zero weights go with the first matrix phase, which has no tile before it)
 #pragma unroll
@@ -681,16 +677,16 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
     const int key0 = w.tile_key(i, KEYS);
     const bool late = key0 + KEYS - 1 > place_lo, early = p.window && key0 <= place_hi - p.window && key0 + KEYS > p.sinks;
     if (late || early) mask<NB>(p, s, key0, row.place, h, late, early);
-    softmax<D, NB>(p, st, s, wt);
+    softmax<DO, NB>(p, st, s, wt);
   };
   // With turns: tile i of the list, number X of three: its K is in slot X, V of the tile before in slot X - 1.
   auto step = [&](int i, auto number) {
     constexpr int X = decltype(number)::value, NEXT = (X + 1) % 3, LAST = (X + 2) % 3;
-    product_v<D, NB>(st, wt, lds[1][LAST], lane);
+    product_v<D, DO, NB>(st, wt, lds[1][LAST], d0, lane);
     v16f s[NB];
     scores(s, lds[0][X]);
     // Four fragments are read ahead of the matrix instruction that takes them.
-    constexpr int NVF = D / 32 * NB * 2, NKF = D / 16 * NB, AHEAD = 4;  // V and K fragments (and matrix instructions)
+    constexpr int NVF = DO / 32 * NB * 2, NKF = D / 16 * NB, AHEAD = 4;  // V and K fragments (and matrix instructions)
     __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
 #pragma unroll
     for (int x = 0; x < NVF - AHEAD; ++x) {
@@ -730,7 +726,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
     __builtin_amdgcn_sched_barrier(0);
     weights(i, s);
     __builtin_amdgcn_sched_barrier(0);
-    product_v<D, NB>(st, wt, lds[1][X], lane);
+    product_v<D, DO, NB>(st, wt, lds[1][X], d0, lane);
     put(ahead, lds[0][1 - X], lds[1][1 - X]);
     __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 1);
 #pragma unroll
@@ -744,8 +740,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
     __syncthreads();
   };
   if (w.t0 < w.t1) {
-#pragma unroll
-    for (int n = 0; n < NK; ++n) at[n] = place_rows(w.tile_key(w.t0, KEYS) + (wave + n * NW) % GROUPS * GR);
+    at = place_tile(w.t0);
     Stage first;
     fetch(first, w.t0 - 2);
     fetch(ahead, w.t0 - 1);
@@ -766,7 +761,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
         last = 2;
         if (i + 3 == w.t1) break;
       }
-      product_v<D, NB>(st, wt, lds[1][last], lane);
+      product_v<D, DO, NB>(st, wt, lds[1][last], d0, lane);
     } else {
       put(first, lds[0][0], lds[1][0]);
       __syncthreads();
@@ -776,7 +771,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 256 ? 1 : D == 64 ? 3 :
       }
     }
   }
-  store_row<D>(p, w, row, st.o, st.m, both_sum(st.z), h);
+  store_row<D, DO>(p, w, row, st.o, st.m, both_sum(st.z), d0, h);
 }
 
 // ---------------------------------------------------------------- few rows: single tokens
