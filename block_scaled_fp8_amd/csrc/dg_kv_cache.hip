@@ -11,10 +11,11 @@
 // lanes of 8 values (16 bytes of BF16), a lane handles the key and the value row of its token
 // and head, and a workgroup takes consecutive tokens of one head, whose cache rows and scale
 // bytes are neighbours when their slots are.  Measured, BF16, 8 heads of 128: writing 8192 tokens
-// 11.9 us (4.2 TB/s; 14.4 with two tokens a lane, 15.7 with four, 12.8 with the rows loaded before
-// the slot is known: more, smaller waves hide the latency better); reading 16384 tokens back
-// 16.2 us (6.2 TB/s, part of it out of the last-level cache; 16.8 with one token a lane); 2.7 us
-// for a decode step's 24 tokens.
+// 10.4 us (4.9 TB/s; 12.1 with a check of each value for infinities and NaN and the row's maximum through
+// LDS: the vector unit was busy 92% of the time.  In that form, 11.9 with one token a lane, 14.4 with two,
+// 15.7 with four, 12.8 with the rows loaded before the slot is known: more, smaller waves hide the latency
+// better); reading 16384 tokens back 16.2 us (6.2 TB/s, part of it out of the last-level cache; 16.8 with
+// one token a lane); 2.4 us for a decode step's 24 tokens.
 #include "dg_kv.h"
 
 namespace dg {
@@ -47,30 +48,52 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, float (&x)[8
   }
 }
 
+// The largest x of a row's lanes, L = 8, 16 or 32 consecutive ones: neighbours, pairs, quads (mirrored halves of
+// eight), eights (mirrored rows), and the two rows of 16.
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xf, 0xf, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xf, 0xf, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, true));
+  if constexpr (L >= 16) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xf, 0xf, true));
+  if constexpr (L == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = max(r[0], r[1]);
+  }
+  return x;
+}
+
 // Codes of a lane's 8 values and the row's scale code.  The row's lanes are L consecutive ones.
-// An infinite value does not count for the scale and saturates; a NaN becomes the NaN code.
+// An infinite value does not count for the scale and saturates; a NaN becomes the NaN code.  Waves
+// without either, whose values stay within 448 s by the choice of s, need no check for each value.
 template <int L>
 __device__ __forceinline__ v2u encode8(const float (&x)[8], uint32_t& sf) {
-  float amax = 0.f;
+  constexpr uint32_t INF = 0x7F800000u;
+  uint32_t b = 0;  // the largest magnitude, as bits
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(x[i]);
-    amax = a < __builtin_inff() ? fmaxf(amax, a) : amax;
+  for (int i = 0; i < 8; ++i) b = max(b, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  const bool special = __any(b >= INF);
+  if (special) {
+    b = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t a = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      b = a < INF ? max(b, a) : b;
+    }
   }
-#pragma unroll
-  for (int d = L / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+  b = row_max<L>(b);
   // 448 = 1.75 * 2^8: the smallest power of two >= amax / 448 has amax's exponent minus 8, plus
   // one when amax's mantissa is above 1.75
-  const uint32_t b = __float_as_uint(amax);
   const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   // (up to 224 of FP32's smallest steps, amax / 448 is zero in FP32, as for a row of zeros)
   sf = b <= 224u ? 127u : (uint32_t)max(e, 1);
   const float inv = __uint_as_float((254u - sf) << 23);  // 1 / s, exact (s <= 2^120)
   float c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = fminf(fmaxf(x[i] * inv, -448.f), 448.f);
-    c[i] = x[i] == x[i] ? y : x[i];
+  for (int i = 0; i < 8; ++i) c[i] = x[i] * inv;
+  if (special) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = x[i] == x[i] ? fminf(fmaxf(c[i], -448.f), 448.f) : x[i];
   }
   v2u r;
   r.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
