@@ -1133,15 +1133,28 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
     float m = NEG_INF, z = 0.f;
     v4f o = {0.f, 0.f, 0.f, 0.f};
     if (live) {
-      // (each group by its own running maximum)
-      for (int x = group; x < n; x += G) {
-        const v2f a = mz[x * step];
-        const v4f b = *(const v4f*)(part + x * step * D);
-        if (a.x == NEG_INF) continue;  // a part in which the row sees nothing
-        const float top = fmaxf(m, a.x), f = exp2_hw(m - top), g = exp2_hw(a.x - top);
-        z = z * f + a.y * g;
-        o = o * f + b * g;
-        m = top;
+      // (each group by its own running maximum; the loads of AT_ONCE parts go out together: 131071 keys, 96 parts
+      // of 4 rows, 59.5 us, one by one 64.8)
+      constexpr int AT_ONCE = 4;
+      for (int x = group; x < n; x += G * AT_ONCE) {
+        v2f a[AT_ONCE];
+        v4f b[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          a[u] = (v2f){NEG_INF, 0.f};
+          if (x + u * G < n) {
+            a[u] = mz[(x + u * G) * step];
+            b[u] = *(const v4f*)(part + (x + u * G) * step * D);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          if (a[u].x == NEG_INF) continue;  // no part, or one in which the row sees nothing
+          const float top = fmaxf(m, a[u].x), f = exp2_hw(m - top), g = exp2_hw(a[u].x - top);
+          z = z * f + a[u].y * g;
+          o = o * f + b[u] * g;
+          m = top;
+        }
       }
     }
     if constexpr (FEW) {
