@@ -587,11 +587,6 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
   const int place_hi = w.place0 + div(min(wr0 + ROWS, w.rows) - 1, p.group);
 
   v8bf q[D / 16];
-  {
-    const uint16_t* src = p.q + row.token * p.q_token_stride + row.head * p.q_head_stride + 8 * h;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) q[i] = *(const v8bf*)(src + 16 * i);
-  }
   const int32_t* table = p.table + w.seq * p.table_stride;
   const bool page_whole = p.c.page.d % GR == 0;
   const int c = lane % CH, r = lane / CH;
@@ -744,6 +739,11 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
     Stage first;
     fetch(first, w.t0 - 2);
     fetch(ahead, w.t0 - 1);
+    // (after the tiles' loads, whose addresses wait for the block table: loads return in order)
+    __builtin_amdgcn_sched_barrier(0);
+    const uint16_t* src = p.q + row.token * p.q_token_stride + row.head * p.q_head_stride + 8 * h;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) q[i] = *(const v8bf*)(src + 16 * i);
     if constexpr (TURNS) {
       put(first, lds[0][0], lds[1][2]);
       put(ahead, lds[0][1], lds[1][0]);
