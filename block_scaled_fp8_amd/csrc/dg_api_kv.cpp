@@ -154,6 +154,11 @@ AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int
     pl.waves = 8;
   else if (few && pl.items <= (wide ? dg::MAX_SORTED : 1024) && tiles > pl.least_tiles) {
     pl.head_aim = int(slots < num_kv_heads ? 1 : slots / num_kv_heads);
+    // Parts are counted to the nearest, so where there are almost as many items as places, parts of the mean size
+    // would leave items half as long again whole: twice as many.  64 sequences of up to 8192 keys, 8 key heads
+    // (64 items for 96 places a head) 121 -> 115 us, 90 sequences (90 for 96) 169 -> 156, 32 x 16 queries (64
+    // for 64) 131 -> 106; but 20 x 16 queries (40 for 64) 73 -> 75, 32 sequences (32 for 96) 71 -> 75.
+    if (!wide && 3 * (work / num_kv_heads) >= 2 * pl.head_aim) pl.head_aim *= 2;
     // One row after the other where most items may not be cut (12 x 64 to 400 queries 84 -> 78 us); where
     // few items have many parts, as many workgroups as rows give (128 queries over 8128 keys 43 us, with two
     // rows 52).
