@@ -134,7 +134,9 @@ AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int
     if (seen < tiles) tiles = seen;
   }
   // Cutting items along the keys costs a second kernel and the parts' way through memory.  It is for items
-  // that fill at most half of the chip, and for longer ones (whose lengths it also evens out) up to twice it.
+  // that fill at most half of the chip, and for longer ones (whose lengths it also evens out) up to twice it, or
+  // four times with tiles of 32 rows, whose workgroups are long (80 x 16 queries over 5016 keys, 1280 items
+  // for 512 places, 315 us whole, 236 cut; single tokens of 256 sequences, 2048 for 768, 409 whole, 416 cut).
   // Few rows: 128 sequences in a window of 1024 (512 items of 35 tiles for 768 places) 32 us whole, 52 cut;
   // 64 sequences of up to 8192 keys (512 items of up to 256 tiles) 128 whole, 123 cut.  Many rows, one
   // sequence: 1024 queries over 4024 keys (128 items for 256 places) 104 whole, 78 cut; 1280 over 7424 (160
@@ -145,7 +147,7 @@ AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int
   const int64_t work = (with_rows < pl.items ? with_rows : pl.items) * num_kv_heads;
   const int64_t slots = int64_t(num_sms) * dg::attn_per_cu(pl.form, head_dim);
   const bool wide = pl.form == dg::ATTN_WIDE, fills_half = 2 * work <= slots;
-  const bool few = fills_half || (work < 2 * slots && (wide ? a.batch > 1 && tiles >= 64 : tiles >= 128));
+  const bool few = fills_half || (work < (pl.form == dg::ATTN_NARROW_32 ? 4 : 2) * slots && (wide ? a.batch > 1 && tiles >= 64 : tiles >= 128));
   pl.least_tiles = 4;
   // Short contexts of few items: eight waves instead of the second kernel, whose launch costs the host more
   // than it saves the device (1001 keys of 8 key heads: 11.6 against 9.1 us on the device, 8.5 against 12.9 on
