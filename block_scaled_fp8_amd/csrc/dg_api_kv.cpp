@@ -112,7 +112,7 @@ int check_shape(const AttnShape& a, int32_t num_kv_heads) {
 }
 
 struct AttnPlan {
-  int form = 0, q_tiles = 1, head_aim = 0, least_tiles = 1, max_cut = 1, join_rows = 1, join_steps = 1, waves = 4;
+  int form = 0, q_tiles = 1, head_aim = 0, least_tiles = 1, max_cut = 1, join_rows = 1, join_few = 0, join_steps = 1, waves = 4;
   int64_t items = 0, most_parts = 0;
 };
 
@@ -165,6 +165,10 @@ AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int
     // few items have many parts, as many workgroups as rows give (128 queries over 8128 keys 43 us, with two
     // rows 52).
     pl.join_steps = fills_half ? 1 : 2;
+    // 80 x 16 queries over 5016 keys (160 items, 128 places a head) 237 us with a workgroup for each row, 229
+    // without; 32 x 4 queries, 64 values a head (32 items, 128 places) 43.6 and 40.7; but 16 single tokens (16
+    // for 128) 21.4 and 23.6, 16 queries over 4016 keys (2 for 64) 18.7 and 26.6.
+    pl.join_few = !wide && pl.head_aim >= 8 * (work / num_kv_heads);
     pl.max_cut = int((tiles + pl.least_tiles - 1) / pl.least_tiles);
     const int64_t by_aim = (int64_t(pl.head_aim) + pl.items) * num_kv_heads, by_cut = pl.items * num_kv_heads * pl.max_cut;
     pl.most_parts = by_aim < by_cut ? by_aim : by_cut;
@@ -266,6 +270,7 @@ int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t 
   p.head_aim = pl.head_aim;
   p.max_cut = pl.max_cut;
   p.join_rows = pl.join_rows;
+  p.join_few = pl.join_few;
   p.join_steps = pl.join_steps;
   p.most_parts = int(pl.most_parts);
   p.least_tiles = pl.least_tiles;

@@ -1101,7 +1101,7 @@ __global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const
 // ---------------------------------------------------------------- joining the parts
 // out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) z_s over the parts s of a row's item.  A row is G groups of
 // D / 4 lanes; group x takes parts x, x + G, ..., and the groups' sums are added in their order.  256
-// threads for a row where rows are few and their parts many.  Where rows are many, G = 1 and a workgroup
+// threads for a row where rows are few and their parts many.  Otherwise G = 1 and a workgroup
 // has STEPS rows for each lane group: most items may not be cut, and their workgroups' starts are what
 // they cost.
 template <int D, bool FEW>
@@ -1184,7 +1184,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
 template <int D>
 hipError_t launch(const AttnParams& p, int form, hipStream_t stream) {
   const int64_t whole = (int64_t)p.items * p.c.num_heads, grid = p.head_aim ? p.most_parts : whole;
-  const bool few = form != ATTN_WIDE;
+  const bool few = p.join_few;
   const int block_rows = few ? Join<D, true>::PER : Join<D, false>::PER * p.join_steps;
   const int64_t blocks = whole * ((p.join_rows + block_rows - 1) / block_rows);
   if (grid > INT32_MAX || blocks > INT32_MAX) return hipErrorInvalidValue;

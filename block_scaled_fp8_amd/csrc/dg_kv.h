@@ -72,7 +72,8 @@ struct AttnParams {
   int32_t max_cut;           // an item has at most so many parts
   int32_t most_parts;        // a bound of the number of parts
   int32_t join_rows;         // a bound of the rows of a tile
-  int32_t join_steps;        // rows that a lane group of the many-rows join has one after the other
+  int32_t join_few;          // few rows with many parts each: the join has a workgroup for each row
+  int32_t join_steps;        // else: rows that a lane group of the many-rows join has one after the other
   // workspace (head_aim > 0)
   float* part_o;             // [most_parts, tile_rows, head dim] parts' unnormalised sums
   float* part_mz;            // [most_parts, tile_rows, 2] their running maximum (log2 units) and sum of weights

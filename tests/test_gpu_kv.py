@@ -245,6 +245,22 @@ def test_attention_of_many_sequences(new):
             check(p, run(p, 50, 3), 50, 3)
 
 
+@pytest.mark.parametrize("sms", [24, 40, 150])
+@pytest.mark.parametrize("dim,new", [(64, 1), (64, 11), (128, 2), (128, 30), (256, 1), (256, 9)])
+def test_attention_few_rows_in_few_parts(dim, new, sms):
+    """Ragged batches of few rows whose items are cut into two or three parts, or stay whole."""
+    rng = np.random.default_rng(dim + new)
+    lens = [int(x) for x in rng.integers(0, 900, 30)]
+    lens[3], lens[17] = 0, 1
+    news = [int(x) for x in rng.integers(0, new + 1, 30)]
+    news[29] = new
+    p = kv_gen.problem(lens, news, 8, 2, dim, 32, seed=dim + new)
+    say("attention, few parts", dim, new, sms)
+    with num_sms(sms):
+        check(p, run(p, max_seqlen_k=1 << 14))
+        check(p, run(p, 100, 3, max_seqlen_k=1 << 14), 100, 3)
+
+
 @pytest.mark.parametrize("seqs,sms", [(1, 1), (2, 2), (5, 5), (5, 12), (128, 100), (130, 100)])
 @pytest.mark.parametrize("dim,group,mask", [(64, 4, (0, 0)), (128, 8, (200, 3)), (256, 4, (0, 0))])
 def test_attention_pieces_by_size(dim, group, mask, seqs, sms):
