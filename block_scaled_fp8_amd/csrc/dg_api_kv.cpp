@@ -121,7 +121,8 @@ AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int
   const int64_t group = a.num_q_heads / num_kv_heads, rows = per_seq * group;
   AttnPlan pl;
   // The few-rows kernel reads the keys once for every 32 rows (from L2 after the first), the many-rows kernel
-  // spends whole tiles of 128 or 256: 33.1 against 30.6 us at 4 x 8 x 120 rows over 4000 keys.
+  // spends whole tiles of 128 or 256: 28 against 34 us with 4 x 30 queries over 4030 keys (120 rows), 20 against
+  // 30 with 32 over 4032 (128), but 189 against 178 with 32 x 32 over up to 8032.
   pl.form = rows <= 16 ? dg::ATTN_NARROW_16 : rows <= 128 ? dg::ATTN_NARROW_32 : dg::ATTN_WIDE;
   const int tile = dg::attn_tile_rows(pl.form, head_dim), keys = dg::attn_tile_keys(pl.form, head_dim);
   pl.q_tiles = int((rows + tile - 1) / tile);
