@@ -1149,7 +1149,9 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
         }
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u) {
-          if (a[u].x == NEG_INF) continue;  // no part, or one in which the row sees nothing
+          // no part, or one in which the row sees nothing (its sum is zero; a part whose scores are all NaN has no
+          // maximum either, but a NaN for its sum, which has to stay)
+          if (a[u].x == NEG_INF && a[u].y == 0.f) continue;
           const float top = fmaxf(m, a[u].x), f = exp2_hw(m - top), g = exp2_hw(a[u].x - top);
           z = z * f + a[u].y * g;
           o = o * f + b[u] * g;

@@ -438,3 +438,44 @@ def test_quantised_values_survive_being_written_again():
         fine = torch.isfinite(a).all(-1)
         assert int((~fine).sum()) == 1
         assert same(a[fine].cpu().numpy(), b[fine].cpu().numpy())
+
+
+# ---------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("sms", [0, 24, 1 << 14])
+@pytest.mark.parametrize("name", ["single_tokens", "single_tokens_256", "groups_of_seven", "chunks", "chunks_64", "chunks_256", "long"])
+def test_a_query_that_is_not_a_number_gives_no_number(name, sms):
+    """A NaN or infinite query shows in its own output and log-sum, whole and however its keys are cut, and in no
+    other's; one that sees no key gives zeros and -infinity like every other."""
+    lens, news, *shape = CASES[name]
+    p = kv_gen.problem(lens, news, *shape, seed=21)
+    heads, dim = shape[0], shape[2]
+    keys = np.concatenate([np.arange(n) + length - n + 1 for length, n in zip(lens, news)])  # that a row sees
+    seen = keys > 0
+    rng = np.random.default_rng(5)
+    rows = np.unique(np.concatenate([np.flatnonzero(seen)[::3], np.flatnonzero(~seen)[:2], np.flatnonzero(seen)[-1:]]))
+    bad = np.zeros((len(seen), heads), bool)
+    q = p["q_bits"].copy()
+    for i, t in enumerate(rows):
+        h = int(rng.integers(heads))
+        bad[t, h] = True
+        if i % 3 == 0:
+            q[t, h, int(rng.integers(dim))] = 0x7FC0   # one NaN
+        elif i % 3 == 1 or keys[t] < 40:
+            q[t, h] = 0x7F80                           # all infinite: products of both signs for every key
+        else:
+            q[t, h, int(rng.integers(dim))] = 0x7F80   # one infinity: scores of both signs
+    say("attention, queries that are not numbers", name, sms)
+    with num_sms(sms):
+        got = run({**p, "q_bits": q}, max_seqlen_k=1 << 16 if sms else None)
+    nan_out, nan_lse = got[0].isnan().cpu().numpy(), got[1].isnan().cpu().numpy()
+    want = bad & seen[:, None]
+    assert same(nan_lse, want) and same(nan_out.all(-1), want) and same(nan_out.any(-1), want)
+    # (the others as the oracle has them without; their last bits may move, since rows of a wave raise their running
+    # maxima together)
+    o = oracle.paged_attention(p["q"], p["k"], p["v"], p["table"], p["lens"], p["cu"], dim ** -0.5)
+    tol, tol_lse = kv_gen.bounds(o, dim)
+    assert (np.abs(got[0].double().cpu().numpy() - o["out"]) <= tol)[~want].all()
+    lse = got[1].double().cpu().numpy()
+    blind = np.isneginf(o["lse"])
+    assert same(np.isneginf(lse)[~want], blind[~want])
+    assert (np.abs(lse - np.where(blind, 0.0, o["lse"])) <= tol_lse)[~want & ~blind].all()
