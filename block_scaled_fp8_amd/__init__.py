@@ -656,7 +656,8 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
     values are already written).
 
     ``q``: BF16 [total tokens, query heads, head dim], the sequences' new tokens one after the other.
-    ``block_table``: int32 [batch, columns], each sequence's pages in order.  ``seq_lens``: int32 [batch], tokens
+    ``block_table``: int32 [batch, columns], each sequence's pages in order (an expanded table has one row for
+    all).  ``seq_lens``: int32 [batch], tokens
     in the cache, the new ones included.  ``cu_seqlens_q``: int32 [batch + 1], first row of each sequence; without
     it every sequence has the same number of new tokens.  ``max_seqlen_q``: a bound of the new tokens of a
     sequence (needed for a good split where ``cu_seqlens_q`` is given; default: all rows).  ``max_seqlen_k``: a
@@ -686,6 +687,8 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
                 or cu_seqlens_q.device != dev):
             raise ValueError(f"cu_seqlens_q must be contiguous int32 [{batch + 1}] on the cache's GPU")
         cu = cu_seqlens_q.data_ptr()
+    # (the stride of a single row means nothing, and may be anything)
+    table_stride = ts[0] if batch > 1 else cols
     max_q = total if max_seqlen_q is None else int(max_seqlen_q)
     max_k = cols * page if max_seqlen_k is None else int(max_seqlen_k)
     if out is None:
@@ -700,7 +703,7 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
     work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     os_ = out.stride()
     _check(handle.dg_fp8_paged_attention(
-        c, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts[0] if ts[0] > cols else cols, cols,
+        c, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), table_stride, cols,
         seq_lens.data_ptr(), max_k, d ** -0.5 if sm_scale is None else sm_scale, window, sinks, out.data_ptr(), os_[0], os_[1],
         None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(), need, _current_stream(dev)))
     return (out, lse) if return_lse else out

@@ -224,7 +224,9 @@ int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t 
   if (int s = check_cache(cache, empty)) return s;
   if (int s = check_shape(a, cache->num_heads)) return s;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return api_fail(DG_ERR_SHAPE, "sm_scale must be positive and finite");
-  if (table_cols < 0 || table_stride < table_cols) return api_fail(DG_ERR_LAYOUT, "table_cols = %d must not be negative, and table_stride = %lld at least as large", table_cols, (long long)table_stride);
+  // (0: one row for all sequences)
+  if (table_cols < 0 || (table_stride != 0 && table_stride < table_cols))
+    return api_fail(DG_ERR_LAYOUT, "table_cols = %d must not be negative, and table_stride = %lld at least as large, or 0", table_cols, (long long)table_stride);
   if (int64_t(table_cols) * cache->page_size > kMaxIndex) return api_fail(DG_ERR_SHAPE, "table_cols * page_size must be at most 2^30");
   if (empty) return api_ok();
   if (!block_table && table_cols > 0) return api_fail(DG_ERR_NULL, "block_table must not be NULL");

@@ -421,8 +421,8 @@ int dg_fp8_kv_cache_read(const dg_fp8_kv_cache* cache, int32_t num_tokens, void*
  *                  rows that are written), or NULL: every sequence has total_q / batch.
  *  max_seqlen_q  : with cu_seqlens_q, at least the most new tokens of a sequence (rows past it are not
  *                  computed); not read without.
- *  block_table   : device int32 [batch, table_cols] with row stride table_stride: the pages of each
- *                  sequence in order.  Entries for places that no query sees are not used; a used entry
+ *  block_table   : device int32 [batch, table_cols] with row stride table_stride (at least table_cols, or 0:
+ *                  one row for all sequences): the pages of each sequence in order.  Entries for places that no query sees are not used; a used entry
  *                  outside the cache reads page 0.  table_cols * page_size <= 2^30.
  *  seq_lens      : device int32 [batch]; clamped to [0, table_cols * page_size].
  *  max_seqlen_k  : the host's bound of seq_lens, used only to split the work; it never changes which keys count.

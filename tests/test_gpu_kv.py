@@ -479,3 +479,20 @@ def test_a_query_that_is_not_a_number_gives_no_number(name, sms):
     blind = np.isneginf(o["lse"])
     assert same(np.isneginf(lse)[~want], blind[~want])
     assert (np.abs(lse - np.where(blind, 0.0, o["lse"])) <= tol_lse)[~want & ~blind].all()
+
+
+def test_one_row_of_the_block_table_for_all_sequences():
+    """A shared prompt with several samples: an expanded table, whole and cut, gives what its copy gives."""
+    p = kv_gen.problem([300], [1], 8, 2, 128, 16, seed=31)
+    caches = [(cuda(p[x][0]), cuda(p[x][1])) for x in "kv"]
+    table = cuda(p["table"]).expand(5, -1)
+    assert table.stride(0) == 0
+    lens = torch.tensor([300, 17, 0, 299, 160], dtype=torch.int32, device=DEV)
+    for new in (1, 40):
+        q = torch.randn((5 * new, 8, 128), generator=torch.Generator(DEV).manual_seed(new), device=DEV).bfloat16()
+        for sms in (0, 1 << 12):
+            say("attention, expanded table", new, sms)
+            with num_sms(sms):
+                got, want = (dg.fp8_paged_attention(q, *caches, t, lens, return_lse=True) for t in (table, table.contiguous()))
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -208,3 +208,69 @@ def test_bounds_pass_a_correct_result_and_catch_mistakes():
     scaled = oracle.paged_attention(p["q"], (p["k"][0], sf), *args[2:], 0.125)["out"]
     for wrong in (fewer, more, scaled, r["out"] * (1 + 2.0 ** -5)):
         assert not (np.abs(wrong - r["out"]) <= tol).all()
+
+
+# ---------------------------------------------------------------- what the binding hands to the library
+class OnGpu:
+    """A CPU tensor that says it is on a GPU, for calls whose library side is replaced."""
+
+    def __init__(self, t, index=0):
+        self.t, self.device = t, torch.device("cuda", index)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class Recorder:
+    """Stands in for the library: keeps the arguments by function and says that all went well."""
+
+    def __init__(self):
+        self.calls = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.setdefault(name, []).append(args)
+            return 0
+        return call
+
+
+@pytest.fixture
+def recorder(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(dg, "lib", lambda: r)
+    monkeypatch.setattr(dg, "_current_stream", lambda dev: 0)
+    return r
+
+
+def fake_cache(index=0):
+    return [tuple(OnGpu(t, index) for t in x) for x in dg.fp8_kv_cache_empty(6, 2, 16, 64, device="cpu")]
+
+
+def fake_attention(table, batch, index=0, **kw):
+    q = OnGpu(torch.zeros((batch, 4, 64), dtype=torch.bfloat16), index)
+    lens = OnGpu(torch.zeros(batch, dtype=torch.int32), index)
+    return dg.fp8_paged_attention(q, *fake_cache(index), OnGpu(table, index), lens, out=q, **kw)
+
+
+TABLE_STRIDE, TABLE_COLS = 10, 11  # their places among dg_fp8_paged_attention's arguments
+
+
+def test_the_block_table_goes_by_its_own_stride(recorder):
+    """Every row that the kernels may read lies in the table's storage: an expanded table has one row for all."""
+    one = torch.zeros((1, 5), dtype=torch.int32)
+    big = torch.zeros((7, 9), dtype=torch.int32)
+    for table, batch in [(one, 1), (one.expand(4, -1), 4), (big, 7), (big[:, :5], 7), (big[::2, 2:6], 4), (big[:1, :3], 1), (big[:, :1], 7),
+                         (one[:, :1].expand(3, 1), 3), (big[:, :0], 7), (torch.zeros(5, dtype=torch.int32).as_strided((1, 5), (2, 1)), 1)]:
+        fake_attention(table, batch)
+        args = recorder.calls["dg_fp8_paged_attention"][-1]
+        stride, cols = args[TABLE_STRIDE], args[TABLE_COLS]
+        assert cols == table.shape[1] and (stride >= cols or stride == 0)
+        if batch > 1:
+            assert stride == table.stride(0)
+        assert table.storage_offset() + (batch - 1) * stride + cols <= table.untyped_storage().nbytes() // 4
+
+
+def test_a_table_with_one_row_for_all_is_taken():
+    """A row stride of zero passes the checks of the arguments (the next fault is found), one below the columns does not."""
+    assert attend(ts=0, lens=None) == NULL
+    assert attend(ts=3) == LAYOUT and attend(ts=-5) == LAYOUT
