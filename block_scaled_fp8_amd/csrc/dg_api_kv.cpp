@@ -111,23 +111,49 @@ int check_shape(const AttnShape& a, int32_t num_kv_heads) {
   return DG_OK;
 }
 
+// The kernel, and a call's items: tiles of rows of its sequences.
+struct AttnItems {
+  int form;
+  int64_t rows, q_tiles, items;  // rows of a sequence at most, tiles of them, tiles in all
+};
+
+AttnItems items_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim) {
+  const int64_t per_seq = a.equal ? a.total_q / a.batch : a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
+  AttnItems n;
+  n.rows = per_seq * (a.num_q_heads / num_kv_heads);
+  // The few-rows kernel reads the keys once for every 32 rows (from L2 after the first), the many-rows kernel
+  // spends whole tiles of 128 or 256: 28 against 34 us with 4 x 30 queries over 4030 keys (120 rows), 20 against
+  // 30 with 32 over 4032 (128), but 189 against 178 with 32 x 32 over up to 8032.
+  n.form = n.rows <= 16 ? dg::ATTN_NARROW_16 : n.rows <= 128 ? dg::ATTN_NARROW_32 : dg::ATTN_WIDE;
+  const int tile = dg::attn_tile_rows(n.form, head_dim);
+  n.q_tiles = (n.rows + tile - 1) / tile;
+  n.items = a.batch * n.q_tiles;
+  return n;
+}
+
+// Items are 32-bit numbers to the kernels, and a grid has less than 2^32 threads.
+int check_items(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim) {
+  const AttnItems n = items_of(a, num_kv_heads, head_dim);
+  if (n.items > int64_t(UINT32_MAX) / (int64_t(num_kv_heads) * dg::attn_threads(n.form, head_dim)))
+    return api_fail(DG_ERR_SHAPE, "%d sequences of up to %lld query rows a key head are more tiles than a launch holds%s", a.batch,
+                    (long long)n.rows, a.equal ? "" : ": max_seqlen_q should bound the new tokens of a sequence");
+  return DG_OK;
+}
+
 struct AttnPlan {
   int form = 0, q_tiles = 1, head_aim = 0, least_tiles = 1, max_cut = 1, join_rows = 1, join_few = 0, join_steps = 1, waves = 4;
   int64_t items = 0, most_parts = 0;
 };
 
 AttnPlan plan_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim, int num_sms) {
-  const int64_t per_seq = a.equal ? a.total_q / a.batch : a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
-  const int64_t group = a.num_q_heads / num_kv_heads, rows = per_seq * group;
+  const AttnItems n = items_of(a, num_kv_heads, head_dim);
+  const int64_t group = a.num_q_heads / num_kv_heads;
   AttnPlan pl;
-  // The few-rows kernel reads the keys once for every 32 rows (from L2 after the first), the many-rows kernel
-  // spends whole tiles of 128 or 256: 28 against 34 us with 4 x 30 queries over 4030 keys (120 rows), 20 against
-  // 30 with 32 over 4032 (128), but 189 against 178 with 32 x 32 over up to 8032.
-  pl.form = rows <= 16 ? dg::ATTN_NARROW_16 : rows <= 128 ? dg::ATTN_NARROW_32 : dg::ATTN_WIDE;
+  pl.form = n.form;
   const int tile = dg::attn_tile_rows(pl.form, head_dim), keys = dg::attn_tile_keys(pl.form, head_dim);
-  pl.q_tiles = int((rows + tile - 1) / tile);
-  pl.join_rows = int(rows < tile ? rows : tile);
-  pl.items = int64_t(a.batch) * pl.q_tiles;
+  pl.q_tiles = int(n.q_tiles);
+  pl.join_rows = int(n.rows < tile ? n.rows : tile);
+  pl.items = n.items;
   // Key tiles of an item at most, from the host's bound of the lengths (rounded up at both ends of a window).
   int64_t tiles = (a.max_seqlen_k + int64_t(keys) - 1) / keys;
   if (a.window) {
@@ -207,6 +233,7 @@ int64_t dg_fp8_paged_attention_workspace(int32_t batch, int32_t total_q, int32_t
     return api_fail(DG_ERR_UNSUPPORTED, "head_dim = %d: 64, 128 and 256 are supported", head_dim);
   if (int s = check_shape(a, num_kv_heads)) return s;
   if (batch == 0 || total_q == 0 || (!a.equal && max_seqlen_q == 0)) return 0;
+  if (int s = check_items(a, num_kv_heads, head_dim)) return s;
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
   return workspace_of(plan_of(a, num_kv_heads, head_dim, num_sms), head_dim);
@@ -229,6 +256,7 @@ int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t 
     return api_fail(DG_ERR_LAYOUT, "table_cols = %d must not be negative, and table_stride = %lld at least as large, or 0", table_cols, (long long)table_stride);
   if (int64_t(table_cols) * cache->page_size > kMaxIndex) return api_fail(DG_ERR_SHAPE, "table_cols * page_size must be at most 2^30");
   if (empty) return api_ok();
+  if (int s = check_items(a, cache->num_heads, cache->head_dim)) return s;
   if (!block_table && table_cols > 0) return api_fail(DG_ERR_NULL, "block_table must not be NULL");
   if (!seq_lens) return api_fail(DG_ERR_NULL, "seq_lens must not be NULL");
   if (int s = check_rows("q", q, q_token_stride, q_head_stride, 2)) return s;

@@ -89,6 +89,8 @@ inline int attn_tile_rows(int form, int head_dim) {
   return form == ATTN_NARROW_16 ? 16 : form == ATTN_NARROW_32 ? 32 : head_dim == 128 ? 256 : 128;
 }
 inline int attn_tile_keys(int form, int head_dim) { return form != ATTN_WIDE || head_dim == 256 ? 32 : 64; }
+// threads of a workgroup (of the 16-row kernel for more items than there are compute units)
+inline int attn_threads(int form, int head_dim) { return form == ATTN_WIDE && head_dim != 64 ? 512 : 256; }
 // workgroups that a compute unit holds at a time
 inline int attn_per_cu(int form, int head_dim) {
   if (form == ATTN_WIDE) return head_dim == 64 ? 3 : 1;

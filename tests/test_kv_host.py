@@ -274,3 +274,22 @@ def test_a_table_with_one_row_for_all_is_taken():
     """A row stride of zero passes the checks of the arguments (the next fault is found), one below the columns does not."""
     assert attend(ts=0, lens=None) == NULL
     assert attend(ts=3) == LAYOUT and attend(ts=-5) == LAYOUT
+
+
+def test_more_tiles_than_a_launch_holds_are_refused():
+    """batch * tiles of max_seqlen_q past 32 bits, with the binding's default bound (all rows) for example.  (The tables and
+    queries are fake: none of these calls may reach a launch.)"""
+    lib = dg.lib()
+    assert lib.dg_set_num_sms(256) == DG_OK
+    try:
+        for batch, total, hq, hk in [(65537, 1 << 20, 16, 1), (8193, 1 << 20, 128, 1), ((1 << 31) - 1, 1 << 20, 16, 1), (1 << 20, 1 << 20, 16, 4)]:
+            assert lib.dg_fp8_paged_attention_workspace(batch, total, hq, hk, 128, 0, total, 80, 0, 0) == SHAPE, batch
+            assert attend(cache(num_heads=hk), batch=batch, total_q=total, hq=hq, max_q=total) == SHAPE, batch
+            assert b"max_seqlen_q" in lib.dg_get_last_error()
+        # a bound of the new tokens is what such calls lack
+        assert lib.dg_fp8_paged_attention_workspace(65537, 1 << 20, 16, 1, 128, 0, 16, 80, 0, 0) >= 0
+        # 1024 tiles of 256 rows a sequence, 512 threads each: 2^32 threads with 8192 sequences
+        assert lib.dg_fp8_paged_attention_workspace(8191, 1 << 14, 16, 1, 128, 0, 1 << 14, 80, 0, 0) >= 0
+        assert lib.dg_fp8_paged_attention_workspace(8192, 1 << 14, 16, 1, 128, 0, 1 << 14, 80, 0, 0) == SHAPE
+    finally:
+        lib.dg_set_num_sms(0)
