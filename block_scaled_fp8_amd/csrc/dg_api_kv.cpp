@@ -80,17 +80,21 @@ int move(bool write, const dg_fp8_kv_cache* cache, int32_t num_tokens, const voi
   if (!aligned(slots, 8)) return api_fail(DG_ERR_LAYOUT, "slots must be 8-byte aligned");
   dg::KvMoveParams p{};
   p.c = kernel_cache(cache);
-  p.k = const_cast<void*>(k);
-  p.v = const_cast<void*>(v);
   p.k_token_stride = k_token_stride;
   p.k_head_stride = k_head_stride;
   p.v_token_stride = v_token_stride;
   p.v_head_stride = v_head_stride;
-  p.slots = slots;
-  p.num_tokens = num_tokens;
+  // A grid has less than 2^32 threads (one of more is cut to its low 32 bits without an error), and a row takes up to 32.
+  constexpr int32_t kMost = 1 << 26;
   const bool bf16 = dtype == DG_IN_BF16;
-  const hipError_t e = write ? dg::launch_kv_write(p, cache->head_dim, bf16, stream) : dg::launch_kv_read(p, cache->head_dim, bf16, stream);
-  if (e != hipSuccess) return api_fail(DG_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  for (int32_t from = 0; from < num_tokens; from += kMost) {
+    p.k = static_cast<char*>(const_cast<void*>(k)) + from * k_token_stride * esz;
+    p.v = static_cast<char*>(const_cast<void*>(v)) + from * v_token_stride * esz;
+    p.slots = slots + from;
+    p.num_tokens = num_tokens - from < kMost ? num_tokens - from : kMost;
+    const hipError_t e = write ? dg::launch_kv_write(p, cache->head_dim, bf16, stream) : dg::launch_kv_read(p, cache->head_dim, bf16, stream);
+    if (e != hipSuccess) return api_fail(DG_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  }
   return api_ok();
 }
 
@@ -131,7 +135,8 @@ AttnItems items_of(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim) {
   return n;
 }
 
-// Items are 32-bit numbers to the kernels, and a grid has less than 2^32 threads.
+// Items are 32-bit numbers to the kernels, and a grid has less than 2^32 threads (one of more is cut to its low
+// 32 bits without an error).
 int check_items(const AttnShape& a, int32_t num_kv_heads, int32_t head_dim) {
   const AttnItems n = items_of(a, num_kv_heads, head_dim);
   if (n.items > int64_t(UINT32_MAX) / (int64_t(num_kv_heads) * dg::attn_threads(n.form, head_dim)))

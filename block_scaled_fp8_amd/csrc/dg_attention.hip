@@ -1189,7 +1189,8 @@ hipError_t launch(const AttnParams& p, int form, hipStream_t stream) {
   const bool few = p.join_few;
   const int block_rows = few ? Join<D, true>::PER : Join<D, false>::PER * p.join_steps;
   const int64_t blocks = whole * ((p.join_rows + block_rows - 1) / block_rows);
-  if (grid > INT32_MAX || blocks > INT32_MAX) return hipErrorInvalidValue;
+  // threads of a grid stay below 2^32 (of whole items the host sees to it; cut ones are a few times the compute units)
+  if (p.head_aim && (grid * Wide<128>::THREADS > int64_t(UINT32_MAX) || blocks * 256 > int64_t(UINT32_MAX))) return hipErrorInvalidValue;
   if (form == ATTN_WIDE)
     hipLaunchKernelGGL((wide_kernel<D>), dim3((unsigned)grid), dim3(Wide<D>::THREADS), 0, stream, p);
   else if (form == ATTN_NARROW_32)

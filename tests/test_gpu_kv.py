@@ -496,3 +496,21 @@ def test_one_row_of_the_block_table_for_all_sequences():
                 got, want = (dg.fp8_paged_attention(q, *caches, t, lens, return_lse=True) for t in (table, table.contiguous()))
             torch.cuda.synchronize()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_more_tokens_than_a_launch_holds():
+    """2^28 rows of 128 values take 16 lanes each, 2^32 threads; every token but six has no slot, and all share one row."""
+    n = (1 << 28) + 9
+    k_cache, v_cache = dg.fp8_kv_cache_empty(1, 1, 16, 128, device=DEV)
+    row = torch.from_numpy(kv_gen.rows(np.random.default_rng(2), 1, 1, 128)).to(DEV)
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    for i, t in enumerate((0, (1 << 26) + 1, (1 << 28) - 1, 1 << 28, n - 2, n - 1)):
+        slots[t] = i
+    say("kv write, 2^28 tokens")
+    x = row.expand(n, -1, -1)
+    dg.fp8_kv_cache_write(x, x, k_cache, v_cache, slots)
+    torch.cuda.synchronize()
+    codes, sf = oracle.kv_encode(row.cpu().numpy())
+    for c, s in (k_cache, v_cache):
+        assert same(c[0, 0, :6].cpu().numpy(), np.repeat(codes[:, 0], 6, 0)) and same(s[0, 0, :6].cpu().numpy(), np.repeat(sf[:, 0], 6))
+        assert (c[0, 0, 6:] == 0).all()
