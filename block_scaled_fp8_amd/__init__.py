@@ -582,6 +582,14 @@ def fp8_kv_cache_empty(num_pages, num_kv_heads, page_size, head_dim, device="cud
     return one(), one()
 
 
+_INT32 = 2 ** 31 - 1  # (ctypes would pass the low 32 bits of larger numbers)
+
+
+def _bound(x):
+    """A bound or window: one past 32 bits means the same as their largest number, a negative one stays negative."""
+    return max(-1, min(int(x), _INT32))
+
+
 def _kv_cache(k_cache, v_cache):
     """The C struct of a cache, and its shape and device."""
     (kc, ks), (vc, vs) = k_cache, v_cache
@@ -596,6 +604,8 @@ def _kv_cache(k_cache, v_cache):
     rows = shape[:3]
     if ks.shape != rows or vs.shape != rows or vs.stride() != sf:
         raise ValueError("cache scales must be [pages, heads, page size], keys' and values' with the same strides")
+    if max(shape) > _INT32:
+        raise ValueError(f"cache dimensions must fit 32 bits, got {tuple(shape)}")
     if dev.type != "cuda" or vc.device != dev or ks.device != dev or vs.device != dev:
         raise ValueError("the cache must be on one GPU")
     return _KvCache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), *shape, *st[:3], *sf), shape, dev
@@ -622,6 +632,8 @@ def _kv_move(fn, c, k, v, slots, shape, dev):
         raise ValueError(f"k and v must be [tokens, {shape[1]}, {shape[3]}], contiguous along the last dimension, with one slot for each token")
     if slots.dtype != torch.int64 or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int64 vector")
+    if n > _INT32:
+        raise ValueError(f"the number of tokens must fit 32 bits, got {n}")
     if k.device != dev or v.device != dev or slots.device != dev:
         raise ValueError("k, v and slots must be on the cache's GPU")
     _check(fn(c, n, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _IN_TYPES[k.dtype],
@@ -689,8 +701,11 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
         cu = cu_seqlens_q.data_ptr()
     # (the stride of a single row means nothing, and may be anything)
     table_stride = ts[0] if batch > 1 else cols
-    max_q = total if max_seqlen_q is None else int(max_seqlen_q)
-    max_k = cols * page if max_seqlen_k is None else int(max_seqlen_k)
+    if max(total, hq, batch, cols) > _INT32:
+        raise ValueError("q's and block_table's dimensions must fit 32 bits")
+    max_q = total if max_seqlen_q is None else _bound(max_seqlen_q)
+    max_k = _bound(cols * page if max_seqlen_k is None else max_seqlen_k)
+    window, sinks = _bound(window), _bound(sinks)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != torch.bfloat16 or out.shape != qshape or out.stride(2) != 1 or out.device != dev:

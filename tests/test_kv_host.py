@@ -239,6 +239,7 @@ def recorder(monkeypatch):
     r = Recorder()
     monkeypatch.setattr(dg, "lib", lambda: r)
     monkeypatch.setattr(dg, "_current_stream", lambda dev: 0)
+    monkeypatch.setattr(dg, "_current_device", lambda: 0, raising=False)
     return r
 
 
@@ -293,3 +294,50 @@ def test_more_tiles_than_a_launch_holds_are_refused():
         assert lib.dg_fp8_paged_attention_workspace(8192, 1 << 14, 16, 1, 128, 0, 1 << 14, 80, 0, 0) == SHAPE
     finally:
         lib.dg_set_num_sms(0)
+
+
+WINDOW, SINKS, MAX_Q, MAX_K = 15, 16, 8, 13
+
+
+def test_numbers_past_32_bits_are_not_cut(recorder):
+    """A window or bound past what the library's 32-bit numbers hold means the same as the largest of them."""
+    table = torch.zeros((2, 3), dtype=torch.int32)
+    cu = OnGpu(torch.tensor([0, 1, 2], dtype=torch.int32))
+    top = 2 ** 31 - 1
+    for big in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 70):
+        fake_attention(table, 2, window=big, sinks=big, cu_seqlens_q=cu, max_seqlen_q=big, max_seqlen_k=big)
+        args = recorder.calls["dg_fp8_paged_attention"][-1]
+        assert [args[i] for i in (WINDOW, SINKS, MAX_Q, MAX_K)] == [top] * 4
+        assert recorder.calls["dg_fp8_paged_attention_workspace"][-1][6:] == (top,) * 4
+    fake_attention(table, 2, window=-2 ** 32, sinks=-2 ** 40, cu_seqlens_q=cu, max_seqlen_q=-2 ** 32, max_seqlen_k=-2 ** 32)
+    args = recorder.calls["dg_fp8_paged_attention"][-1]
+    assert all(-2 ** 31 <= args[i] < 0 for i in (WINDOW, SINKS, MAX_Q, MAX_K))   # refused by the library
+    fake_attention(table, 2, window=np.int64(7), sinks=np.int32(2))
+    args = recorder.calls["dg_fp8_paged_attention"][-1]
+    assert (args[WINDOW], args[SINKS]) == (7, 2) and type(args[WINDOW]) is int
+
+
+def test_shapes_past_32_bits_are_refused(recorder):
+    """No dimension reaches the library cut to its low 32 bits."""
+    (kc, ks), (vc, vs) = fake_cache()
+    many = 2 ** 32 + 6
+    x = OnGpu(torch.zeros((1, 2, 64)).expand(many, -1, -1))
+
+    class Slots(OnGpu):
+        shape = (many,)
+
+        def dim(self):
+            return 1
+
+        def is_contiguous(self):
+            return True
+
+    with pytest.raises(ValueError, match="32 bits"):
+        dg.fp8_kv_cache_write(x, x, (kc, ks), (vc, vs), Slots(torch.zeros(1, dtype=torch.int64)))
+    big = [OnGpu(t.t[:1].expand(many, *t.shape[1:])) for t in (kc, ks)]
+    with pytest.raises(ValueError, match="32 bits"):
+        dg.fp8_kv_cache_read(big, big, OnGpu(torch.zeros(1, dtype=torch.int64)), out=(x, x))
+    with pytest.raises(ValueError, match="32 bits"):
+        q = OnGpu(torch.zeros((1, 4, 64), dtype=torch.bfloat16).expand(many, -1, -1))
+        dg.fp8_paged_attention(q, *fake_cache(), OnGpu(torch.zeros((1, 3), dtype=torch.int32)), OnGpu(torch.zeros(1, dtype=torch.int32)), out=q)
+    assert not recorder.calls
