@@ -615,6 +615,9 @@ def _kv_cache(k_cache, v_cache):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _current_stream(dev):
     return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
@@ -647,6 +650,9 @@ def fp8_kv_cache_write(k, v, k_cache, v_cache, slots):
     keep the head dimension contiguous), written in place.  ``slots``: int64 [tokens], page * page_size +
     place in the page; a negative one, or one past the cache, is skipped.  No slot may be given twice."""
     c, shape, dev = _kv_cache(k_cache, v_cache)
+    if dev.index != _current_device():  # (the default stream's handle is the same for every GPU, and means the current one's)
+        with torch.cuda.device(dev):
+            return fp8_kv_cache_write(k, v, k_cache, v_cache, slots)
     _kv_move(lib().dg_fp8_kv_cache_write, c, k, v, slots, shape, dev)
 
 
@@ -654,6 +660,9 @@ def fp8_kv_cache_read(k_cache, v_cache, slots, out_dtype=torch.bfloat16, out=Non
     """Keys and values of ``slots`` as ``(k, v)`` [tokens, kv heads, head dim] in BF16 or FP32, exact; zeros
     for slots that are negative or past the cache.  ``out``: ``(k, v)`` to write into."""
     c, shape, dev = _kv_cache(k_cache, v_cache)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return fp8_kv_cache_read(k_cache, v_cache, slots, out_dtype, out)
     if out is None:
         want = (slots.shape[0], shape[1], shape[3])
         out = (torch.empty(want, dtype=out_dtype, device=dev), torch.empty(want, dtype=out_dtype, device=dev))
@@ -678,6 +687,10 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
     ``sinks`` tokens.  Returns ``out`` BF16 [total tokens, query heads, head dim], with ``return_lse`` also the
     FP32 log sum of exponentials [total tokens, query heads]; a query that sees nothing gives zeros and -inf."""
     c, shape, dev = _kv_cache(k_cache, v_cache)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, max_seqlen_k,
+                                       sm_scale, window, sinks, out, return_lse)
     _, hk, page, d = shape
     qshape, qs = q.shape, q.stride()
     if q.dtype != torch.bfloat16 or len(qshape) != 3 or qshape[2] != d or qs[2] != 1:

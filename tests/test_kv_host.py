@@ -341,3 +341,30 @@ def test_shapes_past_32_bits_are_refused(recorder):
         q = OnGpu(torch.zeros((1, 4, 64), dtype=torch.bfloat16).expand(many, -1, -1))
         dg.fp8_paged_attention(q, *fake_cache(), OnGpu(torch.zeros((1, 3), dtype=torch.int32)), OnGpu(torch.zeros(1, dtype=torch.int32)), out=q)
     assert not recorder.calls
+
+
+def test_the_tensors_gpu_is_the_current_one_during_a_call(recorder, monkeypatch):
+    """The default stream's handle names no GPU, and a launch goes to the current one."""
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.index = torch.device(dev).index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *a):
+            now[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(dg, "_current_device", lambda: now[0])
+    monkeypatch.setattr(dg, "_current_stream", lambda dev: seen.append((dev.index, now[0])) or 0)
+    x, slots = (torch.zeros((3, 2, 64)), torch.zeros(3, dtype=torch.int64))
+    for index in (0, 2, 0):
+        k, v = fake_cache(index)
+        dg.fp8_kv_cache_write(OnGpu(x, index), OnGpu(x, index), k, v, OnGpu(slots, index))
+        dg.fp8_kv_cache_read(k, v, OnGpu(slots, index), out=(OnGpu(x, index), OnGpu(x, index)))
+        fake_attention(torch.zeros((2, 3), dtype=torch.int32), 2, index)
+        assert now == [0]
+    assert len(seen) == 9 and all(a == b for a, b in seen)
