@@ -308,7 +308,7 @@ __device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
   const int mine = weight(lane, w);  // (the first 64 items stay in the lanes)
   int per_head = __builtin_amdgcn_readlane(scan(mine), 63);
   for (int base = 64; base < p.items; base += 64) per_head += __builtin_amdgcn_readlane(scan(weight(base + lane, other)), 63);
-  if (per_head == 0) return false;
+  // (without any row too: the join has to find that there are no parts)
   const Cut cut = cut_for(p, per_head);
   int sums = scan(cut.parts(mine)), all = __builtin_amdgcn_readlane(sums, 63);
   if (blockIdx.x == 0 && threadIdx.x < 64 && lane < p.items) p.item_end[lane] = sums;

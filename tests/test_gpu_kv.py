@@ -514,3 +514,21 @@ def test_more_tokens_than_a_launch_holds():
     for c, s in (k_cache, v_cache):
         assert same(c[0, 0, :6].cpu().numpy(), np.repeat(codes[:, 0], 6, 0)) and same(s[0, 0, :6].cpu().numpy(), np.repeat(sf[:, 0], 6))
         assert (c[0, 0, 6:] == 0).all()
+
+
+@pytest.mark.parametrize("max_q", [2, 30, 200])
+def test_a_call_whose_sequences_have_no_rows(max_q):
+    """cu_seqlens_q of one number, with rows present and keys enough to be cut: nothing is written."""
+    p = kv_gen.problem([900, 500, 0], [0, 0, 0], 8, 2, 128, 16, seed=41)
+    caches = [(cuda(p[x][0]), cuda(p[x][1])) for x in "kv"]
+    q = torch.randn((200, 8, 128), device=DEV).bfloat16()
+    for first in (0, 7, 200):
+        cu = torch.full((4,), first, dtype=torch.int32, device=DEV)
+        for sms in (0, 1 << 12):
+            out = torch.full_like(q, 3.0)
+            say("attention, no rows", max_q, first, sms)
+            with num_sms(sms):
+                dg.fp8_paged_attention(q, *caches, cuda(p["table"]), cuda(p["lens"]), cu_seqlens_q=cu, max_seqlen_q=max_q, max_seqlen_k=900,
+                                       out=out, return_lse=True)
+            torch.cuda.synchronize()
+            assert (out == 3.0).all()
