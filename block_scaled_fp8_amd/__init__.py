@@ -678,14 +678,19 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
 
     ``q``: BF16 [total tokens, query heads, head dim], the sequences' new tokens one after the other.
     ``block_table``: int32 [batch, columns], each sequence's pages in order (an expanded table has one row for
-    all).  ``seq_lens``: int32 [batch], tokens
-    in the cache, the new ones included.  ``cu_seqlens_q``: int32 [batch + 1], first row of each sequence; without
-    it every sequence has the same number of new tokens.  ``max_seqlen_q``: a bound of the new tokens of a
-    sequence (needed for a good split where ``cu_seqlens_q`` is given; default: all rows).  ``max_seqlen_k``: a
-    bound of ``seq_lens`` that only guides the split (default: the table's width).  ``sm_scale``: default
-    head_dim ** -0.5.  ``window`` > 0: a query sees its own and the ``window`` - 1 tokens before it, and the first
-    ``sinks`` tokens.  Returns ``out`` BF16 [total tokens, query heads, head dim], with ``return_lse`` also the
-    FP32 log sum of exponentials [total tokens, query heads]; a query that sees nothing gives zeros and -inf."""
+    all).  ``seq_lens``: int32 [batch], tokens in the cache, the new ones included.  ``cu_seqlens_q``: int32
+    [batch + 1], first row of each sequence; without it every sequence has the same number of new tokens.
+    ``max_seqlen_q``, where ``cu_seqlens_q`` is given: a bound of the new tokens of a sequence.  It has to hold, since
+    rows past it are not computed, and it chooses the kernel: without it (all rows) a batch of single tokens goes
+    to the kernel for long chunks.  ``max_seqlen_k``: a bound of ``seq_lens`` that only guides the split (default: the
+    table's width).  ``sm_scale``: default head_dim ** -0.5.  ``window`` > 0: a query sees its own and the
+    ``window`` - 1 tokens before it, and the first ``sinks`` tokens.
+
+    Returns ``out`` BF16 [total tokens, query heads, head dim], with ``return_lse`` also the FP32 log sum of
+    exponentials [total tokens, query heads]; a query that sees nothing gives zeros and -inf.  Only rows of a sequence
+    are written: where ``cu_seqlens_q`` does not cover all rows, or the bound above is too small, the others hold what
+    ``out`` held, or anything in a new one (zeros and -inf where no sequence can have a row: no sequences, or a bound
+    of 0).  No gradient is computed: the result of a query that requires one has none."""
     c, shape, dev = _kv_cache(k_cache, v_cache)
     if dev.index != _current_device():
         with torch.cuda.device(dev):
@@ -719,11 +724,14 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
     max_q = total if max_seqlen_q is None else _bound(max_seqlen_q)
     max_k = _bound(cols * page if max_seqlen_k is None else max_seqlen_k)
     window, sinks = _bound(window), _bound(sinks)
+    blind = batch == 0 or (cu is not None and max_q == 0)  # no query can belong to a sequence, and none is computed
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = (torch.zeros_like if blind else torch.empty_like)(q, memory_format=torch.contiguous_format)
     elif out.dtype != torch.bfloat16 or out.shape != qshape or out.stride(2) != 1 or out.device != dev:
         raise ValueError("out must be bfloat16 of q's shape, contiguous along the last dimension, on the cache's GPU")
     lse = torch.empty((total, hq), dtype=torch.float32, device=dev) if return_lse else None
+    if blind and return_lse:
+        lse.fill_(float("-inf"))
     handle = lib()
     need = handle.dg_fp8_paged_attention_workspace(batch, total, hq, hk, d, cu is None, max_q, max_k, window, sinks)
     if need < 0:

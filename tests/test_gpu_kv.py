@@ -532,3 +532,20 @@ def test_a_call_whose_sequences_have_no_rows(max_q):
                                        out=out, return_lse=True)
             torch.cuda.synchronize()
             assert (out == 3.0).all()
+
+
+@pytest.mark.parametrize("batch,max_q", [(0, 5), (2, 0)])
+def test_rows_of_a_call_without_sequences_or_new_tokens(batch, max_q):
+    """Rows that can belong to no sequence see nothing: zeros and -infinity; a given out stays as it was."""
+    k_cache, v_cache = dg.fp8_kv_cache_empty(2, 2, 16, 64, device=DEV)
+    q = torch.randn((6, 4, 64), device=DEV).bfloat16()
+    table, lens = torch.zeros((batch, 2), dtype=torch.int32, device=DEV), torch.full((batch,), 20, dtype=torch.int32, device=DEV)
+    cu = torch.zeros(batch + 1, dtype=torch.int32, device=DEV)
+    say("attention, no sequences", batch, max_q)
+    left = torch.full_like(q, 7.0), torch.full((6, 4), 7.0, device=DEV)  # (memory that the call's results are likely to get)
+    del left
+    out, lse = dg.fp8_paged_attention(q, k_cache, v_cache, table, lens, cu_seqlens_q=cu, max_seqlen_q=max_q, return_lse=True)
+    mine = torch.full_like(q, 3.0)
+    dg.fp8_paged_attention(q, k_cache, v_cache, table, lens, cu_seqlens_q=cu, max_seqlen_q=max_q, out=mine)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all() and (mine == 3.0).all()
