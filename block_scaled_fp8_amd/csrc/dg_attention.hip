@@ -348,7 +348,7 @@ __device__ __forceinline__ bool get_work(const AttnParams& p, Work& w) {
 
 // The key whose row is loaded for key j: j itself where some row of the tile sees it, else one
 // that is seen.  So nothing is read past a sequence's end or from pages that left the window;
-// the weights of such places are zero, and a visible row times zero stays zero.
+// the weights of such places are zero (and the values finite, or cleared: see below).
 __device__ __forceinline__ int key_to_load(const Work& w, int sinks, int j) {
   j = min(j, w.key_end - 1);
   return j < sinks ? j : max(j, w.key_from);
@@ -391,6 +391,69 @@ __device__ __forceinline__ void init(State<D>& st) {
     for (int j = 0; j < 16; ++j) st.o[i][j] = 0.f;
   st.m = NEG_INF;
   st.z = 0.f;
+}
+
+// Values that are no numbers.  The weight of a place that a query does not see is zero, which is not enough where
+// the value is NaN or infinite and other rows of the tile see it.  So outside of the tiles that every row sees
+// in whole, such values go to LDS as zeros, and where a wave has met one, they are added at the end, from memory,
+// to the outputs of the rows that see them.  Infinite is what BF16 does not hold: codes of 240 and more under
+// scales of 2^120 and more.  Scores need none of this, since mask() replaces them.  (What it costs: nothing
+// for single tokens, 0 to 1% of most chunks, 3% of the shortest prompts and of some at 64 values a head: 2048 queries over 8192
+// keys 228.8 -> 229.0 us, ragged chunks 155.2 -> 155.9, windowed ones 62.4 -> 63.2, 8 prompts of 512 39.1 -> 40.1, 4 x 1024
+// queries at 64 values a head 106.0 -> 109.9.)
+//
+// The tiles of a list that rows at places lo to hi all see in whole, or all alike: n from `from` on.  (Of the first
+// tokens' tiles none is counted where there is a window.)
+struct WholeTiles {
+  int from;
+  unsigned n;
+  __device__ __forceinline__ bool has(int i) const { return (unsigned)(i - from) < n; }
+};
+template <int KEYS>
+__device__ __forceinline__ WholeTiles whole_tiles(const AttnParams& p, const Work& w, int lo, int hi) {
+  if (lo == hi) return {0, UINT32_MAX};
+  // key tile t, number t - first_tile + sink_tiles, lacks no keys at its end up to (t + 1) KEYS - 1 = lo, and by its
+  // window none from t KEYS = hi - window + 1 on
+  const int list = w.sink_tiles - w.first_tile, from = p.window ? list + (hi - p.window + KEYS) / KEYS : 0;
+  return {uniform(from), (unsigned)uniform(max(list + (lo + 1) / KEYS - from, 0))};
+}
+// Whether one of a lane's 16 codes is NaN or may be infinite as BF16.
+__device__ __forceinline__ bool may_be_odd(v4u x, uint32_t sf) {
+  unsigned m = 0;  // bit 7 of a byte: its code is NaN
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= (x[i] & 0x7F7F7F7Fu) + 0x01010101u;
+  return (m & 0x80808080u) != 0 || sf >= 247;  // (247: 2^120)
+}
+// 8 BF16 that are no numbers become zeros.
+__device__ __forceinline__ v4u clear_odd(v4u x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((x[i] & 0x7F80u) == 0x7F80u) x[i] &= 0xFFFF0000u;
+    if ((x[i] & 0x7F800000u) == 0x7F800000u) x[i] &= 0xFFFFu;
+  }
+  return x;
+}
+// Whether a query at `place` sees key j.
+__device__ __forceinline__ bool sees(const AttnParams& p, int place, int j) {
+  return j <= place && (!p.window || j > place - p.window || j < p.sinks);
+}
+// What clear_odd has taken out of four places of a row: NaN, infinities, or nothing.
+__device__ __forceinline__ v4f odd_values(unsigned codes, uint32_t sf) {
+  const float s = __uint_as_float(sf << 23);
+  const unsigned lo = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, false));
+  const unsigned hi = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true));
+  auto odd = [](unsigned bits) { return (bits & 0x7F800000u) == 0x7F800000u ? __uint_as_float(bits) : 0.f; };
+  return (v4f){odd(lo << 16), odd(lo & 0xFFFF0000u), odd(hi << 16), odd(hi & 0xFFFF0000u)};
+}
+// Key j's value row.
+struct ValueRow {
+  const uint8_t* codes;
+  uint32_t sf;
+};
+__device__ __forceinline__ ValueRow value_row(const AttnParams& p, const Work& w, const int32_t* table, int j) {
+  const int col = div(j, p.c.page), off = j - col * p.c.page.d, pg = page_entry(p, table, col);
+  return {p.c.v + pg * p.c.page_stride + w.kv_head * p.c.head_stride + off * p.c.token_stride,
+          p.c.v_sf[pg * p.c.sf_page_stride + w.kv_head * p.c.sf_head_stride + off * p.c.sf_token_stride]};
 }
 
 // Scores of keys that the lane's query does not see become -infinity.  key0: first key; a lane's
@@ -575,6 +638,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
   constexpr int CH = D / 16, GR = 64 / CH;
   static_assert(KEYS / GR == NW);
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][Wide<D>::TURNS ? 3 : 2][TILE];  // [K, V][slot]
+  __shared__ int met_odd[NW];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   Work w;
   if (!get_work<KEYS, true>(p, w)) return;
@@ -639,15 +703,29 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
     to.k = *(const v4u*)(p.c.k + at.code);
     to.k_sf = p.c.k_sf[at.sf];
   };
+  const WholeTiles whole = whole_tiles<KEYS>(p, w, w.place0 + div(w.row0, p.group), w.key_end - 1);
+  // Set where a wave has cleared a value of another tile.  (All waves see it in time, as they see the tile: a barrier
+  // lies between a put and the products with it.)
+  if (lane == 0) met_odd[wave] = 0;
+  const int rr = wave * GR + r;
+  auto store = [&](uint8_t* dst, v4u x, v4u y, int c0, int c1) {
+    *(v4u*)(dst + rr * 2 * D + c0 * 16) = x;
+    *(v4u*)(dst + rr * 2 * D + c1 * 16) = y;
+  };
   auto put = [&](const Stage& from, uint8_t* k, uint8_t* v) {
-    const int rr = wave * GR + r;
-    auto widen_row = [&](uint8_t* dst, v4u x, uint32_t sf, int c0, int c1) {
-      const float s = __uint_as_float(sf << 23);
-      *(v4u*)(dst + rr * 2 * D + c0 * 16) = widen8(x.x, x.y, s);
-      *(v4u*)(dst + rr * 2 * D + c1 * 16) = widen8(x.z, x.w, s);
-    };
-    widen_row(k, from.k, from.k_sf, k_chunk<D>(rr, 2 * c), k_chunk<D>(rr, 2 * c + 1));
-    widen_row(v, from.v, from.v_sf, v_chunk<D>(rr, 2 * c), v_chunk<D>(rr, 2 * c + 1));
+    const float ks = __uint_as_float(from.k_sf << 23), vs = __uint_as_float(from.v_sf << 23);
+    store(k, widen8(from.k.x, from.k.y, ks), widen8(from.k.z, from.k.w, ks), k_chunk<D>(rr, 2 * c), k_chunk<D>(rr, 2 * c + 1));
+    store(v, widen8(from.v.x, from.v.y, vs), widen8(from.v.z, from.v.w, vs), v_chunk<D>(rr, 2 * c), v_chunk<D>(rr, 2 * c + 1));
+  };
+  // after put, with V of tile i
+  auto clear_tile = [&](const Stage& from, uint8_t* v, int i) {
+    if (__builtin_expect(!whole.has(i), 0)) {
+      if (__builtin_expect(__any(may_be_odd(from.v, from.v_sf)), 0)) {
+        const float vs = __uint_as_float(from.v_sf << 23);
+        if (lane == 0) met_odd[wave] = 1;
+        store(v, clear_odd(widen8(from.v.x, from.v.y, vs)), clear_odd(widen8(from.v.z, from.v.w, vs)), v_chunk<D>(rr, 2 * c), v_chunk<D>(rr, 2 * c + 1));
+      }
+    }
   };
 
   State<DO> st;
@@ -704,6 +782,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
     asm volatile("" : "+v"(st.z));
     __builtin_amdgcn_sched_barrier(0);
     put(ahead, lds[0][LAST], lds[1][NEXT]);
+    clear_tile(ahead, lds[1][NEXT], i + 1);
     phase_end(wave >= 4 && i + 1 < w.t1);
   };
   // Without turns: tile i with K and V in slot X; leaves tile i + 1 in the other slot and tile i + 2 on its way.
@@ -731,6 +810,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
     }
     __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 1);
     __builtin_amdgcn_sched_barrier(0);
+    clear_tile(ahead, lds[1][1 - X], i + 1);
     fetch(ahead, i);
     __syncthreads();
   };
@@ -746,7 +826,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
     for (int i = 0; i < D / 16; ++i) q[i] = *(const v8bf*)(src + 16 * i);
     if constexpr (TURNS) {
       put(first, lds[0][0], lds[1][2]);
+      clear_tile(first, lds[1][2], w.t0);
       put(ahead, lds[0][1], lds[1][0]);
+      clear_tile(ahead, lds[1][0], w.t0);
       __syncthreads();
       if (wave >= 4) __syncthreads();
       int last = 0;  // slot of the last tile
@@ -764,10 +846,33 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, D == 64 ? 3 : 2) wide_kernel
       product_v<D, DO, NB>(st, wt, lds[1][last], d0, lane);
     } else {
       put(first, lds[0][0], lds[1][0]);
+      clear_tile(first, lds[1][0], w.t0);
       __syncthreads();
       for (int i = w.t0; i < w.t1; i += 2) {
         plain_step(i, Int<0>{});
         if (i + 1 < w.t1) plain_step(i + 1, Int<1>{});
+      }
+    }
+    int any = 0;
+#pragma unroll
+    for (int x = 0; x < NW; ++x) any |= met_odd[x];
+    if (__builtin_expect(uniform(any), 0)) {
+      for (int i = w.t0; i < w.t1; ++i) {
+        if (whole.has(i)) continue;
+        const int key0 = w.tile_key(i, KEYS);
+        for (int j = key0; j < min(key0 + KEYS, w.key_end); ++j) {
+          if (j < w.key_from && j >= p.sinks) continue;  // (no row sees it, and its page may be gone)
+          const ValueRow v = value_row(p, w, table, j);
+          if (!sees(p, row.place, j)) continue;
+#pragma unroll
+          for (int d = 0; d < DO / 32; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const v4f add = odd_values(*(const unsigned*)(v.codes + d0 + 32 * d + 8 * x + 4 * h), v.sf);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) st.o[d][4 * x + e] += add[e];
+            }
+        }
       }
     }
   }
@@ -936,6 +1041,8 @@ __global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) o[b][d] = (v4f){0.f, 0.f, 0.f, 0.f};
   }
+  const WholeTiles whole = whole_tiles<KEYS>(p, w, place_lo, place_hi);
+  bool odd = false;  // the wave has cleared a value of another tile
   int i = w.t0 + wave;
   if (i < w.t1) {
     place(i);
@@ -978,6 +1085,23 @@ __global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const
       const float scale = __uint_as_float(vs[n] << 23);
       *(v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c) * 16) = widen8(vr[n].x, vr[n].y, scale);
       *(v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c + 1) * 16) = widen8(vr[n].z, vr[n].w, scale);
+    }
+    if (__builtin_expect(!whole.has(i), 0)) {
+      bool may = false;
+#pragma unroll
+      for (int n = 0; n < NP; ++n) may |= may_be_odd(vr[n], vs[n]);
+      if (__builtin_expect(__any(may), 0)) {
+        odd = true;
+#pragma unroll 1
+        for (int n = 0; n < NP; ++n) {
+          const int r = lane / CH + n * PASS, c = lane % CH;
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            v4u* at = (v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c + x) * 16);
+            *at = clear_odd(*at);
+          }
+        }
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     if (more) fetch_v();
@@ -1041,6 +1165,24 @@ __global__ void __launch_bounds__(NW * 64, D == 256 ? 1 : 2) narrow_kernel(const
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+  }
+
+  if (__builtin_expect(odd, 0)) {
+    for (i = w.t0 + wave; i < w.t1; i += NW) {
+      const int key0 = w.tile_key(i, KEYS);
+      if (whole.has(i)) continue;
+      for (int j = key0; j < min(key0 + KEYS, w.key_end); ++j) {
+        if (j < w.key_from && j >= p.sinks) continue;  // (no row sees it, and its page may be gone)
+        const ValueRow v = value_row(p, w, table, j);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          const v4f add = odd_values(*(const unsigned*)(v.codes + 16 * d + 4 * g), v.sf);
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            if (sees(p, row[b].place, j)) o[b][d] += add;
+        }
+      }
+    }
   }
 
   // join the waves: rescale to the common maximum and add up through LDS, JD values of D at a time

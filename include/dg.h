@@ -434,8 +434,10 @@ int dg_fp8_kv_cache_read(const dg_fp8_kv_cache* cache, int32_t num_tokens, void*
  * Products take BF16 operands (the cache's values exactly; the softmax weights rounded to BF16) and
  * accumulate in FP32; maxima and sums are FP32.  Results do not depend on the run (no atomics), but
  * the split, and with it the last bits, depends on batch, max_seqlen_q and max_seqlen_k.
- * A NaN in the cache at a place that some query sees may also reach the other queries of its call
- * and sequence.  batch == 0 or total_q == 0 is a no-op.
+ * NaN and infinities reach the queries that see them and no others: a NaN or infinite query, and one that sees a NaN
+ * key, gives NaN throughout and as its lse; a NaN value gives NaN at its place of the head.  A value that BF16
+ * does not hold (2^128 and more) counts as infinite, and gives an infinity or NaN there.
+ * batch == 0 or total_q == 0 is a no-op.
  */
 int dg_fp8_paged_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t total_q, int32_t num_q_heads,
                            const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -549,3 +549,78 @@ def test_rows_of_a_call_without_sequences_or_new_tokens(batch, max_q):
     dg.fp8_paged_attention(q, k_cache, v_cache, table, lens, cu_seqlens_q=cu, max_seqlen_q=max_q, out=mine)
     torch.cuda.synchronize()
     assert (out == 0).all() and torch.isneginf(lse).all() and (mine == 3.0).all()
+
+
+@pytest.mark.parametrize("sms", [0, 24, 1 << 14])
+@pytest.mark.parametrize("mask", [(0, 0), (33, 0), (20, 9), (40, 70)])
+@pytest.mark.parametrize("name", ["single_tokens", "groups_of_seven", "more_new_than_held", "forty_heads_one_key_head", "chunks", "chunks_64",
+                                  "chunks_256", "long"])
+def test_a_value_that_is_not_a_number_reaches_the_queries_that_see_it(name, mask, sms):
+    """NaN among values and keys: exactly the queries that see their token, and of values exactly their places of the head,
+    give no number; all others give what the cache without them gives."""
+    lens, news, *shape = CASES[name]
+    p = kv_gen.problem(lens, news, *shape, seed=51)
+    heads, hk, dim, page = shape
+    rng = np.random.default_rng(len(name) + sum(mask))
+    first = np.concatenate([[0], np.cumsum(news)])
+    want_out, want_lse = np.zeros((first[-1], heads, dim), bool), np.zeros((first[-1], heads), bool)
+    k, v = (tuple(a.copy() for a in p[x]) for x in "kv")
+    for b, (length, n) in enumerate(zip(lens, news)):
+        seen = oracle.visible(length, n, *mask)
+        # new tokens that only some queries see, and old ones at the window's end
+        at = set(rng.choice(length, min(length, 2), replace=False).tolist()) | {j for j in (length - 1, length - n // 2 - 1, length - n - mask[0] + 1) if 0 <= j < length}
+        for i, j in enumerate(sorted(at)):
+            h, d = int(rng.integers(hk)), int(rng.integers(dim))
+            rows, heads_of = first[b] + np.flatnonzero(seen[:, j]), slice(h * (heads // hk), (h + 1) * (heads // hk))
+            page_at = p["table"][b, j // page], h, j % page
+            if i % 3 != 2:
+                v[0][page_at + (d,)] = 0x7F if i % 2 else 0xFF
+                want_out[rows, heads_of, d] = True
+            else:
+                k[0][page_at + (d,)] = 0x7F
+                want_out[rows, heads_of], want_lse[rows, heads_of] = True, True
+    say("attention, cache with NaN", name, mask, sms)
+    with num_sms(sms):
+        got = run({**p, "k": k, "v": v}, *mask, max_seqlen_k=1 << 16 if sms else None)
+    out, lse = got[0].double().cpu().numpy(), got[1].double().cpu().numpy()
+    assert same(np.isnan(lse), want_lse)
+    assert same(np.isnan(out), want_out)
+    o = oracle.paged_attention(p["q"], p["k"], p["v"], p["table"], p["lens"], p["cu"], dim ** -0.5, *mask)
+    tol, tol_lse = kv_gen.bounds(o, dim)
+    blind = np.isneginf(o["lse"])
+    assert (np.abs(out - o["out"]) <= tol)[~want_out].all()
+    assert same(np.isneginf(lse), blind)
+    assert (np.abs(lse - np.where(blind, 0.0, o["lse"])) <= tol_lse)[~want_lse & ~blind].all()
+
+
+@pytest.mark.parametrize("name", ["groups_of_seven", "chunks", "chunks_64", "chunks_256"])
+def test_a_value_past_bf16_reaches_the_queries_that_see_it(name):
+    """Codes whose value BF16 does not hold (FP32 rows near its largest number, or scales of another writer): queries that see the token
+    give no finite number at these places of the head, all others what they give without it."""
+    lens, news, *shape = CASES[name]
+    p = kv_gen.problem(lens, news, *shape, seed=61)
+    heads, hk, dim, page = shape
+    first = np.concatenate([[0], np.cumsum(news)])
+    want, big = np.zeros((first[-1], heads, dim), bool), []
+    v = tuple(a.copy() for a in p["v"])
+    for b, (length, n) in enumerate(zip(lens, news)):
+        j = length - 1 - n // 3
+        at = p["table"][b, j // page], hk - 1, j % page
+        v[0][at] = 0x30              # (1/2)
+        v[0][at + (5,)], v[0][at + (dim - 3,)] = 0x7E, 0xFE
+        v[1][at] = 250               # 448 * 2^123
+        rows = first[b] + np.flatnonzero(oracle.visible(length, n)[:, j])
+        for d in (5, dim - 3):
+            want[rows, heads - heads // hk:, d] = True
+        big.append(rows)             # (their other places hold 2^122 times a weight: not compared)
+    say("attention, values past BF16", name)
+    for sms in (0, 1 << 14):
+        with num_sms(sms):
+            out = run({**p, "v": v}, max_seqlen_k=1 << 16 if sms else None)[0].double().cpu().numpy()
+        finite = np.isfinite(out)
+        assert same(~finite, want)
+        o = oracle.paged_attention(p["q"], p["k"], p["v"], p["table"], p["lens"], p["cu"], dim ** -0.5)
+        tol, _ = kv_gen.bounds(o, dim)
+        plain = np.ones((first[-1], heads), bool)
+        plain[np.concatenate(big), heads - heads // hk:] = False
+        assert (np.abs(out - o["out"]) <= tol)[plain].all()
