@@ -6,7 +6,6 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <string>
 
 #include "../../include/dg.h"
 #include "dg_internal.h"
@@ -14,21 +13,21 @@
 
 namespace {
 
-thread_local std::string g_last_error;
+thread_local char g_last_error[512];
 std::atomic<int> g_num_sms_override{0};
 
+void record(const char* fmt, va_list ap) { vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap); }
+
 int fail(int code, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  record(fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return code;
 }
 
 int ok() {
-  g_last_error.clear();
+  g_last_error[0] = 0;
   return DG_OK;
 }
 
@@ -37,12 +36,10 @@ int ok() {
 // for the other host files
 namespace dg {
 int api_fail(int code, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  record(fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return code;
 }
 int api_ok() { return ok(); }
@@ -832,6 +829,6 @@ int dg_get_gemm_config(int32_t kind, int32_t m, int32_t n, int32_t k, int32_t nu
   return ok();
 }
 
-const char* dg_get_last_error(void) { return g_last_error.c_str(); }
+const char* dg_get_last_error(void) { return g_last_error; }
 
 }  // extern "C"

@@ -7,7 +7,7 @@
 namespace dg {
 
 // Shared by the host files: record a failure (returns `code`), record success (returns DG_OK),
-// and the persistent grid size in force (0 if the device cannot be queried).
+// and the persistent grid size in force (negative if the device cannot be queried).
 int api_fail(int code, const char* fmt, ...);
 int api_ok();
 int api_num_sms();
