@@ -624,3 +624,30 @@ def test_a_value_past_bf16_reaches_the_queries_that_see_it(name):
         plain = np.ones((first[-1], heads), bool)
         plain[np.concatenate(big), heads - heads // hk:] = False
         assert (np.abs(out - o["out"]) <= tol)[plain].all()
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 15])
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 1), (128, 6), (256, 2), (64, 50), (128, 50), (256, 40)])
+def test_attention_small_pages_in_parts(dim, new, page):
+    """Pages that hold no row of 16 keys together, cut into many parts and few; pages that end anywhere in a tile."""
+    p = kv_gen.problem([700, 0, 333, 64], [new, 1, max(1, new - 1), new], 8, 2, dim, page, seed=page + dim)
+    say("attention, small pages", dim, new, page)
+    for sms in (0, 24, 1 << 14):
+        for mask in ((0, 0), (90, 2)):
+            with num_sms(sms):
+                check(p, run(p, *mask, max_seqlen_k=1 << 14), *mask)
+
+
+@pytest.mark.parametrize("batch,new", [(1024, 1), (1025, 1), (1500, 2), (520, 33)])
+def test_attention_of_more_items_than_are_cut(batch, new):
+    """Around the number of items up to which they may be cut, which more compute units than there are ask for."""
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(0, 70, batch)]
+    lens[-1] = 600
+    news = [min(new, int(x)) for x in rng.integers(0, new + 2, batch)]
+    news[-1] = new
+    p = kv_gen.problem(lens, news, 4, 1, 64, 16, seed=batch)
+    say("attention, many items", batch, new)
+    for sms in (0, 1 << 12):
+        with num_sms(sms):
+            check(p, run(p, max_seqlen_k=1 << 13))
