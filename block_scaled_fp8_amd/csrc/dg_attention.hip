@@ -605,7 +605,7 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Work& w, co
 // waves without 70).  D = 256: a wave with the queries and outputs of 32 rows has no room beside it on its
 // SIMD, and a single one is bound by how fast it issues.  So two waves, one of each half of the workgroup,
 // share 32 rows: both compute their scores and weights, each half of the outputs (1536 queries, 16 heads, 4
-// key heads, over 7680 keys: 314 us; with four waves, each alone with its rows, 405).
+// key heads, over 7680 keys: 314 us; with four waves, each alone with its rows, 405; now 295).
 //
 // Tiles lie widened in LDS.  With turns, in rings of three: stage i brings K of tile i + 2 and V of tile
 // i + 1; a wave issues its loads at the end of its matrix phase of tile i, when its LDS reads are out

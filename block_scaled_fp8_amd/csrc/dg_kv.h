@@ -91,7 +91,8 @@ inline int attn_tile_rows(int form, int head_dim) {
 inline int attn_tile_keys(int form, int head_dim) { return form != ATTN_WIDE || head_dim == 256 ? 32 : 64; }
 // threads of a workgroup (of the 16-row kernel for more items than there are compute units)
 inline int attn_threads(int form, int head_dim) { return form == ATTN_WIDE && head_dim != 64 ? 512 : 256; }
-// workgroups that a compute unit holds at a time
+// workgroups that a compute unit holds at a time, by the registers of a lane: few rows of 16 102, 152 and 255 at head_dim
+// 64, 128 and 256, of 32 136, 213 and all, many rows 162, 228 and 236 (of 512 for the waves of a SIMD)
 inline int attn_per_cu(int form, int head_dim) {
   if (form == ATTN_WIDE) return head_dim == 64 ? 3 : 1;
   if (head_dim == 256) return 1;

@@ -396,8 +396,9 @@ int dg_fp8_kv_cache_write(const dg_fp8_kv_cache* cache, int32_t num_tokens, cons
                           int32_t dtype, const int64_t* slots, hipStream_t stream);
 
 /*
- * Read slots back: k and v [num_tokens, num_heads, head_dim] as BF16 or FP32, both exact (the smallest
- * scales apart, where BF16 or FP32 runs out of exponent).  A slot that is negative or past the cache gives zeros.
+ * Read slots back: k and v [num_tokens, num_heads, head_dim] as BF16 or FP32, both exact but where BF16 or FP32
+ * runs out of exponent: under the smallest scales, and in a row near FP32's largest number, whose largest code stands
+ * for 2^128 and reads as infinity.  A slot that is negative or past the cache gives zeros.
  * Arguments as in dg_fp8_kv_cache_write; a slot may be given more than once.
  */
 int dg_fp8_kv_cache_read(const dg_fp8_kv_cache* cache, int32_t num_tokens, void* k, int64_t k_token_stride,
@@ -432,10 +433,12 @@ int dg_fp8_kv_cache_read(const dg_fp8_kv_cache* cache, int32_t num_tokens, void*
  *  workspace     : device memory of at least dg_fp8_paged_attention_workspace() bytes for the same
  *                  arguments, 16-byte aligned; contents on entry do not matter.  NULL where that is 0.
  * Products take BF16 operands (the cache's values exactly; the softmax weights rounded to BF16) and
- * accumulate in FP32; maxima and sums are FP32.  Results do not depend on the run (no atomics), but
- * the split, and with it the last bits, depends on batch, max_seqlen_q and max_seqlen_k.
- * NaN and infinities reach the queries that see them and no others: a NaN or infinite query, and one that sees a NaN
- * key, gives NaN throughout and as its lse; a NaN value gives NaN at its place of the head.  A value that BF16
+ * accumulate in FP32; maxima and sums are FP32.  The same call gives the same results in every run (no atomics).  A
+ * sequence's last bits depend on the whole call, though: the work is split by the lengths and new tokens of all its
+ * sequences, the head counts and head_dim, window, sinks, max_seqlen_q, max_seqlen_k and the number of compute units
+ * (dg_set_num_sms), and rows that share a wave raise their running maxima together.
+ * NaN and infinities reach the queries that see them and no others: a query one of whose scores is NaN or +infinity
+ * (by its own values or a key's) gives NaN throughout and as its lse; a NaN value gives NaN at its place of the head.  A value that BF16
  * does not hold (2^128 and more) counts as infinite, and gives an infinity or NaN there.
  * batch == 0 or total_q == 0 is a no-op.
  */
