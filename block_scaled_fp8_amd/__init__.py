@@ -27,7 +27,8 @@ __all__ = [
     "transform_sf", "get_mn_major_tma_aligned_tensor", "get_mn_major_tma_aligned_packed_ue8m0_tensor",
     "per_token_group_cast_fp8", "k_grouped_fp8_gemm_nt_contiguous", "k_grouped_fp8_gemm_tn_contiguous", "transform_sf_into_required_layout",
     "fp8_fp4_gemm_nt", "m_grouped_fp8_fp4_gemm_nt_contiguous", "m_grouped_fp8_fp4_gemm_nt_masked", "get_tma_aligned_size", "get_mk_alignment_for_contiguous_layout", "set_num_sms", "get_num_sms",
-    "get_gemm_config", "fp8_kv_cache_empty", "fp8_kv_cache_write", "fp8_kv_cache_read", "fp8_paged_attention", "LIB_PATH",
+    "get_gemm_config", "fp8_kv_cache_empty", "fp8_kv_cache_write", "fp8_kv_cache_read", "fp8_paged_attention",
+    "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_fp8_kv_cache_write", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdg.so")
@@ -47,7 +48,21 @@ class _KvCache(ctypes.Structure):
                 ("sf_page_stride", _i64), ("sf_head_stride", _i64), ("sf_token_stride", _i64)]
 
 
+class _NormRope(ctypes.Structure):
+    """dg_norm_rope (include/dg.h)."""
+    _fields_ = [("num_tokens", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32),
+                ("dtype", _i32), ("weight_dtype", _i32), ("q_weight", _p), ("k_weight", _p),
+                ("cos_sin", _p), ("cos_sin_stride", _i64), ("num_positions", _i64), ("positions", _p),
+                ("rot_dim", _i32), ("interleaved", _i32), ("eps", ctypes.c_float)]
+
+
+class _Rows(ctypes.Structure):
+    """dg_rows (include/dg.h)."""
+    _fields_ = [("p", _p), ("token_stride", _i64), ("head_stride", _i64)]
+
+
 _c = ctypes.POINTER(_KvCache)
+_n = ctypes.POINTER(_NormRope)
 _SIGS = {
     **{f"dg_fp8_gemm_{lay}": (_i32, [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _i32,
                                      _p, _i64, _p, _i64, _i32, _p]) for lay in ("nt", "nn", "tn", "tt")},
@@ -74,6 +89,10 @@ _SIGS = {
     "dg_fp8_paged_attention": (_i32, [_c, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32,
                                       ctypes.c_float, _i32, _i32, _p, _i64, _i64, _p, _p, _i64, _p]),
     "dg_fp8_paged_attention_workspace": (_i64, [_i32] * 10),
+    "dg_qk_norm_rope": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _p]),
+    "dg_qk_norm_rope_backward": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _Rows, _Rows, _p, _p, _p, _i64, _p]),
+    "dg_qk_norm_rope_backward_workspace": (_i64, [_i32] * 4),
+    "dg_qk_norm_rope_fp8_kv_cache_write": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _c, _p, _p]),
     "dg_get_tma_aligned_size": (_i64, [_i64, _i32]),
     "dg_get_mk_alignment_for_contiguous_layout": (_i32, []),
     "dg_set_num_sms": (_i32, [_i32]),
@@ -743,3 +762,109 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
         seq_lens.data_ptr(), max_k, d ** -0.5 if sm_scale is None else sm_scale, window, sinks, out.data_ptr(), os_[0], os_[1],
         None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(), need, _current_stream(dev)))
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- norm and rotation of queries and keys
+def _rows(name, x, like, dev):
+    """The C struct of rows [tokens, heads, head dim] of the shape and type of ``like`` (a shape and a dtype)."""
+    shape, dtype = like
+    st = x.stride()
+    if tuple(x.shape) != shape or x.dtype != dtype or st[2] != 1 or x.device != dev:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {dev}, contiguous along the last dimension")
+    return _Rows(x.data_ptr(), st[0], st[1])
+
+
+def _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved):
+    """The C struct of a call, and the shapes and type of the queries' and keys' rows."""
+    dtype, dev = q.dtype, q.device
+    if dtype not in _IN_TYPES or k.dtype != dtype:
+        raise TypeError(f"q and k must both be bfloat16 or float32, got {dtype} and {k.dtype}")
+    qs, ks = tuple(q.shape), tuple(k.shape)
+    if len(qs) != 3 or len(ks) != 3 or qs[0] != ks[0] or qs[2] != ks[2]:
+        raise ValueError(f"q and k must be [tokens, heads, head dim] with the same tokens and head dim, got {list(qs)} and {list(ks)}")
+    t, hq, d = qs
+    if q_weight.dtype not in _IN_TYPES or k_weight.dtype != q_weight.dtype:
+        raise TypeError(f"q_weight and k_weight must both be bfloat16 or float32, got {q_weight.dtype} and {k_weight.dtype}")
+    if tuple(q_weight.shape) != (d,) or tuple(k_weight.shape) != (d,) or not q_weight.is_contiguous() or not k_weight.is_contiguous():
+        raise ValueError(f"q_weight and k_weight must be contiguous [{d}]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.stride(1) != 1:
+        raise ValueError("cos_sin must be float32 [positions, rotated dim], contiguous along the last dimension")
+    if positions.dtype != torch.int64 or tuple(positions.shape) != (t,) or not positions.is_contiguous():
+        raise ValueError(f"positions must be contiguous int64 [{t}]")
+    if dev.type != "cuda" or any(x.device != dev for x in (k, q_weight, k_weight, cos_sin, positions)):
+        raise ValueError("q, k, the weights, cos_sin and positions must be on one GPU")
+    if max(*qs, ks[1]) > _INT32:
+        raise ValueError("q's and k's dimensions must fit 32 bits")
+    a = _NormRope(t, hq, ks[1], d, _IN_TYPES[dtype], _IN_TYPES[q_weight.dtype], q_weight.data_ptr(), k_weight.data_ptr(),
+                  cos_sin.data_ptr(), cos_sin.stride(0), cos_sin.shape[0], positions.data_ptr(), cos_sin.shape[1],
+                  bool(interleaved), eps)
+    return a, (qs, dtype), (ks, dtype), dev
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interleaved=False, out=None):
+    """Norm and rotation of queries and keys for each head: ``w * x / sqrt(mean(x ** 2) + eps)`` of each row, whose
+    first R values then turn in pairs (i, i + R // 2), or (2 i, 2 i + 1) with ``interleaved``, by the token's angles.
+
+    ``q`` [tokens, query heads, head dim] and ``k`` [tokens, key heads, head dim]: both BF16 or both FP32, any strides that
+    keep 16-byte aligned rows (slices of one projection's output).  ``q_weight``, ``k_weight``: [head dim], BF16 or FP32.
+    ``cos_sin``: FP32 [positions, R], a position's R // 2 cosines, then its sines; R a multiple of 16 up to the head dim.
+    ``positions``: int64 [tokens]; a token whose position is negative or past the table is padding, and gives zeros.
+    ``out``: ``(q, k)`` to write into, which may be ``q`` and ``k`` themselves.  Returns ``(q, k)`` of the inputs' type.
+    The results have no autograd history; their gradients come from ``qk_norm_rope_backward``."""
+    a, ql, kl, dev = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, out)
+    if out is None:
+        out = torch.empty(ql[0], dtype=ql[1], device=dev), torch.empty(kl[0], dtype=kl[1], device=dev)
+    q_out, k_out = out
+    _check(lib().dg_qk_norm_rope(a, _rows("q", q, ql, dev), _rows("k", k, kl, dev), _rows("out[0]", q_out, ql, dev),
+                                 _rows("out[1]", k_out, kl, dev), _current_stream(dev)))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interleaved=False, out=None):
+    """Gradients of ``qk_norm_rope``: ``dq_out`` and ``dk_out`` are those of its results, the other arguments the forward
+    call's.  Returns ``(dq, dk, dq_weight, dk_weight)``: the rows' in their type, the weights' FP32 [head dim], summed over tokens
+    and heads (zeros without a token).  ``out``: ``(dq, dk)`` to write into, which may be ``dq_out`` and ``dk_out``."""
+    a, ql, kl, dev = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, out)
+    if out is None:
+        out = torch.empty(ql[0], dtype=ql[1], device=dev), torch.empty(kl[0], dtype=kl[1], device=dev)
+    dq, dk = out
+    (t, hq, d), hk = ql[0], kl[0][1]
+    handle = lib()
+    need = handle.dg_qk_norm_rope_backward_workspace(t, hq, hk, d)
+    if need < 0:
+        _check(need)
+    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    dw = torch.empty((2, d), dtype=torch.float32, device=dev)
+    _check(handle.dg_qk_norm_rope_backward(
+        a, _rows("dq_out", dq_out, ql, dev), _rows("dk_out", dk_out, kl, dev), _rows("q", q, ql, dev), _rows("k", k, kl, dev),
+        _rows("out[0]", dq, ql, dev), _rows("out[1]", dk, kl, dev), dw.data_ptr(), dw.data_ptr() + 4 * d,
+        None if work is None else work.data_ptr(), need, _current_stream(dev)))
+    return dq, dk, dw[0], dw[1]
+
+
+def qk_norm_rope_fp8_kv_cache_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slots, eps=1e-6,
+                                    interleaved=False, out=None):
+    """``qk_norm_rope`` whose keys, and the values ``v``, go to the slots of an FP8 cache as ``fp8_kv_cache_write`` writes them
+    (the keys quantised from FP32, without a rounding to BF16 between).  Returns the queries; ``out``: where to write them,
+    may be ``q``.  A padding token's keys and values are not written, nor those of a slot that is negative or past the cache."""
+    a, ql, kl, dev = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope_fp8_kv_cache_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slots, eps,
+                                                   interleaved, out)
+    c, _, cache_dev = _kv_cache(k_cache, v_cache)
+    if slots.dtype != torch.int64 or tuple(slots.shape) != ql[0][:1] or not slots.is_contiguous():
+        raise ValueError(f"slots must be contiguous int64 [{ql[0][0]}]")
+    if cache_dev != dev or slots.device != dev:
+        raise ValueError("the cache and slots must be on q's GPU")
+    if out is None:
+        out = torch.empty(ql[0], dtype=ql[1], device=dev)
+    _check(lib().dg_qk_norm_rope_fp8_kv_cache_write(a, _rows("q", q, ql, dev), _rows("k", k, kl, dev), _rows("v", v, kl, dev),
+                                                    _rows("out", out, ql, dev), c, slots.data_ptr(), _current_stream(dev)))
+    return out

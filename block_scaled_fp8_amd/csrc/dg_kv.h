@@ -48,6 +48,36 @@ struct KvMoveParams {  // write and read
 hipError_t launch_kv_write(const KvMoveParams& p, int head_dim, bool bf16, hipStream_t stream);
 hipError_t launch_kv_read(const KvMoveParams& p, int head_dim, bool bf16, hipStream_t stream);
 
+// Rows [tokens, heads, head dim], strides in elements.
+struct Rows {
+  void* p;
+  int64_t token_stride, head_stride;
+};
+
+// Norm and rotation of queries' and keys' rows: forward (q, k -> q_out, k_out), with the keys, and the values v, going to
+// the cache instead (slots), or backward (and dq, dk, the gradients of the results; q_out and k_out are those of q and k).
+struct RopeParams {
+  Rows q, k, v, dq, dk, q_out, k_out;
+  const void *q_weight, *k_weight;  // [head dim]
+  const float* cos_sin;             // [num_positions, rot]
+  int64_t cos_sin_stride;
+  const int64_t* positions;         // [num_tokens]
+  int64_t num_positions;
+  int32_t rot, num_tokens, q_heads, kv_heads;
+  float eps;
+  int32_t weights_bf16;
+  KvCache c;
+  const int64_t* slots;
+  FastDiv pieces;                   // waves that share a token (backward: of the section)
+  float *dq_weight, *dk_weight;     // [head dim]
+  float* parts;                     // [workgroups, 2, head dim] sums of the weights' gradients (workgroups > 1)
+  int32_t workgroups;               // backward only
+};
+hipError_t launch_norm_rope(const RopeParams& p, int head_dim, bool bf16, bool interleaved, bool write, hipStream_t stream);
+hipError_t launch_norm_rope_backward(const RopeParams& p, int head_dim, bool bf16, bool interleaved, hipStream_t stream);
+// heads of a token that a wave takes at once
+inline int rope_heads(int head_dim) { return 1024 / head_dim; }
+
 struct AttnParams {
   KvCache c;
   const uint16_t* q;

@@ -1,0 +1,282 @@
+// Norm and rotation of queries and keys for each head, for gfx950 (MI355X): forward, forward into the FP8
+// key/value cache, and backward.
+//
+// For a row x (one token and head, D values), weights w and the token's angles a_i, i < R / 2:
+//   y = w x r,  r = 1 / sqrt(mean(x^2) + eps),  and each pair (y_i, y_j) of the first R values turns:
+//   (y_i cos a_i - y_j sin a_i, y_i sin a_i + y_j cos a_i),  j = i + R / 2, or (2 i, 2 i + 1) interleaved.
+// Backward, with t the gradient of the result turned back, u = x r and g = w t:
+//   dx = r (g - u mean(g u)),  dw = sum of t u over tokens and heads.
+// All of it in FP32, rounded once at the end.
+//
+// Bound by memory.  A row is D / 16 lanes of 16 values, two chunks of eight that hold whole pairs: lane l < R / 16
+// has chunks l and l + R / 16 (interleaved: 2 l and 2 l + 1), so a pair never leaves its lane, and both
+// forms take the same cosines and sines, 8 l to 8 l + 7.  The rest of the row goes in pairs of chunks to the
+// lanes after those.  A wave takes 1024 / D heads of one token.
+#include <type_traits>
+
+#include "dg_kv_device.h"
+
+namespace dg {
+namespace rope {
+
+constexpr int THREADS = 256, WAVES = THREADS / 64;
+
+// A lane's place in its row.
+struct Lane {
+  int c0, c1;  // its chunks, as offsets of values
+  bool turns;
+};
+template <int D, bool INTER>
+__device__ __forceinline__ Lane lane_of(int l, int rot) {
+  const int r = rot / 16;
+  const bool turns = l < r;
+  if (INTER) return {16 * l, 16 * l + 8, turns};
+  // (past the turning lanes, 2 r + 2 (l - r) = 2 l)
+  return turns ? Lane{8 * l, 8 * l + 8 * r, true} : Lane{16 * l, 16 * l + 8, false};
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load16(const void* base, int64_t at, const Lane& l, float (&x)[16]) {
+  load8<BF16>(base, at + l.c0, *(float(*)[8])x);
+  load8<BF16>(base, at + l.c1, *(float(*)[8])(x + 8));
+}
+
+__device__ __forceinline__ unsigned pack2(float x, float y) {
+  return __builtin_bit_cast(unsigned, (v2bf){(__bf16)x, (__bf16)y});
+}
+template <bool BF16>
+__device__ __forceinline__ void store16(void* base, int64_t at, const Lane& l, const float (&x)[16]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int64_t to = at + (c ? l.c1 : l.c0);
+    const float* y = x + 8 * c;
+    if constexpr (BF16) {
+      *(v4u*)((uint16_t*)base + to) = (v4u){pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *(v4u*)((float*)base + to + i) = (v4u){__float_as_uint(y[i]), __float_as_uint(y[i + 1]), __float_as_uint(y[i + 2]), __float_as_uint(y[i + 3])};
+    }
+  }
+}
+
+// Sum over the L lanes of a row, 4, 8 or 16 consecutive ones, in all of them.
+template <int L>
+__device__ __forceinline__ float row_sum(float x) {
+  auto from = [](float v, auto ctrl) { return __uint_as_float((unsigned)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true)); };
+  x += from(x, std::integral_constant<int, 0xB1>());
+  x += from(x, std::integral_constant<int, 0x4E>());
+  if constexpr (L >= 8) x += from(x, std::integral_constant<int, 0x141>());
+  if constexpr (L >= 16) x += from(x, std::integral_constant<int, 0x140>());
+  return x;
+}
+
+template <int D>
+__device__ __forceinline__ float inverse_rms(const float (&x)[16], float eps) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s = __builtin_fmaf(x[i], x[i], s);
+  return 1.f / __builtin_sqrtf(__builtin_fmaf(row_sum<D / 16>(s), 1.f / D, eps));
+}
+
+struct Angles {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_angles(const RopeParams& p, int64_t position, int l, Angles& a) {
+  const float* row = p.cos_sin + position * p.cos_sin_stride + 8 * l;
+  load8<false>(row, 0, a.c);
+  load8<false>(row, p.rot / 2, a.s);
+}
+// The pairs turned by the angles (SIGN 1) or back (-1).
+template <bool INTER, int SIGN>
+__device__ __forceinline__ void turn(float (&y)[16], const Angles& a) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float &u = y[INTER ? 2 * i : i], &v = y[INTER ? 2 * i + 1 : 8 + i];
+    const float s = SIGN * a.s[i], x = __builtin_fmaf(u, a.c[i], -(v * s));
+    v = __builtin_fmaf(u, s, v * a.c[i]);
+    u = x;
+  }
+}
+
+__device__ __forceinline__ void load_weights(const void* w, bool bf16, const Lane& l, float (&x)[16]) {
+  if (bf16)
+    load16<true>(w, 0, l, x);
+  else
+    load16<false>(w, 0, l, x);
+}
+
+// ---------------------------------------------------------------- forward
+template <int D, bool BF16, bool INTER, bool WRITE>
+__global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
+  constexpr int L = D / 16, HEADS = 64 / L;
+  const int lane = threadIdx.x & 63, l = lane % L;
+  const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * WAVES + (threadIdx.x >> 6));
+  const int token = div(wave, p.pieces);
+  if (token >= p.num_tokens) return;
+  // rows of a token: its queries, keys and (where they are written) values
+  const int row = (wave - token * p.pieces.d) * HEADS + lane / L;
+  const int keys = row - p.q_heads, values = keys - p.kv_heads;
+  if (keys >= (WRITE ? 2 : 1) * p.kv_heads) return;
+  const bool is_q = keys < 0, is_v = WRITE && values >= 0;
+  const int head = is_q ? row : is_v ? values : keys;
+  const int64_t position = p.positions[token];
+  const bool live = (uint64_t)position < (uint64_t)p.num_positions;
+  Place at;
+  bool put = false;
+  if (WRITE && !is_q) {
+    put = live && place_of(p.c, p.slots[token], head, at);
+    if (!put) return;
+  }
+  const Lane my = is_v ? Lane{16 * l, 16 * l + 8, false} : lane_of<D, INTER>(l, p.rot);
+  const Rows& from = is_q ? p.q : is_v ? p.v : p.k;
+  float x[16] = {};
+  if (live) {
+    load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
+    if (!is_v) {
+      float w[16];
+      Angles a;
+      load_weights(is_q ? p.q_weight : p.k_weight, p.weights_bf16, my, w);
+      if (my.turns) load_angles(p, position, l, a);
+      const float r = inverse_rms<D>(x, p.eps);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+      if (my.turns) turn<INTER, 1>(x, a);
+    }
+  }
+  if (WRITE && !is_q) {
+    uint32_t sf;
+    v2u codes[2];
+    encode<L>(x, codes, sf);
+    uint8_t* to = (is_v ? p.c.v : p.c.k) + at.code;
+    *(v2u*)(to + my.c0) = codes[0];
+    *(v2u*)(to + my.c1) = codes[1];
+    if (l == 0) (is_v ? p.c.v_sf : p.c.k_sf)[at.sf] = (uint8_t)sf;
+    return;
+  }
+  const Rows& to = is_q ? p.q_out : p.k_out;
+  store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+}
+
+// ---------------------------------------------------------------- backward
+template <int D, bool BF16, bool INTER>
+__global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
+  constexpr int L = D / 16, HEADS = 64 / L;
+  __shared__ float sums[2][WAVES][D];
+  const int lane = threadIdx.x & 63, l = lane % L, wave = threadIdx.x >> 6;
+  const Lane my = lane_of<D, INTER>(l, p.rot);
+#pragma unroll 1
+  for (int section = 0; section < 2; ++section) {
+    const Rows &from = section ? p.k : p.q, &grad = section ? p.dk : p.dq, &to = section ? p.k_out : p.q_out;
+    const int heads = section ? p.kv_heads : p.q_heads, pieces = (heads + HEADS - 1) / HEADS;
+    float w[16], dw[16] = {};
+    load_weights(section ? p.k_weight : p.q_weight, p.weights_bf16, my, w);
+    const int64_t items = (int64_t)p.num_tokens * pieces;
+    for (int64_t item = blockIdx.x * WAVES + wave; item < items; item += p.workgroups * WAVES) {
+      const int token = (int)(item / pieces), head = (int)(item - (int64_t)token * pieces) * HEADS + lane / L;
+      if (head >= heads) continue;
+      const int64_t position = p.positions[token];
+      float x[16] = {}, t[16] = {};
+      if ((uint64_t)position < (uint64_t)p.num_positions) {
+        Angles a;
+        load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
+        load16<BF16>(grad.p, token * grad.token_stride + head * grad.head_stride, my, t);
+        if (my.turns) load_angles(p, position, l, a);
+        const float r = inverse_rms<D>(x, p.eps);
+        if (my.turns) turn<INTER, -1>(t, a);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          x[i] *= r;
+          dw[i] = __builtin_fmaf(t[i], x[i], dw[i]);
+          t[i] *= w[i];
+          s = __builtin_fmaf(t[i], x[i], s);
+        }
+        const float mean = row_sum<L>(s) * (1.f / D);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = r * (t[i] - x[i] * mean);
+      }
+      store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+    }
+    // over the wave's rows: lanes l, l + L, ...
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+      for (int step = L; step < 64; step *= 2) dw[i] += __shfl_xor(dw[i], step);
+    }
+    if (lane < L) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sums[section][wave][(i < 8 ? my.c0 + i : my.c1 + i - 8)] = dw[i];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
+    const int section = i / D, d = i % D;
+    float s = 0.f;
+#pragma unroll
+    for (int x = 0; x < WAVES; ++x) s += sums[section][x][d];
+    if (p.workgroups == 1)
+      (section ? p.dk_weight : p.dq_weight)[d] = s;
+    else
+      p.parts[(int64_t)blockIdx.x * 2 * D + i] = s;
+  }
+}
+
+// The workgroups' sums of the weights' gradients, added up: a workgroup for 32 values.
+template <int D>
+__global__ void __launch_bounds__(1024) weights_kernel(const RopeParams p) {
+  __shared__ float sums[32][33];
+  const int i = blockIdx.x * 32 + (threadIdx.x & 31), group = threadIdx.x >> 5;
+  float s = 0.f;
+#pragma unroll 8
+  for (int b = group; b < p.workgroups; b += 32) s += p.parts[(int64_t)b * 2 * D + i];
+  sums[group][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (group) return;
+  s = 0.f;
+#pragma unroll
+  for (int x = 0; x < 32; ++x) s += sums[x][threadIdx.x];
+  (i < D ? p.dq_weight : p.dk_weight)[i % D] = s;
+}
+
+template <int D, bool BF16, bool INTER>
+hipError_t forward(const RopeParams& p, bool write, hipStream_t stream) {
+  const unsigned grid = (unsigned)(((int64_t)p.num_tokens * p.pieces.d + WAVES - 1) / WAVES);
+  if (write)
+    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, true>), dim3(grid), dim3(THREADS), 0, stream, p);
+  else
+    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, false>), dim3(grid), dim3(THREADS), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <int D, bool BF16, bool INTER>
+hipError_t backward(const RopeParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL((backward_kernel<D, BF16, INTER>), dim3(p.workgroups), dim3(THREADS), 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.workgroups == 1) return e;
+  hipLaunchKernelGGL((weights_kernel<D>), dim3(2 * D / 32), dim3(1024), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace rope
+
+#define DG_ROPE_CASES(CALL, ...)                                                                       \
+  switch (head_dim) {                                                                                  \
+    case 64: return bf16 ? (interleaved ? rope::CALL<64, true, true>(__VA_ARGS__) : rope::CALL<64, true, false>(__VA_ARGS__))    \
+                         : (interleaved ? rope::CALL<64, false, true>(__VA_ARGS__) : rope::CALL<64, false, false>(__VA_ARGS__)); \
+    case 128: return bf16 ? (interleaved ? rope::CALL<128, true, true>(__VA_ARGS__) : rope::CALL<128, true, false>(__VA_ARGS__))    \
+                          : (interleaved ? rope::CALL<128, false, true>(__VA_ARGS__) : rope::CALL<128, false, false>(__VA_ARGS__)); \
+    case 256: return bf16 ? (interleaved ? rope::CALL<256, true, true>(__VA_ARGS__) : rope::CALL<256, true, false>(__VA_ARGS__))    \
+                          : (interleaved ? rope::CALL<256, false, true>(__VA_ARGS__) : rope::CALL<256, false, false>(__VA_ARGS__)); \
+  }                                                                                                    \
+  return hipErrorInvalidValue
+
+hipError_t launch_norm_rope(const RopeParams& p, int head_dim, bool bf16, bool interleaved, bool write, hipStream_t stream) {
+  DG_ROPE_CASES(forward, p, write, stream);
+}
+hipError_t launch_norm_rope_backward(const RopeParams& p, int head_dim, bool bf16, bool interleaved, hipStream_t stream) {
+  DG_ROPE_CASES(backward, p, stream);
+}
+#undef DG_ROPE_CASES
+
+}  // namespace dg

@@ -456,6 +456,67 @@ int64_t dg_fp8_paged_attention_workspace(int32_t batch, int32_t total_q, int32_t
                                          int32_t head_dim, int32_t equal_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
                                          int32_t window, int32_t sinks);
 
+/*
+ * Norm and rotation of queries and keys, for each head.  For a row x (one token and head, D = head_dim values) with the
+ * weights w and the token's angles a_i, i < R / 2 (R = rot_dim):
+ *
+ *   y = w * x / sqrt(mean(x^2) + eps),   then for each pair of the first R values
+ *   (y_i, y_j) -> (y_i cos a_i - y_j sin a_i, y_i sin a_i + y_j cos a_i),   j = i + R / 2, or with `interleaved` the pairs (2i, 2i + 1).
+ *
+ *  num_tokens, num_q_heads, num_kv_heads, head_dim : shape; head_dim 64, 128 or 256.
+ *  dtype             : of all rows, DG_IN_BF16 or DG_IN_F32.  Rows [num_tokens, heads, head_dim] have strides in elements and
+ *                      16-byte aligned rows (start, token stride, head stride).
+ *  q_weight, k_weight: [head_dim], 16-byte aligned, weight_dtype DG_IN_BF16 or DG_IN_F32.
+ *  cos_sin           : FP32 [num_positions, rot_dim] with row stride cos_sin_stride (elements), rows 16-byte aligned: R / 2
+ *                      cosines, then R / 2 sines.  rot_dim a multiple of 16 in [16, head_dim].
+ *  positions         : device int64 [num_tokens], rows of cos_sin.  A token whose position is negative or past the table is a
+ *                      padding token: its rows come back as zeros and add nothing to the weights' gradients.
+ *  eps               : finite, not negative.
+ * Everything is computed in FP32 and rounded once.  A row's squares are summed in FP32: a row of values past 2^60 or so gives zeros.
+ */
+typedef struct {
+  int32_t num_tokens, num_q_heads, num_kv_heads, head_dim;
+  int32_t dtype, weight_dtype;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  int64_t cos_sin_stride;
+  int64_t num_positions;
+  const int64_t* positions;
+  int32_t rot_dim, interleaved;
+  float eps;
+} dg_norm_rope;
+
+/* Rows of an operand: [num_tokens, heads, head_dim], strides in elements. */
+typedef struct {
+  void* p;
+  int64_t token_stride, head_stride;
+} dg_rows;
+
+/* q_out and k_out may be q and k themselves.  num_tokens == 0 is a no-op. */
+int dg_qk_norm_rope(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows q_out, dg_rows k_out, hipStream_t stream);
+
+/*
+ * Its gradients: dq_out, dk_out (of the results) and the forward call's q and k -> dq and dk (written), and the
+ * weights' dq_weight, dk_weight: FP32 [head_dim], written, not added to (zeros where there is no token).  dq and dk may be
+ * dq_out and dk_out.  workspace: at least dg_qk_norm_rope_backward_workspace() bytes, 16-byte aligned; contents on entry do not
+ * matter.  No atomics: the same call gives the same bits (the order of sums follows from the shape and the number of compute
+ * units, dg_set_num_sms).
+ */
+int dg_qk_norm_rope_backward(const dg_norm_rope* a, dg_rows dq_out, dg_rows dk_out, dg_rows q, dg_rows k, dg_rows dq, dg_rows dk,
+                             float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+/* Bytes of its workspace (0: none), or a negative dg_status. */
+int64_t dg_qk_norm_rope_backward_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * The serving form: q -> q_out as above; the keys, normed and rotated, and the values v as they are go to the cache's
+ * `slots` as dg_fp8_kv_cache_write writes them (quantised from FP32: a key is not rounded to BF16 before).  A padding token's keys
+ * and values are not written, nor those of a slot that is negative or past the cache; no slot may be given twice.
+ * cache->head_dim and num_heads are those of `a`.
+ */
+int dg_qk_norm_rope_fp8_kv_cache_write(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows v, dg_rows q_out,
+                                       const dg_fp8_kv_cache* cache, const int64_t* slots, hipStream_t stream);
+
 /* align(mn, 16 / elem_bytes): the padded MN extent of an MN-major scale tensor whose
  * K slices start on 16-byte boundaries (page "02 · DeepGEMM 技术解析" §3.1, ALIGN_MN).
  * elem_bytes must be 1, 2, 4, 8 or 16; returns -1 otherwise. */
