@@ -28,6 +28,7 @@ __all__ = [
     "per_token_group_cast_fp8", "k_grouped_fp8_gemm_nt_contiguous", "k_grouped_fp8_gemm_tn_contiguous", "transform_sf_into_required_layout",
     "fp8_fp4_gemm_nt", "m_grouped_fp8_fp4_gemm_nt_contiguous", "m_grouped_fp8_fp4_gemm_nt_masked", "get_tma_aligned_size", "get_mk_alignment_for_contiguous_layout", "set_num_sms", "get_num_sms",
     "get_gemm_config", "fp8_kv_cache_empty", "fp8_kv_cache_write", "fp8_kv_cache_read", "fp8_paged_attention",
+    "fp8_kv_block_keys_empty", "fp8_kv_block_keys_update", "fp8_kv_select_blocks", "fp8_block_sparse_attention",
     "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_fp8_kv_cache_write", "LIB_PATH",
 ]
 
@@ -61,7 +62,13 @@ class _Rows(ctypes.Structure):
     _fields_ = [("p", _p), ("token_stride", _i64), ("head_stride", _i64)]
 
 
+class _BlockKeys(ctypes.Structure):
+    """dg_fp8_block_keys (include/dg.h)."""
+    _fields_ = [("codes", _p), ("scales", _p), ("num_pages", _i32), ("num_heads", _i32), ("head_dim", _i32)]
+
+
 _c = ctypes.POINTER(_KvCache)
+_b = ctypes.POINTER(_BlockKeys)
 _n = ctypes.POINTER(_NormRope)
 _SIGS = {
     **{f"dg_fp8_gemm_{lay}": (_i32, [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _i32,
@@ -89,6 +96,11 @@ _SIGS = {
     "dg_fp8_paged_attention": (_i32, [_c, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32,
                                       ctypes.c_float, _i32, _i32, _p, _i64, _i64, _p, _p, _i64, _p]),
     "dg_fp8_paged_attention_workspace": (_i64, [_i32] * 10),
+    "dg_fp8_kv_block_keys_update": (_i32, [_c, _b, _i32, _p, _p]),
+    "dg_fp8_kv_select_blocks": (_i32, [_b, _i32, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32, _i32, _i32, _p, _p]),
+    "dg_fp8_block_sparse_attention": (_i32, [_c, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _p, _i32, ctypes.c_float,
+                                             _p, _i64, _i64, _p, _p, _i64, _p]),
+    "dg_fp8_block_sparse_attention_workspace": (_i64, [_i32] * 9),
     "dg_qk_norm_rope": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _p]),
     "dg_qk_norm_rope_backward": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _Rows, _Rows, _p, _p, _p, _i64, _p]),
     "dg_qk_norm_rope_backward_workspace": (_i64, [_i32] * 4),
@@ -761,6 +773,146 @@ def fp8_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q
         c, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), table_stride, cols,
         seq_lens.data_ptr(), max_k, d ** -0.5 if sm_scale is None else sm_scale, window, sinks, out.data_ptr(), os_[0], os_[1],
         None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(), need, _current_stream(dev)))
+    return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- sparse attention over chosen blocks of the cache
+def fp8_kv_block_keys_empty(num_pages, num_kv_heads, head_dim, device="cuda"):
+    """Block keys of zeros: ``(codes int8 [pages, heads, head dim], scales float32 [pages, heads])``."""
+    return (torch.zeros((num_pages, num_kv_heads, head_dim), dtype=torch.int8, device=device),
+            torch.ones((num_pages, num_kv_heads), dtype=torch.float32, device=device))
+
+
+def _block_keys(block_keys):
+    """The C struct of block keys, and their shape and device."""
+    codes, scales = block_keys
+    shape, dev = codes.shape, codes.device
+    if codes.dtype != torch.int8 or len(shape) != 3 or not codes.is_contiguous():
+        raise ValueError("block keys must be contiguous int8 [pages, heads, head dim]")
+    if scales.dtype != torch.float32 or scales.shape != shape[:2] or not scales.is_contiguous() or scales.device != dev:
+        raise ValueError("block keys' scales must be contiguous float32 [pages, heads] on the codes' device")
+    if max(shape) > _INT32:
+        raise ValueError(f"block keys' dimensions must fit 32 bits, got {tuple(shape)}")
+    if dev.type != "cuda":
+        raise ValueError("the block keys must be on a GPU")
+    return _BlockKeys(codes.data_ptr(), scales.data_ptr(), *shape), shape, dev
+
+
+def fp8_kv_block_keys_update(k_cache, block_keys, pages):
+    """Block keys of pages that have filled up: for each head, the mean of the page's keys as signed 8-bit codes and a power of two.
+
+    ``k_cache``: ``(codes, scale codes)``.  ``block_keys``: as ``fp8_kv_block_keys_empty`` makes them, written in place.  ``pages``:
+    int32 vector of page numbers, in any order, the same one more than once if need be; a negative one, or one past the cache, is skipped (so a
+    step can pass one for each sequence, negative where its page is not full)."""
+    c, shape, dev = _kv_cache(k_cache, k_cache)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return fp8_kv_block_keys_update(k_cache, block_keys, pages)
+    b, _, keys_dev = _block_keys(block_keys)
+    if pages.dtype != torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous int32 vector")
+    if keys_dev != dev or pages.device != dev:
+        raise ValueError("block_keys and pages must be on the cache's GPU")
+    if pages.shape[0] > _INT32:
+        raise ValueError("the number of pages must fit 32 bits")
+    _check(lib().dg_fp8_kv_block_keys_update(c, b, pages.shape[0], pages.data_ptr(), _current_stream(dev)))
+
+
+def _sequences(q, d, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, dev):
+    """Checks what attention over chosen blocks and their choice share: (total, heads, batch, columns, row stride of the table, pointer to the first
+    rows, bound of the new tokens, whether no query can belong to a sequence)."""
+    qshape, qs = q.shape, q.stride()
+    if q.dtype != torch.bfloat16 or len(qshape) != 3 or qshape[2] != d or qs[2] != 1:
+        raise ValueError(f"q must be bfloat16 [tokens, heads, {d}], contiguous along the last dimension")
+    total, hq, _ = qshape
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch, columns]")
+    batch, cols = block_table.shape
+    ts = block_table.stride()
+    if cols > 1 and ts[1] != 1:
+        raise ValueError("block_table must be contiguous along its columns")
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens must be contiguous int32 [{batch}]")
+    if q.device != dev or block_table.device != dev or seq_lens.device != dev:
+        raise ValueError("q, block_table and seq_lens must be on the cache's GPU")
+    cu = None
+    if cu_seqlens_q is not None:
+        if (cu_seqlens_q.dtype != torch.int32 or cu_seqlens_q.shape != (batch + 1,) or not cu_seqlens_q.is_contiguous()
+                or cu_seqlens_q.device != dev):
+            raise ValueError(f"cu_seqlens_q must be contiguous int32 [{batch + 1}] on the cache's GPU")
+        cu = cu_seqlens_q.data_ptr()
+    if max(total, hq, batch, cols) > _INT32:
+        raise ValueError("q's and block_table's dimensions must fit 32 bits")
+    max_q = total if max_seqlen_q is None else _bound(max_seqlen_q)
+    # (the stride of a single row means nothing, and may be anything)
+    return total, hq, batch, cols, ts[0] if batch > 1 else cols, cu, max_q, batch == 0 or (cu is not None and max_q == 0)
+
+
+def fp8_kv_select_blocks(q, block_keys, block_table, seq_lens, page_size, top, first=1, last=1, cu_seqlens_q=None, max_seqlen_q=None, out=None):
+    """Blocks (pages) for each sequence's newest tokens to attend to: int32 [total tokens, kv heads, ``top``], block numbers of the
+    sequence (columns of ``block_table``), ascending, then -1.
+
+    A token gets the first ``first`` blocks, the last ``last`` (its own among them, so at least 1), and those between whose block keys
+    score highest against its query, equal scores by lower index; all blocks where there are no more than ``top``.  A block's score is the
+    largest, over the query heads that share a key head, of the product of the query in 8-bit codes and the block key: exact, so the
+    choice is the same in any call that has the token.
+
+    ``q``, ``block_table``, ``seq_lens``, ``cu_seqlens_q``, ``max_seqlen_q``: as for ``fp8_paged_attention``; the table has at most 32768 columns.
+    ``block_keys``: up to date for all full pages before a token's own.  Only rows of a sequence are written (all -1 where no sequence
+    can have a row)."""
+    b, shape, dev = _block_keys(block_keys)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return fp8_kv_select_blocks(q, block_keys, block_table, seq_lens, page_size, top, first, last, cu_seqlens_q, max_seqlen_q, out)
+    _, hk, d = shape
+    total, hq, batch, cols, ts, cu, max_q, blind = _sequences(q, d, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, dev)
+    want = (total, hk, int(top))
+    if want[2] < 1 or max(want[2], int(page_size), int(first), int(last)) > _INT32:
+        raise ValueError("top must be positive, and top, page_size, first and last fit 32 bits")
+    if out is None:
+        out = torch.full(want, -1, dtype=torch.int32, device=dev) if blind else torch.empty(want, dtype=torch.int32, device=dev)
+    elif out.dtype != torch.int32 or tuple(out.shape) != want or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be contiguous int32 {list(want)} on the block keys' GPU")
+    qs = q.stride()
+    _check(lib().dg_fp8_kv_select_blocks(b, page_size, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts, cols,
+                                         seq_lens.data_ptr(), want[2], first, last, out.data_ptr(), _current_stream(dev)))
+    return out
+
+
+def fp8_block_sparse_attention(q, k_cache, v_cache, block_table, seq_lens, blocks, cu_seqlens_q=None, max_seqlen_q=None, sm_scale=None, out=None,
+                               return_lse=False):
+    """``fp8_paged_attention`` in which a token sees, for each key head, only the keys of the blocks (pages) that ``blocks`` lists, up to its own place.
+
+    ``blocks``: int32 [total tokens, kv heads, top], contiguous, as ``fp8_kv_select_blocks`` gives them or from elsewhere: numbers of blocks in the
+    token's sequence, strictly ascending, then negative ones.  Every other argument, and what is returned, is as there."""
+    c, shape, dev = _kv_cache(k_cache, v_cache)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return fp8_block_sparse_attention(q, k_cache, v_cache, block_table, seq_lens, blocks, cu_seqlens_q, max_seqlen_q, sm_scale, out, return_lse)
+    _, hk, page, d = shape
+    total, hq, batch, cols, ts, cu, max_q, blind = _sequences(q, d, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, dev)
+    if blocks.dtype != torch.int32 or blocks.dim() != 3 or blocks.shape[:2] != (total, hk) or not blocks.is_contiguous() or blocks.device != dev:
+        raise ValueError(f"blocks must be contiguous int32 [{total}, {hk}, top] on the cache's GPU")
+    top = blocks.shape[2]
+    if top > _INT32:
+        raise ValueError("top must fit 32 bits")
+    if out is None:
+        out = (torch.zeros_like if blind else torch.empty_like)(q, memory_format=torch.contiguous_format)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or out.stride(2) != 1 or out.device != dev:
+        raise ValueError("out must be bfloat16 of q's shape, contiguous along the last dimension, on the cache's GPU")
+    lse = torch.empty((total, hq), dtype=torch.float32, device=dev) if return_lse else None
+    if blind and return_lse:
+        lse.fill_(float("-inf"))
+    handle = lib()
+    need = handle.dg_fp8_block_sparse_attention_workspace(batch, total, hq, hk, d, cu is None, max_q, page, top)
+    if need < 0:
+        _check(need)
+    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    qs, os_ = q.stride(), out.stride()
+    _check(handle.dg_fp8_block_sparse_attention(
+        c, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts, cols, seq_lens.data_ptr(), blocks.data_ptr(), top,
+        d ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
+        None if work is None else work.data_ptr(), need, _current_stream(dev)))
     return (out, lse) if return_lse else out
 
 

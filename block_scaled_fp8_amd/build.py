@@ -94,10 +94,10 @@ def build(verbose=False, jobs=None):
                   "-o", os.path.join(bdir, "dg_quant.o")])
     # (dg_attention: MFMA results in VGPRs here too, where the softmax reads them; without it the
     # compiler moves them through accumulation registers and spills at head_dim 256)
-    for name in ("dg_kv_cache", "dg_attention", "dg_rope"):
+    for name in ("dg_kv_cache", "dg_attention", "dg_rope", "dg_blocks", "dg_sparse"):
         steps.append([HIPCC, *FLAGS, "-mllvm", "-amdgpu-mfma-vgpr-form", "-Rpass-analysis=kernel-resource-usage", "-c", os.path.join(CSRC, name + ".hip"),
                       "-o", os.path.join(bdir, name + ".o")])
-    for name in ("dg_api", "dg_api_kv", "dg_api_rope"):
+    for name in ("dg_api", "dg_api_kv", "dg_api_rope", "dg_api_sparse"):
         steps.append([HIPCC, "-O2", "-std=c++20", "-fPIC", f"--offload-arch={ARCH}", "-c", os.path.join(CSRC, name + ".cpp"),
                       "-o", os.path.join(bdir, name + ".o")])
     jobs = jobs or min(16, os.cpu_count() or 4)

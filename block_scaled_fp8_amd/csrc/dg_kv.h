@@ -110,6 +110,67 @@ struct AttnParams {
   int32_t* item_end;         // [items] a head's parts up to and with each item
 };
 
+// A page's block key, for each head: int8 codes [pages, heads, head dim] and a power of two [pages, heads].
+struct BlockKeys {
+  int8_t* codes;
+  float* scales;
+};
+
+struct BlockKeysParams {
+  KvCache c;  // (keys only)
+  BlockKeys b;
+  const int32_t* pages;
+  int32_t num_pages;  // entries of `pages`
+};
+hipError_t launch_block_keys(const BlockKeysParams& p, int head_dim, hipStream_t stream);
+
+// The newest tokens of sequences, as attention over chosen blocks sees them.
+struct Sequences {
+  const uint16_t* q;
+  int64_t q_token_stride, q_head_stride;
+  const int32_t* table;      // [batch, table_cols]
+  int64_t table_stride;
+  const int32_t* seq_lens;   // [batch]
+  const int32_t* cu_q;       // nullptr: every sequence has q_per_seq queries
+  int32_t table_cols, batch, total_q, q_per_seq, num_q_heads;
+};
+
+struct SelectParams {
+  Sequences s;
+  BlockKeys b;
+  int32_t num_pages, num_heads;  // of the block keys
+  FastDiv page;                  // tokens of a block
+  int32_t top, first, last;
+  FastDiv group;                 // query heads per key head
+  FastDiv q_tiles;               // tiles of tokens per sequence
+  int32_t tile_tokens, items;    // tokens of a tile; batch * q_tiles
+  int32_t row_words;             // LDS words of a token's scores
+  int32_t waves;
+  int32_t* out;                  // [total_q, heads, top]
+};
+// tiles of 16 columns (a token's heads, rounded up to a power of two) of a workgroup: their codes stay in registers
+constexpr int select_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
+hipError_t launch_select_blocks(const SelectParams& p, int head_dim, hipStream_t stream);
+
+struct SparseParams {
+  Sequences s;
+  KvCache c;
+  const int32_t* blocks;     // [total_q, heads, top]
+  uint16_t* out;
+  int64_t o_token_stride, o_head_stride;
+  float* lse;                // nullptr, or [total_q, query heads]
+  float scale_log2;          // softmax scale * log2(e)
+  int32_t top;
+  FastDiv list;              // `top` as a divisor
+  FastDiv group;             // query heads per key head
+  FastDiv q_tiles;           // tiles of tokens per sequence
+  int32_t tile_tokens, head_tiles, items;  // tokens of a tile, tiles of 16 heads of a token (one of the two is 1), batch * q_tiles
+  int32_t parts;             // workgroups that share a tile and key head (a power of two)
+  float* part_o;             // [items, heads, head_tiles, parts, 16, head dim] (parts > 1)
+  float* part_mz;            // [.., 16, 2]
+};
+hipError_t launch_sparse_attention(const SparseParams& p, int head_dim, hipStream_t stream);
+
 // The kernels: four waves over the same 16 or 32 query rows, or waves of 32 rows each.
 enum AttnForm { ATTN_NARROW_16 = 0, ATTN_NARROW_32 = 1, ATTN_WIDE = 2 };
 // The many-rows kernel deals the pieces of up to so many items by size, and cuts items of such calls only: a

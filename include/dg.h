@@ -457,6 +457,69 @@ int64_t dg_fp8_paged_attention_workspace(int32_t batch, int32_t total_q, int32_t
                                          int32_t window, int32_t sinks);
 
 /*
+ * Sparse attention over blocks that a cheap score selects for each query: for long contexts, of which a query then reads a few
+ * thousand keys.  A block is a page of the cache.  Three calls:
+ *  - dg_fp8_kv_block_keys_update, when pages have filled up: their block keys.
+ *  - dg_fp8_kv_select_blocks: for each new token and key head, a list of blocks.
+ *  - dg_fp8_block_sparse_attention: causal attention over the keys of these blocks (any lists will do).
+ *
+ * A page's block key is, for each head, the mean of its keys (as the cache holds them) in signed 8-bit codes under a power of two s, the
+ * smallest with |mean| <= 127 s (at least 2^-126; 1 for zeros): code = mean / s rounded to nearest, ties to even.
+ *  codes  : int8 [num_pages, num_heads, head_dim], contiguous, 16-byte aligned.
+ *  scales : FP32 [num_pages, num_heads], contiguous.
+ */
+typedef struct {
+  int8_t* codes;
+  float* scales;
+  int32_t num_pages, num_heads, head_dim;
+} dg_fp8_block_keys;
+
+/*
+ * Block keys of `pages` (device int32 [num_entries]; an entry that is negative or past the cache is skipped, one may be given
+ * twice): of all page_size places, so of pages that are full.  The cache's values are not read (v and v_sf may be NULL).  A NaN among the keys counts as zero.
+ * The mean is taken in 64 bits: exact where a page's scales are less than 2^25 apart.  num_entries == 0 is a no-op.
+ */
+int dg_fp8_kv_block_keys_update(const dg_fp8_kv_cache* cache, const dg_fp8_block_keys* keys, int32_t num_entries, const int32_t* pages,
+                                hipStream_t stream);
+
+/*
+ * Choose `top` blocks for each new token and key head.  A token at place x has the own block x / page_size.  It gets the first `first`
+ * blocks and the last `last` (its own, and those before it), and of the ones between, by score, so many that there are `top`, equal
+ * scores by lower index; all of its blocks where there are no more than that.  A block's score: the query's codes, made like a block key's for each query
+ * head (s = smallest power of two with max|q| <= 127 s; infinities and NaN count as zeros), times the block's: an integer; as FP32, times
+ * the block's scale, times the query's; the largest over the query heads that share the key head.  No rounding enters
+ * (short of FP32's range), so the choice depends on nothing else.
+ *
+ *  page_size, batch, total_q, num_q_heads, q, cu_seqlens_q, max_seqlen_q, block_table, table_stride, table_cols, seq_lens :
+ *           as in dg_fp8_paged_attention.  table_cols <= 32768 (DG_ERR_UNSUPPORTED beyond).  An entry outside the block keys scores as page 0.
+ *  first >= 0, last >= 1, first + last <= top <= 2^20.
+ *  blocks : int32 [total_q, keys->num_heads, top], contiguous: numbers of blocks in the sequence (columns of block_table), ascending, then
+ *           -1 up to `top`.  Rows of no sequence are not written.
+ */
+int dg_fp8_kv_select_blocks(const dg_fp8_block_keys* keys, int32_t page_size, int32_t batch, int32_t total_q, int32_t num_q_heads,
+                            const void* q, int64_t q_token_stride, int64_t q_head_stride, const int32_t* cu_seqlens_q, int32_t max_seqlen_q,
+                            const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* seq_lens, int32_t top,
+                            int32_t first, int32_t last, int32_t* blocks, hipStream_t stream);
+
+/*
+ * Causal attention of each sequence's newest tokens over chosen blocks: as dg_fp8_paged_attention (arguments, numerics, rows that
+ * are written, values that are no numbers), but a query at place x sees the keys j <= x of the blocks that blocks[token, key head] lists.
+ *  blocks : device int32 [total_q, cache->num_heads, top], contiguous: block numbers, strictly ascending, negative ones
+ *           at the end only.  (What is not so gives wrong sums, but reads nothing outside the cache.)  Blocks past the query's
+ *           place, and past the table, hold nothing that it sees.  A query without a key gives zeros and lse = -infinity.
+ * The same call gives the same results in every run (no atomics); a token's last bits depend on the shape of the call and the lists of
+ * the tokens beside it.
+ */
+int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, int32_t total_q, int32_t num_q_heads, const void* q,
+                                  int64_t q_token_stride, int64_t q_head_stride, const int32_t* cu_seqlens_q, int32_t max_seqlen_q,
+                                  const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* seq_lens,
+                                  const int32_t* blocks, int32_t top, float sm_scale, void* out, int64_t o_token_stride,
+                                  int64_t o_head_stride, float* lse, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+/* Its workspace in bytes (0: none), or a negative dg_status.  equal_q: 1 where cu_seqlens_q is NULL. */
+int64_t dg_fp8_block_sparse_attention_workspace(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                int32_t equal_q, int32_t max_seqlen_q, int32_t page_size, int32_t top);
+
+/*
  * Norm and rotation of queries and keys, for each head.  For a row x (one token and head, D = head_dim values) with the
  * weights w and the token's angles a_i, i < R / 2 (R = rot_dim):
  *

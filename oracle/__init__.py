@@ -29,15 +29,17 @@ Modules:
   quant   -- the per-token-group FP8 cast (E4M3 codes and 1x128 FP32 scales)
   kv_cache -- the FP8 key/value cache (encode, write, read) and causal attention over its pages,
              with a window and first tokens that stay visible
+  blocks  -- block keys, the choice of blocks by them, and attention over chosen blocks
   rope    -- norm and rotation of queries and keys, and its gradients
 
 Parity pins: every function here is pinned by a `-m "not gpu"` test in
-``tests/test_oracle_pins.py``, ``tests/test_kv_host.py`` or ``tests/test_rope_host.py`` against something other than itself (closed
+``tests/test_oracle_pins.py``, ``tests/test_kv_host.py``, ``tests/test_rope_host.py`` or
+``tests/test_sparse_host.py`` against something other than itself (closed
 forms, worked examples printed on the pages, exact rational brute force,
 library routines on special cases).  No function is "parity unpinned"; the
 comparison with the original CUDA library itself cannot be made here.
 """
-from . import codecs, layout, gemm, quant, kv_cache, rope  # noqa: F401
+from . import codecs, layout, gemm, quant, kv_cache, blocks, rope  # noqa: F401
 from .codecs import (e4m3_decode_table, e4m3_decode, ue8m0_encode, ue8m0_decode,
                      bf16_rne, bf16_bits_to_f64, pow2_violation, e2m1_decode_table, e2m1_decode,
                      unpack_fp4)  # noqa: F401
@@ -49,3 +51,4 @@ from .gemm import (gemm_nt, gemm_nt_points, grouped_contiguous, grouped_masked, 
 from .quant import e4m3_encode_rne, per_token_group_cast  # noqa: F401
 from .kv_cache import kv_encode, kv_decode, kv_write, kv_read, visible, paged_attention  # noqa: F401
 from .rope import norm_rope, norm_rope_backward  # noqa: F401
+from .blocks import block_keys, select_blocks, block_sparse_attention  # noqa: F401
