@@ -97,7 +97,8 @@ _SIGS = {
                                       ctypes.c_float, _i32, _i32, _p, _i64, _i64, _p, _p, _i64, _p]),
     "dg_fp8_paged_attention_workspace": (_i64, [_i32] * 10),
     "dg_fp8_kv_block_keys_update": (_i32, [_c, _b, _i32, _p, _p]),
-    "dg_fp8_kv_select_blocks": (_i32, [_b, _i32, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32, _i32, _i32, _p, _p]),
+    "dg_fp8_kv_select_blocks": (_i32, [_b, _i32, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _i32, _i32, _i32, _p, _p, _i64, _p]),
+    "dg_fp8_kv_select_blocks_workspace": (_i64, [_i32] * 11),
     "dg_fp8_block_sparse_attention": (_i32, [_c, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _p, _i32, ctypes.c_float,
                                              _p, _i64, _i64, _p, _p, _i64, _p]),
     "dg_fp8_block_sparse_attention_workspace": (_i64, [_i32] * 9),
@@ -873,9 +874,15 @@ def fp8_kv_select_blocks(q, block_keys, block_table, seq_lens, page_size, top, f
         out = torch.full(want, -1, dtype=torch.int32, device=dev) if blind else torch.empty(want, dtype=torch.int32, device=dev)
     elif out.dtype != torch.int32 or tuple(out.shape) != want or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be contiguous int32 {list(want)} on the block keys' GPU")
+    handle = lib()
+    need = handle.dg_fp8_kv_select_blocks_workspace(batch, total, hq, hk, d, cu is None, max_q, cols, want[2], first, last)
+    if need < 0:
+        _check(need)
+    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     qs = q.stride()
-    _check(lib().dg_fp8_kv_select_blocks(b, page_size, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts, cols,
-                                         seq_lens.data_ptr(), want[2], first, last, out.data_ptr(), _current_stream(dev)))
+    _check(handle.dg_fp8_kv_select_blocks(b, page_size, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts, cols,
+                                          seq_lens.data_ptr(), want[2], first, last, out.data_ptr(), None if work is None else work.data_ptr(), need,
+                                          _current_stream(dev)))
     return out
 
 

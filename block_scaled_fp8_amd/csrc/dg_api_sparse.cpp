@@ -18,6 +18,9 @@ constexpr int32_t kMaxTop = 1 << 20;
 // A workgroup keeps the scores of a token's blocks in LDS (160 KiB).
 constexpr int32_t kMaxColumns = 32768;
 
+// The lists of a tile of several tokens lie in LDS: 16 KiB at most.
+constexpr int64_t kMaxListed = 4096;
+
 int check_block_keys(const dg_fp8_block_keys* b, bool empty) {
   if (!b) return api_fail(DG_ERR_NULL, "block keys must not be NULL");
   if (b->head_dim != 64 && b->head_dim != 128 && b->head_dim != 256)
@@ -96,16 +99,18 @@ int check_grid(const Batch& a, int64_t workgroups, int threads) {
   return DG_OK;
 }
 
-// Choosing: tokens of a workgroup.
+// Choosing: tokens of a workgroup, its waves, and workgroups that share the blocks.
 struct SelectPlan {
   int64_t tile_tokens, items, row_words;
+  bool one_tile;
+  int waves, parts;
 };
-SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, int32_t table_cols, int32_t first, int32_t last, int num_sms) {
+SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, int32_t table_cols, int32_t top, int32_t first, int32_t last, int num_sms) {
   const int32_t group = a.num_q_heads / num_kv_heads;
   const int width = group > 8 ? 16 : group > 4 ? 8 : group > 2 ? 4 : group;  // columns of a token
   SelectPlan pl;
-  const int64_t scored = table_cols - first - last;
-  pl.row_words = ceil_div(scored > 0 ? scored : 1, 16) * 16 + 4;
+  const int64_t scored = table_cols > top ? table_cols - first - last : 1;
+  pl.row_words = ceil_div(scored, 16) * 16 + 4;
   // Scores of up to 64 KiB, so that two workgroups share a compute unit.
   const int64_t fit = 65536 / (4 * pl.row_words), per_tile = 16 / width;
   pl.tile_tokens = per_tile * dg::select_tiles(head_dim);
@@ -113,7 +118,29 @@ SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
                                 a.batch * ceil_div(a.most_tokens(), pl.tile_tokens) * num_kv_heads < num_sms))
     pl.tile_tokens /= 2;
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
+  pl.one_tile = pl.tile_tokens <= per_tile;
+  pl.waves = pl.one_tile && head_dim != 256 && scored > 512 ? 16 : 8;
+  pl.parts = 1;
+  // Few tiles of many blocks: a workgroup for each 256 blocks.
+  const int64_t tiles = pl.items * num_kv_heads;
+  if (pl.one_tile && scored > 512 && 4 * tiles <= num_sms) {
+    pl.waves = 8;
+    const int64_t by_blocks = ceil_div(scored, 256), by_units = num_sms / tiles;
+    pl.parts = int(by_blocks < by_units ? by_blocks : by_units);
+  }
   return pl;
+}
+int64_t select_workspace(const SelectPlan& pl, int32_t num_kv_heads) {
+  return pl.parts > 1 ? pl.items * num_kv_heads * pl.tile_tokens * pl.row_words * int64_t(sizeof(uint32_t)) : 0;
+}
+int check_choice(int32_t top, int32_t first, int32_t last) {
+  if (first < 0 || last < 1 || first > top || last > top - first)
+    return api_fail(DG_ERR_SHAPE, "first = %d must not be negative, last = %d at least 1, and both together at most top = %d", first, last, top);
+  return DG_OK;
+}
+int check_columns(int32_t table_cols) {
+  if (table_cols > kMaxColumns) return api_fail(DG_ERR_UNSUPPORTED, "table_cols = %d: sequences of up to %d blocks are supported", table_cols, kMaxColumns);
+  return DG_OK;
 }
 
 // Attention: tokens of a tile, and workgroups that share its keys.
@@ -124,6 +151,7 @@ SparsePlan sparse_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
   const int32_t group = a.num_q_heads / num_kv_heads;
   SparsePlan pl;
   pl.tile_tokens = group > 16 ? 1 : 16 / group;
+  if (pl.tile_tokens * top > kMaxListed) pl.tile_tokens = top < kMaxListed ? kMaxListed / top : 1;
   pl.head_tiles = ceil_div(group, 16);
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
   const int64_t with_rows = a.total_q / pl.tile_tokens + a.batch;  // of the items, at most
@@ -172,26 +200,43 @@ int dg_fp8_kv_block_keys_update(const dg_fp8_kv_cache* cache, const dg_fp8_block
   return api_ok();
 }
 
+int64_t dg_fp8_kv_select_blocks_workspace(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t equal_q, int32_t max_seqlen_q, int32_t table_cols, int32_t top, int32_t first, int32_t last) {
+  const Batch a{batch, total_q, num_q_heads, max_seqlen_q, equal_q != 0};
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return api_fail(DG_ERR_UNSUPPORTED, "head_dim = %d: 64, 128 and 256 are supported", head_dim);
+  if (int s = check_batch(a, num_kv_heads, top)) return s;
+  if (table_cols < 0) return api_fail(DG_ERR_LAYOUT, "table_cols = %d must not be negative", table_cols);
+  if (int s = check_choice(top, first, last)) return s;
+  if (int s = check_columns(table_cols)) return s;
+  if (a.empty()) return 0;
+  const int num_sms = dg::api_num_sms();
+  if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
+  return select_workspace(select_plan(a, num_kv_heads, head_dim, table_cols, top, first, last, num_sms), num_kv_heads);
+}
+
 int dg_fp8_kv_select_blocks(const dg_fp8_block_keys* keys, int32_t page_size, int32_t batch, int32_t total_q, int32_t num_q_heads,
                             const void* q, int64_t q_token_stride, int64_t q_head_stride, const int32_t* cu_seqlens_q, int32_t max_seqlen_q,
                             const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* seq_lens, int32_t top,
-                            int32_t first, int32_t last, int32_t* blocks, hipStream_t stream) {
+                            int32_t first, int32_t last, int32_t* blocks, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   const Batch a{batch, total_q, num_q_heads, max_seqlen_q, cu_seqlens_q == nullptr};
   if (int s = check_block_keys(keys, a.empty())) return s;
   if (int s = check_batch(a, keys->num_heads, top)) return s;
   if (page_size <= 0) return api_fail(DG_ERR_SHAPE, "page_size = %d must be positive", page_size);
-  if (first < 0 || last < 1 || first > top || last > top - first)
-    return api_fail(DG_ERR_SHAPE, "first = %d must not be negative, last = %d at least 1, and both together at most top = %d", first, last, top);
+  if (int s = check_choice(top, first, last)) return s;
   if (int s = check_table(table_cols, table_stride, page_size)) return s;
-  if (table_cols > kMaxColumns) return api_fail(DG_ERR_UNSUPPORTED, "table_cols = %d: sequences of up to %d blocks are supported", table_cols, kMaxColumns);
+  if (int s = check_columns(table_cols)) return s;
   if (a.empty()) return api_ok();
   if (int s = check_sequences(q, q_token_stride, q_head_stride, cu_seqlens_q, block_table, table_cols, seq_lens, blocks)) return s;
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
-  const SelectPlan pl = select_plan(a, keys->num_heads, keys->head_dim, table_cols, first, last, num_sms);
+  const SelectPlan pl = select_plan(a, keys->num_heads, keys->head_dim, table_cols, top, first, last, num_sms);
+  if (int s = check_grid(a, pl.items * keys->num_heads, pl.waves * 64)) return s;
+  const int64_t need = select_workspace(pl, keys->num_heads);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);
+  if (need > 0 && !aligned(workspace, 16)) return api_fail(DG_ERR_LAYOUT, "workspace must be 16-byte aligned");
   dg::SelectParams p{};
-  p.waves = 8;
-  if (int s = check_grid(a, pl.items * keys->num_heads, p.waves * 64)) return s;
   p.s = sequences(a, q, q_token_stride, q_head_stride, cu_seqlens_q, block_table, table_stride, table_cols, seq_lens);
   p.b = {keys->codes, keys->scales};
   p.num_pages = keys->num_pages;
@@ -205,8 +250,11 @@ int dg_fp8_kv_select_blocks(const dg_fp8_block_keys* keys, int32_t page_size, in
   p.tile_tokens = int32_t(pl.tile_tokens);
   p.items = int32_t(pl.items);
   p.row_words = int32_t(pl.row_words);
+  p.waves = pl.waves;
+  p.parts = pl.parts;
+  p.scores = static_cast<uint32_t*>(workspace);
   p.out = blocks;
-  const hipError_t e = dg::launch_select_blocks(p, keys->head_dim, stream);
+  const hipError_t e = dg::launch_select_blocks(p, keys->head_dim, pl.one_tile, stream);
   if (e != hipSuccess) return api_fail(DG_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   return api_ok();
 }
@@ -241,7 +289,7 @@ int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, i
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
   const SparsePlan pl = sparse_plan(a, cache->num_heads, cache->head_dim, cache->page_size, top, num_sms);
-  if (int s = check_grid(a, pl.items * cache->num_heads * pl.head_tiles * (pl.parts > 4 ? pl.parts : 4), 256)) return s;
+  if (int s = check_grid(a, pl.items * cache->num_heads * pl.head_tiles * (pl.parts > 16 ? pl.parts : 16), 256)) return s;
   const int64_t need = workspace_of(pl, cache->num_heads, cache->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);

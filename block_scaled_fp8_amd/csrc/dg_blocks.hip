@@ -92,8 +92,12 @@ __global__ void __launch_bounds__(KEYS_WAVES * 64) block_keys_kernel(const Block
 // A workgroup has a tile of tokens of one sequence and a key head.  Its waves score the blocks between the first and the last
 // ones, 16 at a time: S = K Q^T on the 16 x 16 x 64 integer matrix instruction, a block key straight from memory into operand registers, the queries'
 // codes as its 16 columns: a token takes 1, 2, 4, 8 or 16 of them (its group's heads, rounded up; more heads go 16 after 16).  The
-// largest over a token's columns goes to LDS as a number that compares like the score.  Then a wave has a token:
-// it finds the largest threshold that enough scores reach, bit by bit, and writes the chosen blocks in order.
+// largest over a token's columns goes to LDS as a number that compares like the score.  Then a wave has a token: it
+// finds the largest threshold that enough scores reach by bisection, a compare and a population count for 64 of them, and writes
+// the chosen blocks in order.
+//
+// Few sequences with many blocks leave most of the chip idle in that form.  There the scores go to memory, a slice of
+// the blocks to a workgroup, and a second kernel with a wave for each token and key head chooses.
 
 // The order of floats as unsigned numbers, none of which is 0.
 __device__ __forceinline__ uint32_t sortable(float x) {
@@ -134,80 +138,117 @@ __device__ __forceinline__ uint32_t largest(v4u a) {
   return m;
 }
 
-template <int D>
-__global__ void __launch_bounds__(512) select_kernel(const SelectParams p) {
-  constexpr int Y = D / 64, TILES = select_tiles(D);
-  extern __shared__ __attribute__((aligned(16))) uint32_t scores[];  // [tile_tokens][row_words]
-  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), g = lane >> 4, col = lane & 15;
-  const int kv_head = blockIdx.x % p.num_heads, rank = blockIdx.x / p.num_heads;
-  const int seq = rank % p.s.batch, tile = p.q_tiles.d - 1 - rank / p.s.batch;
-  // the tile's tokens and their places
-  int first_row, n;
+// A tile's tokens.
+struct Tokens {
+  int seq, kv_head;
+  int first_row, tokens;  // packed row of the first one, and how many there are
+  int place0;             // place of the first one (negative where queries exceed the context)
+  int64_t slot;           // number of the tile and key head
+};
+// Tile `id` of those of a launch; false if it has no tokens.
+__device__ __forceinline__ bool get_tokens(const SelectParams& p, int id, Tokens& t) {
+  // with the key head as the fastest index, and a multiple of eight heads, those of a head land on one XCD
+  const int rank = id / p.num_heads;
+  t.kv_head = id % p.num_heads;
+  t.seq = rank % p.s.batch;
+  const int tile = p.q_tiles.d - 1 - rank / p.s.batch;
+  int n;
   if (p.s.cu_q) {
-    const int a = uniform(p.s.cu_q[seq]), b = uniform(p.s.cu_q[seq + 1]);
-    first_row = min(max(a, 0), p.s.total_q);
-    n = min(max(b, first_row), p.s.total_q) - first_row;
+    const int a = uniform(p.s.cu_q[t.seq]), b = uniform(p.s.cu_q[t.seq + 1]);
+    t.first_row = min(max(a, 0), p.s.total_q);
+    n = min(max(b, t.first_row), p.s.total_q) - t.first_row;
   } else {
-    first_row = seq * p.s.q_per_seq;
+    t.first_row = t.seq * p.s.q_per_seq;
     n = p.s.q_per_seq;
   }
-  const int t0 = tile * p.tile_tokens, tokens = min(p.tile_tokens, n - t0);
-  if (tokens <= 0) return;
-  const int ctx = min(max(uniform(p.s.seq_lens[seq]), 0), p.s.table_cols * p.page.d);
-  const int place0 = ctx - n + t0;  // of the tile's first token
-  // blocks that are scored: of the tile's last token
-  const int last_place = place0 + tokens - 1, own = last_place >= 0 ? div(last_place, p.page) : -1;
-  const int lo = p.first, hi = own + 1 - p.last;
-  const int32_t* table = p.s.table + seq * p.s.table_stride;
-  if (own + 1 > p.top) {
-    const int width = p.group.d > 8 ? 16 : p.group.d > 4 ? 8 : p.group.d > 2 ? 4 : p.group.d;  // columns of a token
-    const int per_tile = 16 / width, tiles = (tokens + per_tile - 1) / per_tile;
-    for (int head0 = 0; head0 < p.group.d; head0 += 16) {
-      v4u q[TILES][Y];
-      float sq[TILES];
+  const int t0 = tile * p.tile_tokens;
+  t.tokens = min(p.tile_tokens, n - t0);
+  t.first_row += t0;
+  const int ctx = min(max(uniform(p.s.seq_lens[t.seq]), 0), p.s.table_cols * p.page.d);
+  t.place0 = ctx - n + t0;
+  t.slot = id;
+  return t.tokens > 0;
+}
+// Blocks up to and with a place's own.
+__device__ __forceinline__ int blocks_to(const SelectParams& p, int place) { return place >= 0 ? div(place, p.page) + 1 : 0; }
+
+// Scores of blocks [lo, hi) by the tile's tokens, of which this is the part `part` of `parts` (of 16 blocks at a time, in turn for the waves of all
+// parts), to rows of p.row_words numbers from block `base` on.
+template <int D, int TILES>
+__device__ __forceinline__ void score(const SelectParams& p, const Tokens& t, int base, int lo, int hi, int part, int parts, uint32_t* scores,
+                                      v4u (&codes)[TILES][D / 64][64], float (&query_scales)[TILES][16]) {
+  // AHEAD groups of 16 blocks at a time: their pages' loads go out together, then their keys'
+  constexpr int Y = D / 64, AHEAD = TILES > 1 || D == 256 ? 2 : 4;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), g = lane >> 4, col = lane & 15;
+  const int width = p.group.d > 8 ? 16 : p.group.d > 4 ? 8 : p.group.d > 2 ? 4 : p.group.d;  // columns of a token
+  const int per_tile = 16 / width, tiles = (t.tokens + per_tile - 1) / per_tile;
+  const int32_t* table = p.s.table + t.seq * p.s.table_stride;
+  const int first = lo + 16 * (part * p.waves + wave), step = 16 * p.waves * parts;
+  int pages[AHEAD];
+  auto load_pages = [&](int b0) {
 #pragma unroll
-      for (int c = 0; c < TILES; ++c) {
-        const int token = c * per_tile + col / width, h = head0 + col % width;
-        const bool live = token < tokens && h < p.group.d;
-        const uint16_t* src = p.s.q + (first_row + t0 + min(token, tokens - 1)) * p.s.q_token_stride +
-                              (kv_head * p.group.d + min(h, p.group.d - 1)) * p.s.q_head_stride + 16 * g;
-        v4u x[Y][2];
-        uint32_t m = 0;
+    for (int a = 0; a < AHEAD; ++a) pages[a] = table[min(b0 + step * a + col, hi - 1)];
+  };
+  for (int head0 = 0; head0 < p.group.d; head0 += 16) {
+    if (head0) __syncthreads();
+    load_pages(first);
+    for (int c = wave; c < tiles; c += p.waves) {
+      const int token = c * per_tile + col / width, h = head0 + col % width;
+      const bool live = token < t.tokens && h < p.group.d;
+      const uint16_t* src = p.s.q + (t.first_row + min(token, t.tokens - 1)) * p.s.q_token_stride +
+                            (t.kv_head * p.group.d + min(h, p.group.d - 1)) * p.s.q_head_stride + 16 * g;
+      v4u x[Y][2];
+      uint32_t m = 0;
 #pragma unroll
-        for (int y = 0; y < Y; ++y) {
-          x[y][0] = x[y][1] = (v4u){0, 0, 0, 0};
-          if (c < tiles) {
-            x[y][0] = *(const v4u*)(src + 64 * y);
-            x[y][1] = *(const v4u*)(src + 64 * y + 8);
-          }
-          m = max(m, max(largest(x[y][0]), largest(x[y][1])));
-        }
-        m = __float_as_uint(attn::groups_max(__uint_as_float(m)));
-        const uint32_t e = m ? max((int)(m >> 23) - 6 + ((m & 0x7FFFFFu) > 0x7E0000u ? 1 : 0), 1) : 127u;
-        const float inv = __uint_as_float((254u - e) << 23);
-        sq[c] = live ? __uint_as_float(e << 23) : attn::NEG_INF;
-#pragma unroll
-        for (int y = 0; y < Y; ++y) q[c][y] = to_codes(x[y][0], x[y][1], inv);
+      for (int y = 0; y < Y; ++y) {
+        x[y][0] = *(const v4u*)(src + 64 * y);
+        x[y][1] = *(const v4u*)(src + 64 * y + 8);
+        m = max(m, max(largest(x[y][0]), largest(x[y][1])));
       }
-      for (int b0 = lo + 16 * wave; b0 < hi; b0 += 16 * p.waves) {
-        int page = table[min(b0 + col, hi - 1)];
-        if ((unsigned)page >= (unsigned)p.num_pages) page = 0;
-        const int64_t at = (int64_t)page * p.num_heads + kv_head;
-        const int8_t* key = p.b.codes + at * D + 16 * g;
-        v4u k[Y];
+      m = __float_as_uint(attn::groups_max(__uint_as_float(m)));
+      const uint32_t e = m ? max((int)(m >> 23) - 6 + ((m & 0x7FFFFFu) > 0x7E0000u ? 1 : 0), 1) : 127u;
+      const float inv = __uint_as_float((254u - e) << 23);
+      if (g == 0) query_scales[c][col] = live ? __uint_as_float(e << 23) : attn::NEG_INF;
 #pragma unroll
-        for (int y = 0; y < Y; ++y) k[y] = *(const v4u*)(key + 64 * y);
-        const float scale = p.b.scales[at];
+      for (int y = 0; y < Y; ++y) codes[c][y][lane] = to_codes(x[y][0], x[y][1], inv);
+    }
+    __syncthreads();
+    v4u q[TILES][Y];
+    float sq[TILES];
+#pragma unroll
+    for (int c = 0; c < TILES; ++c) {
+      if (c >= tiles) continue;
+      sq[c] = query_scales[c][col];
+#pragma unroll
+      for (int y = 0; y < Y; ++y) q[c][y] = codes[c][y][lane];
+    }
+    for (int b0 = first; b0 < hi; b0 += step * AHEAD) {
+      v4u k[AHEAD][Y];
+      float scale[AHEAD];
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int64_t at = (int64_t)((unsigned)pages[a] < (unsigned)p.num_pages ? pages[a] : 0) * p.num_heads + t.kv_head;
+        const int8_t* key = p.b.codes + at * D + 16 * g;
+        if (b0 + step * a >= hi) continue;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) k[a][y] = *(const v4u*)(key + 64 * y);
+        scale[a] = p.b.scales[at];
+      }
+      load_pages(b0 + step * AHEAD);
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int from = b0 + step * a;
+        if (from >= hi) continue;
         float sk[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sk[i] = __shfl(scale, 4 * g + i);
+        for (int i = 0; i < 4; ++i) sk[i] = __shfl(scale[a], 4 * g + i);
 #pragma unroll
         for (int c = 0; c < TILES; ++c) {
           if (c >= tiles) continue;
           v4i s = {0, 0, 0, 0};
 #pragma unroll
           for (int y = 0; y < Y; ++y)
-            s = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, k[y]), __builtin_bit_cast(v4i, q[c][y]), s, 0, 0, 0);
+            s = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, k[a][y]), __builtin_bit_cast(v4i, q[c][y]), s, 0, 0, 0);
           v4u w;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -215,8 +256,8 @@ __global__ void __launch_bounds__(512) select_kernel(const SelectParams p) {
             w[i] = sortable(columns_max(x, width));
           }
           const int token = c * per_tile + col / width;
-          if (col % width == 0 && token < tokens) {
-            v4u* dst = (v4u*)(scores + token * p.row_words + b0 - lo + 4 * g);
+          if (col % width == 0 && token < t.tokens) {
+            v4u* dst = (v4u*)(scores + token * p.row_words + from - base + 4 * g);
             if (head0) {  // (the same lane's, of the heads before)
 #pragma unroll
               for (int i = 0; i < 4; ++i) w[i] = max(w[i], (*dst)[i]);
@@ -226,52 +267,228 @@ __global__ void __launch_bounds__(512) select_kernel(const SelectParams p) {
         }
       }
     }
-    __syncthreads();
   }
-  for (int token = wave; token < tokens; token += p.waves) {
-    const int place = place0 + token, mine = place >= 0 ? div(place, p.page) : -1;
-    int32_t* out = p.out + ((int64_t)(first_row + t0 + token) * p.num_heads + kv_head) * p.top;
-    const int all = mine + 1;
-    if (all <= p.top) {
-      for (int i = lane; i < p.top; i += 64) out[i] = i < all ? i : -1;
-      continue;
-    }
-    // (first + last <= top < all, so they do not meet)
-    const int need = p.top - p.first - p.last, count = all - p.last - p.first;
-    for (int i = lane; i < p.first; i += 64) out[i] = i;
-    for (int i = lane; i < p.last; i += 64) out[p.first + need + i] = all - p.last + i;
-    if (need == 0) continue;
-    const uint32_t* row = scores + token * p.row_words;
-    // the largest threshold that at least `need` scores reach, and how many do
-    uint32_t t = 0;
-    int reach = count;
-    for (uint32_t bit = 1u << 31; bit && reach > need; bit >>= 1) {
-      int x = 0;
-      for (int i = lane; i < count; i += 64) x += row[i] >= (t | bit) ? 1 : 0;
+}
+
+// Largest of the lanes' numbers.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  auto from = [&](auto ctrl, auto rows) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, decltype(rows)::value, 0xf, false); };
+  using std::integral_constant;
+  x = max(x, from(integral_constant<int, 0x111>(), integral_constant<int, 0xf>()));  // 1, 2, 4, 8 lanes before, in rows of 16
+  x = max(x, from(integral_constant<int, 0x112>(), integral_constant<int, 0xf>()));
+  x = max(x, from(integral_constant<int, 0x114>(), integral_constant<int, 0xf>()));
+  x = max(x, from(integral_constant<int, 0x118>(), integral_constant<int, 0xf>()));
+  x = max(x, from(integral_constant<int, 0x142>(), integral_constant<int, 0xa>()));  // the last lane of row 0 (2) into row 1 (3)
+  x = max(x, from(integral_constant<int, 0x143>(), integral_constant<int, 0xc>()));  // lane 31 into rows 2 and 3
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// The largest number that at least `need` of what `count` counts reach, from `low`, which `reach` of them do, to `high`.  Leaves in
+// `reach` how many reach it; with EARLY, any number that exactly `need` reach will do.
+template <bool EARLY, class Count>
+__device__ __forceinline__ uint32_t threshold(uint32_t low, uint32_t high, int need, int& reach, Count count) {
+  while (low < high && !(EARLY && reach == need)) {
+    const uint32_t mid = low + (high - low) / 2 + 1;
+    const int n = count(mid);
+    if (n >= need)
+      low = mid, reach = n;
+    else
+      high = mid - 1;
+  }
+  return low;
+}
+
+// A wave's room in LDS for scores that may be among the chosen.
+constexpr int CANDIDATES = 512;
+
+// The blocks of the token at `place`, by a wave, into `out`.  row: its scores, from block `first` on.
+__device__ __forceinline__ void choose(const SelectParams& p, int place, const uint32_t* row, uint32_t* candidates, int32_t* out) {
+  const int lane = threadIdx.x & 63, all = blocks_to(p, place);
+  if (all <= p.top) {
+    for (int i = lane; i < p.top; i += 64) out[i] = i < all ? i : -1;
+    return;
+  }
+  // (first + last <= top < all, so they do not meet)
+  const int need = p.top - p.first - p.last, count = all - p.last - p.first;
+  for (int i = lane; i < p.first; i += 64) out[i] = i;
+  for (int i = lane; i < p.last; i += 64) out[p.first + need + i] = all - p.last + i;
+  if (need == 0) return;
+  const uint64_t below = (1ull << lane) - 1;
+  constexpr int HELD = CANDIDATES / 64;
+  uint32_t x[HELD] = {};  // up to CANDIDATES scores that hold the chosen ones, number i in lane i % 64's register i / 64
+  uint32_t low, high;
+  int held = count;
+  if (count > CANDIDATES) {
+    // A lane's KEPT largest of every 64th score: `need` of all lanes' reach some number, so of all scores at least as many do, and
+    // the threshold is no smaller.  Few others reach it, unless lanes have many more than they kept.
+    constexpr int KEPT = 4;
+    uint32_t kept[KEPT] = {};
+#pragma unroll 8
+    for (int i = lane; i < count; i += 64) {
+      uint32_t y = row[i];
 #pragma unroll
-      for (int step = 1; step < 64; step *= 2) x += __shfl_xor(x, step);
-      if (x >= need) t |= bit, reach = x;
+      for (int k = 0; k < KEPT; ++k) {
+        const uint32_t larger = max(kept[k], y);
+        y = min(kept[k], y);
+        kept[k] = larger;
+      }
+    }
+    auto keeping = [&](uint32_t t) {
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < KEPT; ++k) n += (int)__popcll(__ballot(kept[k] >= t));
+      return n;
+    };
+    high = wave_max(kept[0]);
+    // (the smallest of the lanes' largest is reached by every lane; no score is 0)
+    low = need <= 64 ? max(~wave_max(~kept[0]), 1u) : 1u;
+    int reach = keeping(low);
+    if (reach >= need) low = threshold<true>(low, high, need, reach, keeping);
+    held = 0;
+#pragma unroll 4
+    for (int i0 = 0; i0 < count; i0 += 64) {
+      const uint32_t y = row[min(i0 + lane, count - 1)];
+      const bool may = i0 + lane < count && y >= low;
+      const uint64_t some = __ballot(may);
+      const int at = held + (int)__popcll(some & below);
+      if (may && at < CANDIDATES) candidates[at] = y;
+      held += (int)__popcll(some);
+    }
+    if (held <= CANDIDATES) {
+      // (the wave reads what its other lanes wrote: its LDS operations complete in order)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int r = 0; r < HELD; ++r)
+        if (64 * r + lane < held) x[r] = candidates[64 * r + lane];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  } else {
+    uint32_t most = 0;
+#pragma unroll
+    for (int r = 0; r < HELD; ++r)
+      if (64 * r < count) {
+        if (64 * r + lane < count) x[r] = row[64 * r + lane];
+        most = max(most, x[r]);
+      }
+    high = wave_max(most);
+    low = need <= 64 ? max(~wave_max(~most), 1u) : 1u;
+  }
+  auto search = [&](auto reaching) {
+    int reach = reaching(low);
+    const uint32_t t = threshold<true>(low, high, need, reach, reaching);
+    if (reach == need) {
+      int at = p.first;
+#pragma unroll 4
+      for (int i0 = 0; i0 < count; i0 += 64) {
+        const bool take = i0 + lane < count && row[min(i0 + lane, count - 1)] >= t;
+        const uint64_t taken = __ballot(take);
+        if (take) out[at + (int)__popcll(taken & below)] = p.first + i0 + lane;
+        at += (int)__popcll(taken);
+      }
+      return;
     }
     // those above it, and of those equal to it the first ones
-    int above = 0;
-    if (reach > need) {
-      for (int i = lane; i < count; i += 64) above += row[i] > t ? 1 : 0;
-#pragma unroll
-      for (int step = 1; step < 64; step *= 2) above += __shfl_xor(above, step);
-    }
-    int equals = reach > need ? need - above : INT32_MAX, at = p.first;
+    int at = p.first, equals = need - (t == UINT32_MAX ? 0 : reaching(t + 1));
     for (int i0 = 0; i0 < count; i0 += 64) {
-      const int i = i0 + lane;
-      const uint32_t x = i < count ? row[i] : 0u;
-      const uint64_t same = __ballot(i < count && x == t);
-      const uint64_t below = (1ull << lane) - 1;
-      const bool take = i < count && (x > t || (x == t && (int)__popcll(same & below) < equals));
+      const uint32_t y = i0 + lane < count ? row[i0 + lane] : 0u;
+      const uint64_t same = __ballot(y == t);
+      const bool take = y > t || (y == t && (int)__popcll(same & below) < equals);
       const uint64_t taken = __ballot(take);
-      if (take) out[at + (int)__popcll(taken & below)] = p.first + i;
+      if (take) out[at + (int)__popcll(taken & below)] = p.first + i0 + lane;
       at += (int)__popcll(taken);
       equals -= min((int)__popcll(same), equals);
     }
+  };
+  auto search_held = [&](auto registers) {
+    search([&](uint32_t t) {
+      int n = 0;
+#pragma unroll
+      for (int r = 0; r < decltype(registers)::value; ++r) n += (int)__popcll(__ballot(x[r] >= t));
+      return n;
+    });
+  };
+  if (held <= 128)
+    search_held(std::integral_constant<int, 2>());
+  else if (held <= CANDIDATES)
+    search_held(std::integral_constant<int, HELD>());
+  else  // (more candidates than there is room for: more than 256 blocks to choose, or many equal scores)
+    search([&](uint32_t t) {
+      int n = 0;
+#pragma unroll 8
+      for (int i0 = 0; i0 < count; i0 += 64) n += (int)__popcll(__ballot(i0 + lane < count && row[min(i0 + lane, count - 1)] >= t));
+      return n;
+    });
+}
+
+constexpr int select_threads(int head_dim, int tiles) { return tiles == 1 && head_dim != 256 ? 1024 : 512; }
+
+template <int D, int TILES>
+__global__ void __launch_bounds__(select_threads(D, TILES), D == 256 ? 2 : 4) select_kernel(const SelectParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint32_t scores[];  // [tile_tokens][row_words], then [waves][CANDIDATES]
+  __shared__ __attribute__((aligned(16))) v4u codes[TILES][D / 64][64];  // the queries as operands
+  __shared__ float query_scales[TILES][16];
+  Tokens t;
+  if (!get_tokens(p, blockIdx.x, t)) return;
+  const int wave = uniform((int)threadIdx.x >> 6), blocks = blocks_to(p, t.place0 + t.tokens - 1);
+  if (blocks > p.top) {
+    score<D, TILES>(p, t, p.first, p.first, blocks - p.last, 0, 1, scores, codes, query_scales);
+    __syncthreads();
   }
+  for (int token = wave; token < t.tokens; token += p.waves)
+    choose(p, t.place0 + token, scores + token * p.row_words, scores + p.tile_tokens * p.row_words + wave * CANDIDATES,
+           p.out + ((int64_t)(t.first_row + token) * p.num_heads + t.kv_head) * p.top);
+}
+
+// The two steps as kernels of their own, with the scores in memory.
+template <int D>
+__global__ void __launch_bounds__(512, D == 256 ? 2 : 4) score_kernel(const SelectParams p) {
+  __shared__ __attribute__((aligned(16))) v4u codes[1][D / 64][64];
+  __shared__ float query_scales[1][16];
+  Tokens t;
+  const int tiles = p.items * p.num_heads;
+  if (!get_tokens(p, blockIdx.x % tiles, t)) return;
+  const int blocks = blocks_to(p, t.place0 + t.tokens - 1);
+  if (blocks > p.top)
+    score<D, 1>(p, t, p.first, p.first, blocks - p.last, blockIdx.x / tiles, p.parts, p.scores + t.slot * p.tile_tokens * p.row_words, codes, query_scales);
+}
+
+// (a workgroup for a token and key head: all of it brings the scores to LDS, where one wave goes over them several times)
+constexpr int CHOOSE_THREADS = 256;
+__global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint32_t scores[];  // [row_words], then [CANDIDATES]
+  Tokens t;
+  const int tiles = p.items * p.num_heads, token = blockIdx.x / tiles;
+  if (!get_tokens(p, blockIdx.x % tiles, t) || token >= t.tokens) return;
+  const int count = blocks_to(p, t.place0 + token) - p.last - p.first;
+  const uint32_t* row = p.scores + (t.slot * p.tile_tokens + token) * p.row_words;
+  if (count + p.first + p.last > p.top) {
+#pragma unroll 4
+    for (int i = 4 * threadIdx.x; i < count; i += 4 * CHOOSE_THREADS) *(v4u*)(scores + i) = *(const v4u*)(row + i);  // (whole groups of 16 are written)
+  }
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  choose(p, t.place0 + token, scores, scores + p.row_words, p.out + ((int64_t)(t.first_row + token) * p.num_heads + t.kv_head) * p.top);
+}
+
+template <int D>
+hipError_t select(const SelectParams& p, bool one_tile, hipStream_t stream) {
+  const unsigned tiles = (unsigned)((int64_t)p.items * p.num_heads);
+  const dim3 threads(p.waves * 64);
+  if (p.parts > 1) {
+    hipLaunchKernelGGL((score_kernel<D>), dim3(tiles * p.parts), threads, 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((choose_kernel), dim3(tiles * p.tile_tokens), dim3(CHOOSE_THREADS), (size_t)(p.row_words + CANDIDATES) * 4, stream, p);
+    return hipGetLastError();
+  }
+  const size_t lds = ((size_t)p.tile_tokens * p.row_words + (size_t)p.waves * CANDIDATES) * 4;
+  if (one_tile)
+    hipLaunchKernelGGL((select_kernel<D, 1>), dim3(tiles), threads, lds, stream, p);
+  else
+    hipLaunchKernelGGL((select_kernel<D, select_tiles(D)>), dim3(tiles), threads, lds, stream, p);
+  return hipGetLastError();
 }
 
 }  // namespace blocks
@@ -290,18 +507,11 @@ hipError_t launch_block_keys(const BlockKeysParams& p, int head_dim, hipStream_t
   return hipGetLastError();
 }
 
-hipError_t launch_select_blocks(const SelectParams& p, int head_dim, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.items * p.num_heads)), threads(p.waves * 64);
-  const size_t lds = (size_t)p.tile_tokens * p.row_words * 4;
-  if (head_dim == 64)
-    hipLaunchKernelGGL((blocks::select_kernel<64>), grid, threads, lds, stream, p);
-  else if (head_dim == 128)
-    hipLaunchKernelGGL((blocks::select_kernel<128>), grid, threads, lds, stream, p);
-  else if (head_dim == 256)
-    hipLaunchKernelGGL((blocks::select_kernel<256>), grid, threads, lds, stream, p);
-  else
-    return hipErrorInvalidValue;
-  return hipGetLastError();
+hipError_t launch_select_blocks(const SelectParams& p, int head_dim, bool one_tile, hipStream_t stream) {
+  if (head_dim == 64) return blocks::select<64>(p, one_tile, stream);
+  if (head_dim == 128) return blocks::select<128>(p, one_tile, stream);
+  if (head_dim == 256) return blocks::select<256>(p, one_tile, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace dg

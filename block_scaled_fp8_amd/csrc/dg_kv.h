@@ -144,13 +144,16 @@ struct SelectParams {
   FastDiv group;                 // query heads per key head
   FastDiv q_tiles;               // tiles of tokens per sequence
   int32_t tile_tokens, items;    // tokens of a tile; batch * q_tiles
-  int32_t row_words;             // LDS words of a token's scores
-  int32_t waves;
+  int32_t row_words;             // words of a token's scores
+  int32_t waves;                 // of a workgroup
+  int32_t parts;                 // workgroups that share a tile's blocks, with the scores in memory; 1: one kernel, scores in LDS
+  uint32_t* scores;              // [items, heads, tile_tokens, row_words] (parts > 1)
   int32_t* out;                  // [total_q, heads, top]
 };
 // tiles of 16 columns (a token's heads, rounded up to a power of two) of a workgroup: their codes stay in registers
 constexpr int select_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
-hipError_t launch_select_blocks(const SelectParams& p, int head_dim, hipStream_t stream);
+// one_tile: a workgroup's tokens fit one tile of columns
+hipError_t launch_select_blocks(const SelectParams& p, int head_dim, bool one_tile, hipStream_t stream);
 
 struct SparseParams {
   Sequences s;

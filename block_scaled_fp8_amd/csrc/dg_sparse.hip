@@ -35,13 +35,13 @@ struct Tile {
   int64_t slot;                // number of the tile and key head, for parts
 };
 
-__device__ __forceinline__ bool get_tile(const SparseParams& p, Tile& t) {
+// Workgroup `id` of those of a launch with so many parts; false if it has no rows.
+__device__ __forceinline__ bool get_tile(const SparseParams& p, Tile& t, int id, int parts) {
   // with the key head as the fastest index, and a multiple of eight heads, those of a head land on one XCD
-  int id = blockIdx.x;
   t.kv_head = id % p.c.num_heads;
   id /= p.c.num_heads;
-  t.part = id & (p.parts - 1);
-  id /= p.parts;
+  t.part = id % parts;
+  id /= parts;
   const int head_tile = id % p.head_tiles;
   id /= p.head_tiles;
   t.seq = id % p.s.batch;
@@ -100,20 +100,25 @@ __device__ __forceinline__ bool has(const int32_t* list, int top, int v) {
   return at < top && list[at] == v;
 }
 
-__device__ __forceinline__ void load_entries(const SparseParams& p, const Tile& t, const int32_t* lists, int64_t list_stride, int from, int before,
-                                             Entries& e) {
+// SHARED: several tokens, whose lists lie one after the other in LDS; else the one token's list in memory.
+template <bool SHARED>
+__device__ __forceinline__ void load_entries(const SparseParams& p, const Tile& t, const int32_t* lists, int from, int before, Entries& e) {
   const int lane = threadIdx.x & 63, i = from + lane;
   e.tokens = 0;
   e.block = e.page = 0;
   if (i < t.tokens * p.top) {
-    const int mine = div(i, p.list);
-    const int b = lists[mine * list_stride + (i - mine * p.top)];
+    const int b = lists[i];
     // (blocks past the tile's last token hold no key that counts)
     if (b >= 0 && b < p.s.table_cols && b * p.c.page.d < t.key_end) {
-      unsigned tokens = 1u << mine;
-      for (int x = 0; x < t.tokens; ++x)
-        if (x != mine && has(lists + x * list_stride, p.top, b)) tokens |= 1u << x;
-      if ((tokens & ((1u << mine) - 1)) == 0) {
+      unsigned tokens = 1u;
+      if (SHARED) {
+        const int mine = div(i, p.list);
+        tokens = 1u << mine;
+        for (int x = 0; x < t.tokens; ++x)
+          if (x != mine && has(lists + x * p.top, p.top, b)) tokens |= 1u << x;
+        if (tokens & ((1u << mine) - 1)) tokens = 0;
+      }
+      if (tokens) {
         const int pg = p.s.table[t.seq * p.s.table_stride + b];
         e.tokens = tokens;
         e.block = b;
@@ -140,18 +145,17 @@ struct Walk {
   unsigned tokens;
 };
 
-template <int D>
-__device__ __forceinline__ bool next_segment(const SparseParams& p, const Tile& t, const int32_t* lists, int64_t list_stride, int segments, int share,
-                                             int shares, Walk& w) {
+template <bool SHARED>
+__device__ __forceinline__ bool next_segment(const SparseParams& p, const Tile& t, const int32_t* lists, int segments, int share, int shares, Walk& w) {
   w.segment += shares;
   while (w.segment >= segments) {
     while (!w.left) {
       if (w.from >= t.tokens * p.top) return false;
-      load_entries(p, t, lists, list_stride, w.from, w.before, w.e);
+      load_entries<SHARED>(p, t, lists, w.from, w.before, w.e);
       w.from += 64;
       w.before += (int)__popcll(__ballot(w.e.tokens != 0));
       // segment s of entry n is number n * segments + s
-      w.left = __ballot(w.e.tokens != 0 && ((share - w.e.number * segments) & (shares - 1)) < segments);
+      w.left = __ballot(w.e.tokens != 0 && (int)((unsigned)(share - w.e.number * segments) & (unsigned)(shares - 1)) < segments);
     }
     const int l = __builtin_ctzll(w.left);
     w.left &= w.left - 1;
@@ -163,7 +167,7 @@ __device__ __forceinline__ bool next_segment(const SparseParams& p, const Tile& 
   return true;
 }
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(const SparseParams p) {
   constexpr int KEYS = 32, TILE = KEYS * D * 2;
   constexpr int CH = D / 16, PASS = 64 / CH, NP = KEYS / PASS;  // V: 16-code chunks of a row, rows of a load, loads
@@ -171,10 +175,11 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
   constexpr int JOIN = WAVES * 16 * (JD + 4) * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * TILE > JOIN ? WAVES * TILE : JOIN];
   __shared__ float mz[WAVES][2][16];
+  extern __shared__ int32_t tile_lists[];  // [tile_tokens][top] (SHARED)
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), g = lane >> 4, col = lane & 15;
   uint8_t* vt = lds + wave * TILE;
   Tile t;
-  if (!get_tile(p, t)) return;
+  if (!get_tile(p, t, blockIdx.x, p.parts)) return;
   const Row row = row_of(p, t, col);
   const bool live = col < t.rows;
   const int place = live ? t.place0 + row.token : INT32_MIN / 2;
@@ -189,6 +194,14 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
   }
   const int64_t list_stride = (int64_t)p.c.num_heads * p.top;
   const int32_t* lists = p.blocks + (int64_t)t.first_row * list_stride + t.kv_head * p.top;
+  if (SHARED) {
+    for (int i = threadIdx.x; i < t.tokens * p.top; i += WAVES * 64) {
+      const int x = div(i, p.list);
+      tile_lists[i] = lists[x * list_stride + i - x * p.top];
+    }
+    __syncthreads();
+    lists = tile_lists;
+  }
   const int segments = (p.c.page.d + SEGMENT - 1) / SEGMENT, shares = WAVES * p.parts, share = t.part * WAVES + wave;
   const int64_t head_at = t.kv_head * p.c.head_stride, head_sf = t.kv_head * p.c.sf_head_stride;
   const unsigned every = (1u << t.tokens) - 1;
@@ -197,7 +210,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
   // the next 16 keys of the wave's share
   auto next_half = [&](Half& h) {
     if (w.offset >= w.end) {
-      if (!next_segment<D>(p, t, lists, list_stride, segments, share, shares, w)) {
+      if (!next_segment<SHARED>(p, t, lists, segments, share, shares, w)) {
         h.keys = 0;
         h.tokens = 0;
         return;
@@ -238,36 +251,43 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
 
   v4u kr[2][D / 64], vr[NP];
   uint32_t ks[2], vs[NP];
+  // (through buffer descriptors of the pages, whose addresses are scalar)
   auto fetch_k = [&](const Half (&h)[2]) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int off = h[x].offset + min(col, h[x].keys - 1);
-      const uint8_t* codes = p.c.k + h[x].page * p.c.page_stride + head_at;
-      const uint8_t* sf = p.c.k_sf + h[x].page * p.c.sf_page_stride + head_sf;
+      const __amdgpu_buffer_rsrc_t codes = rsrc(p.c.k + h[x].page * p.c.page_stride + head_at), sf = rsrc(p.c.k_sf + h[x].page * p.c.sf_page_stride + head_sf);
 #pragma unroll
-      for (int y = 0; y < D / 64; ++y) kr[x][y] = *(const v4u*)(codes + (uint32_t)(off * (int)p.c.token_stride + 16 * g + 64 * y));
-      ks[x] = sf[(uint32_t)(off * (int)p.c.sf_token_stride)];
-      asm volatile("" : "+v"(ks[x]));
+      for (int y = 0; y < D / 64; ++y) kr[x][y] = __builtin_amdgcn_raw_buffer_load_b128(codes, off * (int)p.c.token_stride + 16 * g + 64 * y, 0, 0);
+      ks[x] = __builtin_amdgcn_raw_buffer_load_b8(sf, off * (int)p.c.sf_token_stride, 0, 0);
     }
   };
   auto fetch_v = [&](const Half (&h)[2]) {
+    __amdgpu_buffer_rsrc_t codes[2], sf[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) codes[x] = rsrc(p.c.v + h[x].page * p.c.page_stride + head_at), sf[x] = rsrc(p.c.v_sf + h[x].page * p.c.sf_page_stride + head_sf);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       const int r = n * PASS + lane / CH, x = n * PASS / 16;  // (a load's rows are in one half)
       const int off = h[x].offset + min(r & 15, h[x].keys - 1);
-      vr[n] = *(const v4u*)(p.c.v + h[x].page * p.c.page_stride + head_at + (uint32_t)(off * (int)p.c.token_stride + 16 * (lane % CH)));
-      vs[n] = p.c.v_sf[h[x].page * p.c.sf_page_stride + head_sf + (uint32_t)(off * (int)p.c.sf_token_stride)];
-      asm volatile("" : "+v"(vs[n]));
+      vr[n] = __builtin_amdgcn_raw_buffer_load_b128(codes[x], off * (int)p.c.token_stride + 16 * (lane % CH), 0, 0);
+      vs[n] = __builtin_amdgcn_raw_buffer_load_b8(sf[x], off * (int)p.c.sf_token_stride, 0, 0);
     }
   };
 
   v4f o[D / 16];
-  float m = NEG_INF, z = 0.f;
+  float m, z;
+  // A hidden value's weight is zero, which is not enough where it is NaN or infinite.  Nobody looks for such values at first: they
+  // leave a NaN in some output.  A wave that ends with an output that is no number goes over its keys again with care: what is no number among the values
+  // that some row does not see goes to LDS as zero, and is added at the end to the outputs of the rows that see it.
+  bool odd = false;  // the wave has cleared a value
+  Half now[2], next[2];
+#pragma unroll 1
+  for (int careful = 0;; ++careful) {
+  m = NEG_INF, z = 0.f;
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) o[d] = (v4f){0.f, 0.f, 0.f, 0.f};
-  bool odd = false;  // the wave has cleared a value
   start();
-  Half now[2], next[2];
   bool more = next_tile(now);
   if (more) {
     fetch_k(now);
@@ -300,12 +320,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
     const bool whole = now[0].tokens == every && now[1].tokens == every && now[0].keys == 16 && now[1].keys == 16 &&
                        now[0].key0 + 15 <= t.place0 && now[1].key0 + 15 <= t.place0;
     if (!whole) {
-      // A hidden value's weight is zero, which is not enough where it is NaN or infinite: such values become zeros here, and
-      // are added at the end to the outputs of the rows that see them.
-      bool may = false;
-#pragma unroll
-      for (int n = 0; n < NP; ++n) may |= may_be_odd(vr[n], vs[n]);
-      if (__builtin_expect(__any(may), 0)) {
+      if (__builtin_expect(careful, 0)) {
         odd = true;
 #pragma unroll 1
         for (int n = 0; n < NP; ++n) {
@@ -370,6 +385,12 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
     __builtin_amdgcn_wave_barrier();
     now[0] = next[0];
     now[1] = next[1];
+  }
+    if (careful) break;
+    float sum = 0.f;  // (a NaN or infinity times zero is NaN)
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) sum += (o[d].x * 0.f + o[d].y * 0.f) + (o[d].z * 0.f + o[d].w * 0.f);
+    if (__builtin_expect(!__any(sum != 0.f), 1)) break;
   }
 
   if (__builtin_expect(odd, 0)) {
@@ -436,64 +457,75 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
   }
 }
 
-// out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) z_s over the parts s of a tile and key head.  A workgroup has 1024 / D rows, D / 4
-// lanes each.
+// out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) z_s over the parts s of a row.  A workgroup has one row: D / 4 lanes for a part, groups of
+// lanes take the parts in turn, and their sums are added in their order.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const SparseParams p) {
-  constexpr int L = D / 4, ROWS = 256 / L, BLOCKS = 16 / ROWS;
+  constexpr int L = D / 4, G = 256 / L;
+  __shared__ __attribute__((aligned(16))) float sums[G][L][4];
+  __shared__ float tops[G][2];
   Tile t;
-  // (the workgroups are numbered like those of the first kernel without parts)
-  int id = blockIdx.x / BLOCKS;
-  t.kv_head = id % p.c.num_heads;
-  id /= p.c.num_heads;
-  const int head_tile = id % p.head_tiles;
-  id /= p.head_tiles;
-  t.seq = id % p.s.batch;
-  const int tile = id / p.s.batch;
-  int n;
-  if (p.s.cu_q) {
-    const int a = uniform(p.s.cu_q[t.seq]), b = uniform(p.s.cu_q[t.seq + 1]);
-    t.first_row = min(max(a, 0), p.s.total_q);
-    n = min(max(b, t.first_row), p.s.total_q) - t.first_row;
-  } else {
-    t.first_row = t.seq * p.s.q_per_seq;
-    n = p.s.q_per_seq;
-  }
-  const int t0 = tile * p.tile_tokens;
-  t.tokens = min(p.tile_tokens, n - t0);
-  if (t.tokens <= 0) return;
-  t.head0 = 16 * head_tile;
-  t.rows = p.head_tiles > 1 ? min(16, p.group.d - t.head0) : t.tokens * p.group.d;
-  const int r = blockIdx.x % BLOCKS * ROWS + threadIdx.x / L, d = 4 * (threadIdx.x % L);
+  if (!get_tile(p, t, blockIdx.x >> 4, 1)) return;
+  const int r = blockIdx.x & 15, lanes = threadIdx.x % L, group = threadIdx.x / L;
   if (r >= t.rows) return;
   const Row row = row_of(p, t, r);
-  const int64_t slot = (((int64_t)(t.seq * p.q_tiles.d + tile) * p.c.num_heads + t.kv_head) * p.head_tiles + head_tile) * p.parts;
   float m = NEG_INF, z = 0.f;
   v4f o = {0.f, 0.f, 0.f, 0.f};
-  for (int x = 0; x < p.parts; ++x) {
-    const int64_t at = (slot + x) * 16 + r;
-    const v2f a = *(const v2f*)(p.part_mz + 2 * at);
-    const v4f b = *(const v4f*)(p.part_o + at * D + d);
-    // a part in which the row sees nothing (one whose scores are all NaN has no maximum either, but a NaN for its sum, which stays)
-    if (a.x == NEG_INF && a.y == 0.f) continue;
-    const float top = fmaxf(m, a.x), f = exp2_hw(m - top), h = exp2_hw(a.x - top);
-    z = z * f + a.y * h;
-    o = o * f + b * h;
-    m = top;
+  constexpr int AT_ONCE = 4;  // (loads that go out together)
+  for (int x = group; x < p.parts; x += G * AT_ONCE) {
+    v2f a[AT_ONCE];
+    v4f b[AT_ONCE];
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      a[u] = (v2f){NEG_INF, 0.f};
+      if (x + u * G < p.parts) {
+        const int64_t at = (t.slot + x + u * G) * 16 + r;
+        a[u] = *(const v2f*)(p.part_mz + 2 * at);
+        b[u] = *(const v4f*)(p.part_o + at * D + 4 * lanes);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      // no part, or one in which the row sees nothing (one whose scores are all NaN has no maximum either, but a NaN for its
+      // sum, which stays)
+      if (a[u].x == NEG_INF && a[u].y == 0.f) continue;
+      const float top = fmaxf(m, a[u].x), f = exp2_hw(m - top), h = exp2_hw(a[u].x - top);
+      z = z * f + a[u].y * h;
+      o = o * f + b[u] * h;
+      m = top;
+    }
+  }
+  *(v4f*)sums[group][lanes] = o;
+  if (lanes == 0) tops[group][0] = m, tops[group][1] = z;
+  __syncthreads();
+  if (group != 0) return;
+#pragma unroll
+  for (int x = 0; x < G; ++x) m = fmaxf(m, tops[x][0]);
+  z = 0.f;
+  o = 0.f;
+#pragma unroll
+  for (int x = 0; x < G; ++x) {
+    // (a group without parts, or with NaN for its sum)
+    const float f = tops[x][0] == NEG_INF ? 1.f : exp2_hw(tops[x][0] - m);
+    z += f * tops[x][1];
+    o += f * *(const v4f*)sums[x][lanes];
   }
   o *= inverse(z);
-  const int64_t token = t.first_row + t0 + row.token;
-  *(v2u*)(p.out + token * p.o_token_stride + row.head * p.o_head_stride + d) = (v2u){pack2(o.x, o.y), pack2(o.z, o.w)};
-  if (p.lse && d == 0) p.lse[token * p.s.num_q_heads + row.head] = log_sum(m, z);
+  const int64_t token = t.first_row + row.token;
+  *(v2u*)(p.out + token * p.o_token_stride + row.head * p.o_head_stride + 4 * lanes) = (v2u){pack2(o.x, o.y), pack2(o.z, o.w)};
+  if (p.lse && lanes == 0) p.lse[token * p.s.num_q_heads + row.head] = log_sum(m, z);
 }
 
 template <int D>
 hipError_t launch(const SparseParams& p, hipStream_t stream) {
   const unsigned tiles = (unsigned)((int64_t)p.items * p.c.num_heads * p.head_tiles);
-  hipLaunchKernelGGL((sparse_kernel<D>), dim3(tiles * p.parts), dim3(WAVES * 64), 0, stream, p);
+  if (p.tile_tokens > 1)
+    hipLaunchKernelGGL((sparse_kernel<D, true>), dim3(tiles * p.parts), dim3(WAVES * 64), (size_t)p.tile_tokens * p.top * 4, stream, p);
+  else
+    hipLaunchKernelGGL((sparse_kernel<D, false>), dim3(tiles * p.parts), dim3(WAVES * 64), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.parts == 1) return e;
-  hipLaunchKernelGGL((join_kernel<D>), dim3(tiles * (D / 64)), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((join_kernel<D>), dim3(tiles * 16), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -495,11 +495,16 @@ int dg_fp8_kv_block_keys_update(const dg_fp8_kv_cache* cache, const dg_fp8_block
  *  first >= 0, last >= 1, first + last <= top <= 2^20.
  *  blocks : int32 [total_q, keys->num_heads, top], contiguous: numbers of blocks in the sequence (columns of block_table), ascending, then
  *           -1 up to `top`.  Rows of no sequence are not written.
+ *  workspace : device memory of at least dg_fp8_kv_select_blocks_workspace() bytes for the same arguments, 16-byte aligned;
+ *           contents on entry do not matter.  NULL where that is 0.
  */
 int dg_fp8_kv_select_blocks(const dg_fp8_block_keys* keys, int32_t page_size, int32_t batch, int32_t total_q, int32_t num_q_heads,
                             const void* q, int64_t q_token_stride, int64_t q_head_stride, const int32_t* cu_seqlens_q, int32_t max_seqlen_q,
                             const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* seq_lens, int32_t top,
-                            int32_t first, int32_t last, int32_t* blocks, hipStream_t stream);
+                            int32_t first, int32_t last, int32_t* blocks, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+/* Its workspace in bytes (0: none), or a negative dg_status.  equal_q: 1 where cu_seqlens_q is NULL. */
+int64_t dg_fp8_kv_select_blocks_workspace(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t equal_q, int32_t max_seqlen_q, int32_t table_cols, int32_t top, int32_t first, int32_t last);
 
 /*
  * Causal attention of each sequence's newest tokens over chosen blocks: as dg_fp8_paged_attention (arguments, numerics, rows that

@@ -100,19 +100,21 @@ CHOICES = {
     "groups_of_sixteen": ([640, 640], [9, 9], 32, 2, 256, 16),
     "more_new_than_held": ([30, 0, 40], [50, 2, 41], 4, 2, 128, 1),
     "long": ([9000], [6], 8, 1, 64, 1),
+    "long_ragged": ([5000, 700, 2500, 0], [2, 1, 5, 1], 4, 2, 128, 1),
 }
 
 
 @pytest.mark.parametrize("ties", [False, True])
-@pytest.mark.parametrize("top,first,last", [(8, 1, 2), (1, 0, 1), (5, 2, 3), (16, 0, 1), (70, 3, 1)])
+@pytest.mark.parametrize("top,first,last", [(8, 1, 2), (1, 0, 1), (5, 2, 3), (16, 0, 1), (70, 3, 1), (300, 1, 1), (200, 0, 2)])
 @pytest.mark.parametrize("name", sorted(CHOICES))
 def test_choice_is_exact(name, top, first, last, ties):
     say("choice", name, top, first, last, ties)
     p = select_problem(*CHOICES[name], seed=top, ties=ties)
     want = oracle.select_blocks(p["q"], p["keys"], p["table"], p["lens"], p["cu"], p["page"], top, first, last)
     assert same(select(p, top, first, last), want)
-    with num_sms(1):  # (larger tiles of tokens)
-        assert same(select(p, top, first, last), want)
+    for sms in (1, 4000):  # (larger tiles of tokens; more workgroups for the blocks of a tile)
+        with num_sms(sms):
+            assert same(select(p, top, first, last), want)
 
 
 def test_choice_from_a_wide_table():

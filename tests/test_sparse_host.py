@@ -34,7 +34,7 @@ def update(c=None, b=None, n=3, pages=P):
 
 def select(b=None, **kw):
     a = dict(page=16, batch=2, total_q=4, hq=8, q=P, qts=1024, qhs=128, cu=P, max_q=2, table=P, ts=5, cols=5, lens=P, top=4, first=1, last=1,
-             blocks=P, stream=None)
+             blocks=P, work=None, work_bytes=0, stream=None)
     a.update(kw)
     return dg.lib().dg_fp8_kv_select_blocks(ctypes.byref(keys() if b is None else b), *a.values())
 
@@ -78,7 +78,7 @@ def test_select_refuses():
         assert select(**kw) == code, kw
     for kw in (dict(batch=0), dict(total_q=0), dict(max_q=0)):
         assert select(keys(codes=None), q=None, table=None, lens=None, blocks=None, **kw) == DG_OK, kw
-    assert dg.lib().dg_fp8_kv_select_blocks(None, *[0] * 4, None, 0, 0, None, 0, None, 0, 0, None, 1, 0, 1, None, None) == NULL
+    assert dg.lib().dg_fp8_kv_select_blocks(None, *[0] * 4, None, 0, 0, None, 0, None, 0, 0, None, 1, 0, 1, None, None, 0, None) == NULL
 
 
 def test_attention_refuses():
@@ -104,6 +104,17 @@ def test_more_tiles_than_a_launch_holds_are_refused():
 def test_a_workspace_that_is_missing_or_small_is_refused():
     dg.set_num_sms(256)
     try:
+        size = dg.lib().dg_fp8_kv_select_blocks_workspace
+        need = size(1, 1, 32, 4, 128, 1, 0, 2000, 20, 1, 1)
+        assert need > 0
+        a = dict(batch=1, total_q=1, hq=32, cu=None, cols=2000, ts=2000, top=20)
+        assert select(**a) == NULL and select(work=P, work_bytes=need - 1, **a) == SHAPE and select(work=P_MIS, work_bytes=need, **a) == LAYOUT
+        assert size(64, 64, 32, 4, 128, 1, 0, 2000, 20, 1, 1) == 0 and size(1, 1, 32, 4, 128, 1, 0, 100, 20, 1, 1) == 0
+        assert size(0, 0, 32, 4, 128, 1, 0, 2000, 20, 1, 1) == 0 and size(1, 1, 32, 4, 128, 1, 0, 20, 20, 1, 1) == 0
+        for bad, code in [((1, 1, 32, 4, 96, 1, 0, 100, 20, 1, 1), UNSUPPORTED), ((1, 1, 30, 4, 128, 1, 0, 100, 20, 1, 1), SHAPE),
+                          ((1, 1, 32, 4, 128, 1, 0, 100, 20, 10, 11), SHAPE), ((1, 1, 32, 4, 128, 1, 0, -1, 20, 1, 1), LAYOUT),
+                          ((1, 1, 32, 4, 128, 1, 0, 40000, 20, 1, 1), UNSUPPORTED)]:
+            assert size(*bad) == code, bad
         size = dg.lib().dg_fp8_block_sparse_attention_workspace
         need = size(1, 1, 32, 8, 128, 1, 0, 64, 64)
         assert need > 0
