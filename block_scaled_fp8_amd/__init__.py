@@ -57,11 +57,6 @@ class _NormRope(ctypes.Structure):
                 ("rot_dim", _i32), ("interleaved", _i32), ("eps", ctypes.c_float)]
 
 
-class _Rows(ctypes.Structure):
-    """dg_rows (include/dg.h)."""
-    _fields_ = [("p", _p), ("token_stride", _i64), ("head_stride", _i64)]
-
-
 class _BlockKeys(ctypes.Structure):
     """dg_fp8_block_keys (include/dg.h)."""
     _fields_ = [("codes", _p), ("scales", _p), ("num_pages", _i32), ("num_heads", _i32), ("head_dim", _i32)]
@@ -102,10 +97,10 @@ _SIGS = {
     "dg_fp8_block_sparse_attention": (_i32, [_c, _i32, _i32, _i32, _p, _i64, _i64, _p, _i32, _p, _i64, _i32, _p, _p, _i32, ctypes.c_float,
                                              _p, _i64, _i64, _p, _p, _i64, _p]),
     "dg_fp8_block_sparse_attention_workspace": (_i64, [_i32] * 9),
-    "dg_qk_norm_rope": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _p]),
-    "dg_qk_norm_rope_backward": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _Rows, _Rows, _p, _p, _p, _i64, _p]),
+    "dg_qk_norm_rope": (_i32, [_n, *[_p, _i64, _i64] * 4, _p]),
+    "dg_qk_norm_rope_backward": (_i32, [_n, *[_p, _i64, _i64] * 6, _p, _p, _p, _i64, _p]),
     "dg_qk_norm_rope_backward_workspace": (_i64, [_i32] * 4),
-    "dg_qk_norm_rope_fp8_kv_cache_write": (_i32, [_n, _Rows, _Rows, _Rows, _Rows, _c, _p, _p]),
+    "dg_qk_norm_rope_fp8_kv_cache_write": (_i32, [_n, *[_p, _i64, _i64] * 4, _c, _p, _p]),
     "dg_get_tma_aligned_size": (_i64, [_i64, _i32]),
     "dg_get_mk_alignment_for_contiguous_layout": (_i32, []),
     "dg_set_num_sms": (_i32, [_i32]),
@@ -871,14 +866,14 @@ def fp8_kv_select_blocks(q, block_keys, block_table, seq_lens, page_size, top, f
     if want[2] < 1 or max(want[2], int(page_size), int(first), int(last)) > _INT32:
         raise ValueError("top must be positive, and top, page_size, first and last fit 32 bits")
     if out is None:
-        out = torch.full(want, -1, dtype=torch.int32, device=dev) if blind else torch.empty(want, dtype=torch.int32, device=dev)
+        out = q.new_full(want, -1, dtype=torch.int32) if blind else q.new_empty(want, dtype=torch.int32)
     elif out.dtype != torch.int32 or tuple(out.shape) != want or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be contiguous int32 {list(want)} on the block keys' GPU")
     handle = lib()
     need = handle.dg_fp8_kv_select_blocks_workspace(batch, total, hq, hk, d, cu is None, max_q, cols, want[2], first, last)
     if need < 0:
         _check(need)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    work = q.new_empty(need, dtype=torch.uint8) if need else None
     qs = q.stride()
     _check(handle.dg_fp8_kv_select_blocks(b, page_size, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts, cols,
                                           seq_lens.data_ptr(), want[2], first, last, out.data_ptr(), None if work is None else work.data_ptr(), need,
@@ -904,17 +899,17 @@ def fp8_block_sparse_attention(q, k_cache, v_cache, block_table, seq_lens, block
     if top > _INT32:
         raise ValueError("top must fit 32 bits")
     if out is None:
-        out = (torch.zeros_like if blind else torch.empty_like)(q, memory_format=torch.contiguous_format)
+        out = q.new_zeros(q.shape) if blind else torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != torch.bfloat16 or out.shape != q.shape or out.stride(2) != 1 or out.device != dev:
         raise ValueError("out must be bfloat16 of q's shape, contiguous along the last dimension, on the cache's GPU")
-    lse = torch.empty((total, hq), dtype=torch.float32, device=dev) if return_lse else None
+    lse = q.new_empty((total, hq), dtype=torch.float32) if return_lse else None
     if blind and return_lse:
         lse.fill_(float("-inf"))
     handle = lib()
     need = handle.dg_fp8_block_sparse_attention_workspace(batch, total, hq, hk, d, cu is None, max_q, page, top)
     if need < 0:
         _check(need)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    work = q.new_empty(need, dtype=torch.uint8) if need else None
     qs, os_ = q.stride(), out.stride()
     _check(handle.dg_fp8_block_sparse_attention(
         c, batch, total, hq, q.data_ptr(), qs[0], qs[1], cu, max_q, block_table.data_ptr(), ts, cols, seq_lens.data_ptr(), blocks.data_ptr(), top,
@@ -924,40 +919,43 @@ def fp8_block_sparse_attention(q, k_cache, v_cache, block_table, seq_lens, block
 
 
 # ---------------------------------------------------------------- norm and rotation of queries and keys
-def _rows(name, x, like, dev):
-    """The C struct of rows [tokens, heads, head dim] of the shape and type of ``like`` (a shape and a dtype)."""
-    shape, dtype = like
+def _rows(name, x, shape, dtype, dev):
+    """Pointer, token and head stride of rows [tokens, heads, head dim]."""
     st = x.stride()
-    if tuple(x.shape) != shape or x.dtype != dtype or st[2] != 1 or x.device != dev:
+    if x.shape != shape or x.dtype != dtype or st[2] != 1 or x.device != dev:
         raise ValueError(f"{name} must be {dtype} {list(shape)} on {dev}, contiguous along the last dimension")
-    return _Rows(x.data_ptr(), st[0], st[1])
+    return x.data_ptr(), st[0], st[1]
 
 
 def _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved):
-    """The C struct of a call, and the shapes and type of the queries' and keys' rows."""
-    dtype, dev = q.dtype, q.device
+    """The C struct of a call, the operands' shapes, type and device, and q's and k's pointers and strides."""
+    dtype, dev, qs, ks = q.dtype, q.device, q.shape, k.shape
     if dtype not in _IN_TYPES or k.dtype != dtype:
         raise TypeError(f"q and k must both be bfloat16 or float32, got {dtype} and {k.dtype}")
-    qs, ks = tuple(q.shape), tuple(k.shape)
     if len(qs) != 3 or len(ks) != 3 or qs[0] != ks[0] or qs[2] != ks[2]:
         raise ValueError(f"q and k must be [tokens, heads, head dim] with the same tokens and head dim, got {list(qs)} and {list(ks)}")
     t, hq, d = qs
-    if q_weight.dtype not in _IN_TYPES or k_weight.dtype != q_weight.dtype:
-        raise TypeError(f"q_weight and k_weight must both be bfloat16 or float32, got {q_weight.dtype} and {k_weight.dtype}")
-    if tuple(q_weight.shape) != (d,) or tuple(k_weight.shape) != (d,) or not q_weight.is_contiguous() or not k_weight.is_contiguous():
+    w_dtype = q_weight.dtype
+    if w_dtype not in _IN_TYPES or k_weight.dtype != w_dtype:
+        raise TypeError(f"q_weight and k_weight must both be bfloat16 or float32, got {w_dtype} and {k_weight.dtype}")
+    if q_weight.shape != (d,) or k_weight.shape != (d,) or not q_weight.is_contiguous() or not k_weight.is_contiguous():
         raise ValueError(f"q_weight and k_weight must be contiguous [{d}]")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.stride(1) != 1:
         raise ValueError("cos_sin must be float32 [positions, rotated dim], contiguous along the last dimension")
-    if positions.dtype != torch.int64 or tuple(positions.shape) != (t,) or not positions.is_contiguous():
+    if positions.dtype != torch.int64 or positions.shape != (t,) or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous int64 [{t}]")
-    if dev.type != "cuda" or any(x.device != dev for x in (k, q_weight, k_weight, cos_sin, positions)):
+    if dev.type != "cuda" or q_weight.device != dev or k_weight.device != dev or cos_sin.device != dev or positions.device != dev:
         raise ValueError("q, k, the weights, cos_sin and positions must be on one GPU")
-    if max(*qs, ks[1]) > _INT32:
-        raise ValueError("q's and k's dimensions must fit 32 bits")
-    a = _NormRope(t, hq, ks[1], d, _IN_TYPES[dtype], _IN_TYPES[q_weight.dtype], q_weight.data_ptr(), k_weight.data_ptr(),
-                  cos_sin.data_ptr(), cos_sin.stride(0), cos_sin.shape[0], positions.data_ptr(), cos_sin.shape[1],
-                  bool(interleaved), eps)
-    return a, (qs, dtype), (ks, dtype), dev
+    table, rot = cos_sin.shape
+    if t > _INT32 or hq > _INT32 or ks[1] > _INT32 or d > _INT32 or rot > _INT32:
+        raise ValueError("dimensions must fit 32 bits")
+    a = _NormRope(t, hq, ks[1], d, _IN_TYPES[dtype], _IN_TYPES[w_dtype], q_weight.data_ptr(), k_weight.data_ptr(),
+                  cos_sin.data_ptr(), cos_sin.stride(0), table, positions.data_ptr(), rot, bool(interleaved), eps)
+    return a, qs, ks, dtype, dev, (*_rows("q", q, qs, dtype, dev), *_rows("k", k, ks, dtype, dev))
+
+
+def _empty(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interleaved=False, out=None):
@@ -970,15 +968,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interle
     ``positions``: int64 [tokens]; a token whose position is negative or past the table is padding, and gives zeros.
     ``out``: ``(q, k)`` to write into, which may be ``q`` and ``k`` themselves.  Returns ``(q, k)`` of the inputs' type.
     The results have no autograd history; their gradients come from ``qk_norm_rope_backward``."""
-    a, ql, kl, dev = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    a, qs, ks, dtype, dev, qk = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, out)
-    if out is None:
-        out = torch.empty(ql[0], dtype=ql[1], device=dev), torch.empty(kl[0], dtype=kl[1], device=dev)
-    q_out, k_out = out
-    _check(lib().dg_qk_norm_rope(a, _rows("q", q, ql, dev), _rows("k", k, kl, dev), _rows("out[0]", q_out, ql, dev),
-                                 _rows("out[1]", k_out, kl, dev), _current_stream(dev)))
+    q_out, k_out = (_empty(q), _empty(k)) if out is None else out
+    _check(lib().dg_qk_norm_rope(a, *qk, *_rows("out[0]", q_out, qs, dtype, dev), *_rows("out[1]", k_out, ks, dtype, dev), _current_stream(dev)))
     return q_out, k_out
 
 
@@ -986,25 +981,22 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
     """Gradients of ``qk_norm_rope``: ``dq_out`` and ``dk_out`` are those of its results, the other arguments the forward
     call's.  Returns ``(dq, dk, dq_weight, dk_weight)``: the rows' in their type, the weights' FP32 [head dim], summed over tokens
     and heads (zeros without a token).  ``out``: ``(dq, dk)`` to write into, which may be ``dq_out`` and ``dk_out``."""
-    a, ql, kl, dev = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    a, qs, ks, dtype, dev, qk = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, out)
-    if out is None:
-        out = torch.empty(ql[0], dtype=ql[1], device=dev), torch.empty(kl[0], dtype=kl[1], device=dev)
-    dq, dk = out
-    (t, hq, d), hk = ql[0], kl[0][1]
-    handle = lib()
-    need = handle.dg_qk_norm_rope_backward_workspace(t, hq, hk, d)
+    dq, dk = (_empty(q), _empty(k)) if out is None else out
+    handle, d = lib(), qs[2]
+    need = handle.dg_qk_norm_rope_backward_workspace(qs[0], qs[1], ks[1], d)
     if need < 0:
         _check(need)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    dw = torch.empty((2, d), dtype=torch.float32, device=dev)
+    work = q.new_empty(need, dtype=torch.uint8) if need else None
+    dq_weight, dk_weight = q.new_empty((2, d), dtype=torch.float32).unbind()
     _check(handle.dg_qk_norm_rope_backward(
-        a, _rows("dq_out", dq_out, ql, dev), _rows("dk_out", dk_out, kl, dev), _rows("q", q, ql, dev), _rows("k", k, kl, dev),
-        _rows("out[0]", dq, ql, dev), _rows("out[1]", dk, kl, dev), dw.data_ptr(), dw.data_ptr() + 4 * d,
-        None if work is None else work.data_ptr(), need, _current_stream(dev)))
-    return dq, dk, dw[0], dw[1]
+        a, *_rows("dq_out", dq_out, qs, dtype, dev), *_rows("dk_out", dk_out, ks, dtype, dev), *qk, *_rows("out[0]", dq, qs, dtype, dev),
+        *_rows("out[1]", dk, ks, dtype, dev), dq_weight.data_ptr(), dk_weight.data_ptr(), None if work is None else work.data_ptr(), need,
+        _current_stream(dev)))
+    return dq, dk, dq_weight, dk_weight
 
 
 def qk_norm_rope_fp8_kv_cache_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slots, eps=1e-6,
@@ -1012,18 +1004,18 @@ def qk_norm_rope_fp8_kv_cache_write(q, k, v, q_weight, k_weight, cos_sin, positi
     """``qk_norm_rope`` whose keys, and the values ``v``, go to the slots of an FP8 cache as ``fp8_kv_cache_write`` writes them
     (the keys quantised from FP32, without a rounding to BF16 between).  Returns the queries; ``out``: where to write them,
     may be ``q``.  A padding token's keys and values are not written, nor those of a slot that is negative or past the cache."""
-    a, ql, kl, dev = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    a, qs, ks, dtype, dev, qk = _norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return qk_norm_rope_fp8_kv_cache_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slots, eps,
                                                    interleaved, out)
     c, _, cache_dev = _kv_cache(k_cache, v_cache)
-    if slots.dtype != torch.int64 or tuple(slots.shape) != ql[0][:1] or not slots.is_contiguous():
-        raise ValueError(f"slots must be contiguous int64 [{ql[0][0]}]")
+    if slots.dtype != torch.int64 or slots.shape != positions.shape or not slots.is_contiguous():
+        raise ValueError(f"slots must be contiguous int64 [{qs[0]}]")
     if cache_dev != dev or slots.device != dev:
         raise ValueError("the cache and slots must be on q's GPU")
     if out is None:
-        out = torch.empty(ql[0], dtype=ql[1], device=dev)
-    _check(lib().dg_qk_norm_rope_fp8_kv_cache_write(a, _rows("q", q, ql, dev), _rows("k", k, kl, dev), _rows("v", v, kl, dev),
-                                                    _rows("out", out, ql, dev), c, slots.data_ptr(), _current_stream(dev)))
+        out = _empty(q)
+    _check(lib().dg_qk_norm_rope_fp8_kv_cache_write(a, *qk, *_rows("v", v, ks, dtype, dev), *_rows("out", out, qs, dtype, dev), c, slots.data_ptr(),
+                                                    _current_stream(dev)))
     return out

@@ -44,11 +44,13 @@ int check_call(const dg_norm_rope* a) {
 
 int element_size(const dg_norm_rope* a) { return a->dtype == DG_IN_BF16 ? 2 : 4; }
 
-int check_operand(const dg_norm_rope* a, const char* name, const dg_rows& r) {
+int check_operand(const dg_norm_rope* a, const char* name, const dg::Rows& r) {
   return check_rows(name, r.p, r.token_stride, r.head_stride, element_size(a));
 }
 
-dg::Rows from_token(const dg_rows& r, int64_t token, int esz) {
+dg::Rows rows(const void* p, int64_t token_stride, int64_t head_stride) { return {const_cast<void*>(p), token_stride, head_stride}; }
+
+dg::Rows from_token(const dg::Rows& r, int64_t token, int esz) {
   return {static_cast<char*>(r.p) + token * r.token_stride * esz, r.token_stride, r.head_stride};
 }
 
@@ -69,7 +71,7 @@ dg::RopeParams kernel_params(const dg_norm_rope* a) {
   return p;
 }
 
-int forward(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows v, dg_rows q_out, dg_rows k_out, const dg_fp8_kv_cache* cache,
+int forward(const dg_norm_rope* a, dg::Rows q, dg::Rows k, dg::Rows v, dg::Rows q_out, dg::Rows k_out, const dg_fp8_kv_cache* cache,
             const int64_t* slots, hipStream_t stream) {
   const int esz = element_size(a), rows = a->num_q_heads + (cache ? 2 : 1) * a->num_kv_heads;
   const int heads = dg::rope_heads(a->head_dim), pieces = (rows + heads - 1) / heads;
@@ -111,30 +113,45 @@ int64_t backward_workspace(int workgroups, int32_t head_dim) { return workgroups
 
 extern "C" {
 
-int dg_qk_norm_rope(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows q_out, dg_rows k_out, hipStream_t stream) {
+int dg_qk_norm_rope(const dg_norm_rope* a, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                    const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                    void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                    void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                    hipStream_t stream) {
+  const dg::Rows q_rows = rows(q, q_token_stride, q_head_stride);
+  const dg::Rows k_rows = rows(k, k_token_stride, k_head_stride);
+  const dg::Rows q_out_rows = rows(q_out, q_out_token_stride, q_out_head_stride);
+  const dg::Rows k_out_rows = rows(k_out, k_out_token_stride, k_out_head_stride);
   if (int s = check_call(a)) return s;
   if (a->num_tokens == 0) return api_ok();
-  if (int s = check_operand(a, "q", q)) return s;
-  if (int s = check_operand(a, "k", k)) return s;
-  if (int s = check_operand(a, "q_out", q_out)) return s;
-  if (int s = check_operand(a, "k_out", k_out)) return s;
-  return forward(a, q, k, {}, q_out, k_out, nullptr, nullptr, stream);
+  if (int s = check_operand(a, "q", q_rows)) return s;
+  if (int s = check_operand(a, "k", k_rows)) return s;
+  if (int s = check_operand(a, "q_out", q_out_rows)) return s;
+  if (int s = check_operand(a, "k_out", k_out_rows)) return s;
+  return forward(a, q_rows, k_rows, {}, q_out_rows, k_out_rows, nullptr, nullptr, stream);
 }
 
-int dg_qk_norm_rope_fp8_kv_cache_write(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows v, dg_rows q_out,
-                                       const dg_fp8_kv_cache* cache, const int64_t* slots, hipStream_t stream) {
+int dg_qk_norm_rope_fp8_kv_cache_write(const dg_norm_rope* a, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                    const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                    const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                    void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                    const dg_fp8_kv_cache* cache, const int64_t* slots, hipStream_t stream) {
+  const dg::Rows q_rows = rows(q, q_token_stride, q_head_stride);
+  const dg::Rows k_rows = rows(k, k_token_stride, k_head_stride);
+  const dg::Rows v_rows = rows(v, v_token_stride, v_head_stride);
+  const dg::Rows q_out_rows = rows(q_out, q_out_token_stride, q_out_head_stride);
   if (int s = check_call(a)) return s;
   if (int s = dg::check_cache(cache, a->num_tokens == 0)) return s;
   if (cache->num_heads != a->num_kv_heads || cache->head_dim != a->head_dim)
     return api_fail(DG_ERR_SHAPE, "the cache has %d heads of %d, the keys %d of %d", cache->num_heads, cache->head_dim, a->num_kv_heads, a->head_dim);
   if (a->num_tokens == 0) return api_ok();
-  if (int s = check_operand(a, "q", q)) return s;
-  if (int s = check_operand(a, "k", k)) return s;
-  if (int s = check_operand(a, "v", v)) return s;
-  if (int s = check_operand(a, "q_out", q_out)) return s;
+  if (int s = check_operand(a, "q", q_rows)) return s;
+  if (int s = check_operand(a, "k", k_rows)) return s;
+  if (int s = check_operand(a, "v", v_rows)) return s;
+  if (int s = check_operand(a, "q_out", q_out_rows)) return s;
   if (!slots) return api_fail(DG_ERR_NULL, "slots must not be NULL");
   if (!aligned(slots, 8)) return api_fail(DG_ERR_LAYOUT, "slots must be 8-byte aligned");
-  return forward(a, q, k, v, q_out, {}, cache, slots, stream);
+  return forward(a, q_rows, k_rows, v_rows, q_out_rows, {}, cache, slots, stream);
 }
 
 int64_t dg_qk_norm_rope_backward_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
@@ -144,20 +161,31 @@ int64_t dg_qk_norm_rope_backward_workspace(int32_t num_tokens, int32_t num_q_hea
   return backward_workspace(backward_workgroups(num_tokens, num_q_heads, num_kv_heads, head_dim, num_sms), head_dim);
 }
 
-int dg_qk_norm_rope_backward(const dg_norm_rope* a, dg_rows dq_out, dg_rows dk_out, dg_rows q, dg_rows k, dg_rows dq, dg_rows dk,
-                             float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+int dg_qk_norm_rope_backward(const dg_norm_rope* a, const void* dq_out, int64_t dq_out_token_stride, int64_t dq_out_head_stride,
+                    const void* dk_out, int64_t dk_out_token_stride, int64_t dk_out_head_stride,
+                    const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                    const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                    void* dq, int64_t dq_token_stride, int64_t dq_head_stride,
+                    void* dk, int64_t dk_token_stride, int64_t dk_head_stride,
+                    float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  const dg::Rows dq_out_rows = rows(dq_out, dq_out_token_stride, dq_out_head_stride);
+  const dg::Rows dk_out_rows = rows(dk_out, dk_out_token_stride, dk_out_head_stride);
+  const dg::Rows q_rows = rows(q, q_token_stride, q_head_stride);
+  const dg::Rows k_rows = rows(k, k_token_stride, k_head_stride);
+  const dg::Rows dq_rows = rows(dq, dq_token_stride, dq_head_stride);
+  const dg::Rows dk_rows = rows(dk, dk_token_stride, dk_head_stride);
   if (int s = check_call(a)) return s;
   if (!dq_weight || !dk_weight) return api_fail(DG_ERR_NULL, "dq_weight and dk_weight must not be NULL");
   if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return api_fail(DG_ERR_LAYOUT, "dq_weight and dk_weight must be 4-byte aligned");
   if (!a->q_weight || !a->k_weight || !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16))
     return api_fail(a->q_weight && a->k_weight ? DG_ERR_LAYOUT : DG_ERR_NULL, "q_weight and k_weight must be given, 16-byte aligned");
   if (a->num_tokens > 0) {
-    if (int s = check_operand(a, "dq_out", dq_out)) return s;
-    if (int s = check_operand(a, "dk_out", dk_out)) return s;
-    if (int s = check_operand(a, "q", q)) return s;
-    if (int s = check_operand(a, "k", k)) return s;
-    if (int s = check_operand(a, "dq", dq)) return s;
-    if (int s = check_operand(a, "dk", dk)) return s;
+    if (int s = check_operand(a, "dq_out", dq_out_rows)) return s;
+    if (int s = check_operand(a, "dk_out", dk_out_rows)) return s;
+    if (int s = check_operand(a, "q", q_rows)) return s;
+    if (int s = check_operand(a, "k", k_rows)) return s;
+    if (int s = check_operand(a, "dq", dq_rows)) return s;
+    if (int s = check_operand(a, "dk", dk_rows)) return s;
   }
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
@@ -167,12 +195,12 @@ int dg_qk_norm_rope_backward(const dg_norm_rope* a, dg_rows dq_out, dg_rows dk_o
   if (need > 0 && (!workspace || workspace_bytes < need))
     return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);
   if (need > 0 && !aligned(workspace, 16)) return api_fail(DG_ERR_LAYOUT, "workspace must be 16-byte aligned");
-  p.q = from_token(q, 0, 1);
-  p.k = from_token(k, 0, 1);
-  p.dq = from_token(dq_out, 0, 1);
-  p.dk = from_token(dk_out, 0, 1);
-  p.q_out = from_token(dq, 0, 1);
-  p.k_out = from_token(dk, 0, 1);
+  p.q = q_rows;
+  p.k = k_rows;
+  p.dq = dq_out_rows;
+  p.dk = dk_out_rows;
+  p.q_out = dq_rows;
+  p.k_out = dk_rows;
   p.dq_weight = dq_weight;
   p.dk_weight = dk_weight;
   p.parts = static_cast<float*>(workspace);

@@ -146,19 +146,27 @@ int check_columns(int32_t table_cols) {
 // Attention: tokens of a tile, and workgroups that share its keys.
 struct SparsePlan {
   int64_t tile_tokens, head_tiles, items, parts;
+  int waves;
 };
 SparsePlan sparse_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int32_t top, int num_sms) {
   const int32_t group = a.num_q_heads / num_kv_heads;
   SparsePlan pl;
   pl.tile_tokens = group > 16 ? 1 : 16 / group;
+  if (pl.tile_tokens > a.most_tokens()) pl.tile_tokens = a.most_tokens();
   if (pl.tile_tokens * top > kMaxListed) pl.tile_tokens = top < kMaxListed ? kMaxListed / top : 1;
   pl.head_tiles = ceil_div(group, 16);
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
   const int64_t with_rows = a.total_q / pl.tile_tokens + a.batch;  // of the items, at most
   const int64_t work = (with_rows < pl.items ? with_rows : pl.items) * num_kv_heads * pl.head_tiles;
-  const int64_t tokens = a.most_tokens() < pl.tile_tokens ? a.most_tokens() : pl.tile_tokens;
-  const int64_t segments = tokens * top * ceil_div(page_size, 64), slots = int64_t(num_sms) * (head_dim == 256 ? 1 : 3);
+  const int64_t segments = pl.tile_tokens * top * ceil_div(page_size, 64), slots = int64_t(num_sms) * (head_dim == 256 ? 1 : 3);
   pl.parts = 1;
+  pl.waves = 4;
+  // Short lists of few tiles: eight waves instead of parts, whose second kernel costs the host more than it saves the device.  (At
+  // 256 values a head eight waves run out of registers.)
+  if (head_dim != 256 && work <= num_sms && segments > 4 && segments <= 20) {
+    pl.waves = 8;
+    return pl;
+  }
   while (pl.parts < 64 && 2 * pl.parts * work <= slots && 8 * pl.parts <= segments) pl.parts *= 2;
   return pl;
 }
@@ -289,7 +297,7 @@ int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, i
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
   const SparsePlan pl = sparse_plan(a, cache->num_heads, cache->head_dim, cache->page_size, top, num_sms);
-  if (int s = check_grid(a, pl.items * cache->num_heads * pl.head_tiles * (pl.parts > 16 ? pl.parts : 16), 256)) return s;
+  if (int s = check_grid(a, pl.items * cache->num_heads * pl.head_tiles * (pl.parts > 16 ? pl.parts : 16), pl.waves * 64)) return s;
   const int64_t need = workspace_of(pl, cache->num_heads, cache->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);
@@ -310,6 +318,7 @@ int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, i
   p.tile_tokens = int32_t(pl.tile_tokens);
   p.head_tiles = int32_t(pl.head_tiles);
   p.items = int32_t(pl.items);
+  p.waves = pl.waves;
   p.parts = int32_t(pl.parts);
   p.part_o = static_cast<float*>(workspace);
   p.part_mz = p.part_o + (pl.parts > 1 ? part_rows(pl, cache->num_heads) * cache->head_dim : 0);

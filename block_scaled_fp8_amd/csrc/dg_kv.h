@@ -168,6 +168,7 @@ struct SparseParams {
   FastDiv group;             // query heads per key head
   FastDiv q_tiles;           // tiles of tokens per sequence
   int32_t tile_tokens, head_tiles, items;  // tokens of a tile, tiles of 16 heads of a token (one of the two is 1), batch * q_tiles
+  int32_t waves;             // of a workgroup: 4 or 8
   int32_t parts;             // workgroups that share a tile and key head (a power of two)
   float* part_o;             // [items, heads, head_tiles, parts, 16, head dim] (parts > 1)
   float* part_mz;            // [.., 16, 2]

@@ -24,7 +24,7 @@ namespace sparse {
 
 using namespace attn;
 
-constexpr int WAVES = 4, SEGMENT = 64;
+constexpr int SEGMENT = 64;
 
 // A workgroup's tile, key head and share.
 struct Tile {
@@ -167,7 +167,7 @@ __device__ __forceinline__ bool next_segment(const SparseParams& p, const Tile& 
   return true;
 }
 
-template <int D, bool SHARED>
+template <int D, bool SHARED, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(const SparseParams p) {
   constexpr int KEYS = 32, TILE = KEYS * D * 2;
   constexpr int CH = D / 16, PASS = 64 / CH, NP = KEYS / PASS;  // V: 16-code chunks of a row, rows of a load, loads
@@ -519,10 +519,19 @@ __global__ void __launch_bounds__(256) join_kernel(const SparseParams p) {
 template <int D>
 hipError_t launch(const SparseParams& p, hipStream_t stream) {
   const unsigned tiles = (unsigned)((int64_t)p.items * p.c.num_heads * p.head_tiles);
-  if (p.tile_tokens > 1)
-    hipLaunchKernelGGL((sparse_kernel<D, true>), dim3(tiles * p.parts), dim3(WAVES * 64), (size_t)p.tile_tokens * p.top * 4, stream, p);
-  else
-    hipLaunchKernelGGL((sparse_kernel<D, false>), dim3(tiles * p.parts), dim3(WAVES * 64), 0, stream, p);
+  const size_t lists = (size_t)p.tile_tokens * p.top * 4;
+  if (p.waves == 4 && p.tile_tokens > 1)
+    hipLaunchKernelGGL((sparse_kernel<D, true, 4>), dim3(tiles * p.parts), dim3(256), lists, stream, p);
+  else if (p.waves == 4)
+    hipLaunchKernelGGL((sparse_kernel<D, false, 4>), dim3(tiles * p.parts), dim3(256), 0, stream, p);
+  else if constexpr (D != 256) {
+    if (p.tile_tokens > 1)
+      hipLaunchKernelGGL((sparse_kernel<D, true, 8>), dim3(tiles * p.parts), dim3(512), lists, stream, p);
+    else
+      hipLaunchKernelGGL((sparse_kernel<D, false, 8>), dim3(tiles * p.parts), dim3(512), 0, stream, p);
+  } else {
+    return hipErrorInvalidValue;
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.parts == 1) return e;
   hipLaunchKernelGGL((join_kernel<D>), dim3(tiles * 16), dim3(256), 0, stream, p);

@@ -555,14 +555,12 @@ typedef struct {
   float eps;
 } dg_norm_rope;
 
-/* Rows of an operand: [num_tokens, heads, head_dim], strides in elements. */
-typedef struct {
-  void* p;
-  int64_t token_stride, head_stride;
-} dg_rows;
-
 /* q_out and k_out may be q and k themselves.  num_tokens == 0 is a no-op. */
-int dg_qk_norm_rope(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows q_out, dg_rows k_out, hipStream_t stream);
+int dg_qk_norm_rope(const dg_norm_rope* a, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                        void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                        void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                        hipStream_t stream);
 
 /*
  * Its gradients: dq_out, dk_out (of the results) and the forward call's q and k -> dq and dk (written), and the
@@ -571,8 +569,13 @@ int dg_qk_norm_rope(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows q_out, 
  * matter.  No atomics: the same call gives the same bits (the order of sums follows from the shape and the number of compute
  * units, dg_set_num_sms).
  */
-int dg_qk_norm_rope_backward(const dg_norm_rope* a, dg_rows dq_out, dg_rows dk_out, dg_rows q, dg_rows k, dg_rows dq, dg_rows dk,
-                             float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int dg_qk_norm_rope_backward(const dg_norm_rope* a, const void* dq_out, int64_t dq_out_token_stride, int64_t dq_out_head_stride,
+                        const void* dk_out, int64_t dk_out_token_stride, int64_t dk_out_head_stride,
+                        const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                        void* dq, int64_t dq_token_stride, int64_t dq_head_stride,
+                        void* dk, int64_t dk_token_stride, int64_t dk_head_stride,
+                        float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, hipStream_t stream);
 /* Bytes of its workspace (0: none), or a negative dg_status. */
 int64_t dg_qk_norm_rope_backward_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
 
@@ -582,8 +585,11 @@ int64_t dg_qk_norm_rope_backward_workspace(int32_t num_tokens, int32_t num_q_hea
  * and values are not written, nor those of a slot that is negative or past the cache; no slot may be given twice.
  * cache->head_dim and num_heads are those of `a`.
  */
-int dg_qk_norm_rope_fp8_kv_cache_write(const dg_norm_rope* a, dg_rows q, dg_rows k, dg_rows v, dg_rows q_out,
-                                       const dg_fp8_kv_cache* cache, const int64_t* slots, hipStream_t stream);
+int dg_qk_norm_rope_fp8_kv_cache_write(const dg_norm_rope* a, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                        const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                        void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                        const dg_fp8_kv_cache* cache, const int64_t* slots, hipStream_t stream);
 
 /* align(mn, 16 / elem_bytes): the padded MN extent of an MN-major scale tensor whose
  * K slices start on 16-byte boundaries (page "02 · DeepGEMM 技术解析" §3.1, ALIGN_MN).

@@ -24,21 +24,20 @@ def call(**kw):
 
 
 def rows(name, kw):
-    p, ts, hs = kw.get(name, (P, 1024, 128))
-    return dg._Rows(p, ts, hs)
+    return kw.get(name, (P, 1024, 128))
 
 
 def forward(**kw):
-    return dg.lib().dg_qk_norm_rope(call(**kw), *[rows(x, kw) for x in ("q", "k", "q_out", "k_out")], None)
+    return dg.lib().dg_qk_norm_rope(call(**kw), *sum((rows(x, kw) for x in ("q", "k", "q_out", "k_out")), ()), None)
 
 
 def backward(**kw):
-    return dg.lib().dg_qk_norm_rope_backward(call(**kw), *[rows(x, kw) for x in ("dq_out", "dk_out", "q", "k", "dq", "dk")],
+    return dg.lib().dg_qk_norm_rope_backward(call(**kw), *sum((rows(x, kw) for x in ("dq_out", "dk_out", "q", "k", "dq", "dk")), ()),
                                              kw.get("dqw", P), kw.get("dkw", P), kw.get("work"), kw.get("work_bytes", 0), None)
 
 
 def write(c=None, **kw):
-    return dg.lib().dg_qk_norm_rope_fp8_kv_cache_write(call(**kw), *[rows(x, kw) for x in ("q", "k", "v", "q_out")],
+    return dg.lib().dg_qk_norm_rope_fp8_kv_cache_write(call(**kw), *sum((rows(x, kw) for x in ("q", "k", "v", "q_out")), ()),
                                                        ctypes.byref(cache() if c is None else c), kw.get("slots", P), None)
 
 
@@ -74,7 +73,7 @@ def test_refusals_of_each():
         assert write(cache(**kw), **({"head_dim": kw["head_dim"]} if kw.get("head_dim") == 0 else {})) in (code, UNSUPPORTED), kw
     assert write(cache(num_heads=5, page_stride=16384)) == SHAPE and write(cache(head_dim=64)) == SHAPE
     assert write(slots=None) == NULL and write(slots=P_ODD) == LAYOUT and write(v=(None, 1024, 128)) == NULL
-    assert dg.lib().dg_qk_norm_rope(None, *[dg._Rows(P, 1024, 128)] * 4, None) == NULL
+    assert dg.lib().dg_qk_norm_rope(None, *[P, 1024, 128] * 4, None) == NULL
     # no tokens: nothing is read or written, so pointers may be NULL
     none = dict(num_tokens=0, q_weight=None, k_weight=None, cos_sin=None, positions=None)
     assert forward(**none, q=(None, 0, 0), q_out=(None, 0, 0)) == DG_OK
