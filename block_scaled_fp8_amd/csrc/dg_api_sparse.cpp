@@ -148,6 +148,21 @@ struct SparsePlan {
   int64_t tile_tokens, head_tiles, items, parts;
   int waves;
 };
+// Segments of a list are 32-bit numbers to the kernel.
+int check_lists(int32_t top, int32_t page_size) {
+  if (top * ceil_div(page_size, 64) > kMaxIndex) return api_fail(DG_ERR_SHAPE, "top = %d blocks of %d tokens are more than 2^30 segments of 64", top, page_size);
+  return DG_OK;
+}
+
+// Whether offsets into the cache's keys (values) or scales pass 32 bits.
+bool is_far(const dg_fp8_kv_cache* c) {
+  auto end = [&](int64_t page, int64_t head, int64_t token, int64_t row) {
+    return double(c->num_pages - 1) * double(page) + double(c->num_heads - 1) * double(head) + double(c->page_size - 1) * double(token) + double(row);
+  };
+  return end(c->page_stride, c->head_stride, c->token_stride, c->head_dim) >= 4294967295.0 ||
+         end(c->sf_page_stride, c->sf_head_stride, c->sf_token_stride, 1) >= 4294967295.0;
+}
+
 SparsePlan sparse_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int32_t top, int num_sms) {
   const int32_t group = a.num_q_heads / num_kv_heads;
   SparsePlan pl;
@@ -274,6 +289,7 @@ int64_t dg_fp8_block_sparse_attention_workspace(int32_t batch, int32_t total_q, 
     return api_fail(DG_ERR_UNSUPPORTED, "head_dim = %d: 64, 128 and 256 are supported", head_dim);
   if (int s = check_batch(a, num_kv_heads, top)) return s;
   if (page_size <= 0) return api_fail(DG_ERR_SHAPE, "page_size = %d must be positive", page_size);
+  if (int s = check_lists(top, page_size)) return s;
   if (a.empty()) return 0;
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
@@ -290,6 +306,7 @@ int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, i
   if (int s = check_batch(a, cache->num_heads, top)) return s;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return api_fail(DG_ERR_SHAPE, "sm_scale must be positive and finite");
   if (int s = check_table(table_cols, table_stride, cache->page_size)) return s;
+  if (int s = check_lists(top, cache->page_size)) return s;
   if (a.empty()) return api_ok();
   if (int s = check_sequences(q, q_token_stride, q_head_stride, cu_seqlens_q, block_table, table_cols, seq_lens, blocks)) return s;
   if (int s = check_rows("out", out, o_token_stride, o_head_stride, 2)) return s;
@@ -313,12 +330,14 @@ int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, i
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.top = top;
   p.list = dg::fast_div(top);
+  p.segments = dg::fast_div(int32_t(ceil_div(cache->page_size, 64)));
   p.group = dg::fast_div(num_q_heads / cache->num_heads);
   p.q_tiles = dg::fast_div(int32_t(pl.items / batch));
   p.tile_tokens = int32_t(pl.tile_tokens);
   p.head_tiles = int32_t(pl.head_tiles);
   p.items = int32_t(pl.items);
-  p.waves = pl.waves;
+  p.far = is_far(cache);
+  p.waves = p.far ? 4 : pl.waves;
   p.parts = int32_t(pl.parts);
   p.part_o = static_cast<float*>(workspace);
   p.part_mz = p.part_o + (pl.parts > 1 ? part_rows(pl, cache->num_heads) * cache->head_dim : 0);

@@ -102,9 +102,10 @@ __device__ __forceinline__ float groups_sum(float x) {
   return both_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// Buffer descriptor from a scalar address on, 2^31 - 1 bytes long (the host keeps a head's page below that).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((int64_t)base), (short)0, 0x7FFFFFFF, 0x00020000);
+// Buffer descriptor from a scalar address on, 2^31 - 1 bytes long (the host keeps a head's page below that).  With 0 bytes, loads
+// give zeros and read nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base, int bytes = 0x7FFFFFFF) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((int64_t)base), (short)0, bytes, 0x00020000);
 }
 
 }  // namespace attn

@@ -165,10 +165,12 @@ struct SparseParams {
   float scale_log2;          // softmax scale * log2(e)
   int32_t top;
   FastDiv list;              // `top` as a divisor
+  FastDiv segments;          // of 64 keys, of a block
   FastDiv group;             // query heads per key head
   FastDiv q_tiles;           // tiles of tokens per sequence
   int32_t tile_tokens, head_tiles, items;  // tokens of a tile, tiles of 16 heads of a token (one of the two is 1), batch * q_tiles
   int32_t waves;             // of a workgroup: 4 or 8
+  int32_t far;               // 1: offsets into the cache may need more than 32 bits (4 waves)
   int32_t parts;             // workgroups that share a tile and key head (a power of two)
   float* part_o;             // [items, heads, head_tiles, parts, 16, head dim] (parts > 1)
   float* part_mz;            // [.., 16, 2]

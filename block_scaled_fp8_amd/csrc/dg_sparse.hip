@@ -14,9 +14,11 @@
 // Lane group g (lane / 16) and column lane % 16 have the roles that they have in attention of few rows over all keys: S^T in
 // blocks of 16 keys, lane group g with keys 4 g + i of its column's query.
 //
-// The entries of a tile's lists go 64 to a wave at a time, one a lane: a lane looks its block up in the other tokens' lists (they
-// ascend), and drops it where an earlier one has it.  The remaining ones, in segments of 64 tokens, are dealt
-// in turn to the waves of the tile's workgroups, which find their own without asking each other.
+// The lists' blocks, in segments of 64 keys, go 32 to a wave at a time, one a lane: a lane looks its block up in the other tokens' lists (they
+// ascend), and drops it where an earlier one has it.  The remaining ones are dealt in turn to the waves of the tile's workgroups, which find
+// their own without asking each other, and put them into LDS as halves of 16 keys, two of which make a wave's tile.
+#include <type_traits>
+
 #include "dg_attn_device.h"
 
 namespace dg {
@@ -24,7 +26,9 @@ namespace sparse {
 
 using namespace attn;
 
+typedef int v2i __attribute__((ext_vector_type(2)));
 constexpr int SEGMENT = 64;
+constexpr float MOST_BF16 = 0x1.FEp127f;
 
 // A workgroup's tile, key head and share.
 struct Tile {
@@ -78,13 +82,6 @@ __device__ __forceinline__ Row row_of(const SparseParams& p, const Tile& t, int 
   return {token, t.kv_head * p.group.d + t.head0 + r - token * p.group.d};
 }
 
-// A tile's entries of the blocks' lists, 64 of the tile's at a time.
-struct Entries {
-  int block, page;  // this lane's: its block, its page of the cache
-  unsigned tokens;  // whose lists have it, by bits; 0: none, or an earlier entry stands for it
-  int number;       // number among the entries that stand
-};
-
 // The first of `top` ascending numbers (negative ones, at the end, count as larger than all) that is not below v: whether it is v.
 __device__ __forceinline__ bool has(const int32_t* list, int top, int v) {
   int at = 0, n = top;
@@ -100,84 +97,181 @@ __device__ __forceinline__ bool has(const int32_t* list, int top, int v) {
   return at < top && list[at] == v;
 }
 
-// SHARED: several tokens, whose lists lie one after the other in LDS; else the one token's list in memory.
-template <bool SHARED>
-__device__ __forceinline__ void load_entries(const SparseParams& p, const Tile& t, const int32_t* lists, int from, int before, Entries& e) {
-  const int lane = threadIdx.x & 63, i = from + lane;
-  e.tokens = 0;
-  e.block = e.page = 0;
-  if (i < t.tokens * p.top) {
-    const int b = lists[i];
-    // (blocks past the tile's last token hold no key that counts)
-    if (b >= 0 && b < p.s.table_cols && b * p.c.page.d < t.key_end) {
-      unsigned tokens = 1u;
+// Up to 16 keys of one block.
+template <bool FAR>
+struct Half {
+  using Offset = std::conditional_t<FAR, int64_t, uint32_t>;
+  Offset code, sf;  // of the first one, in bytes
+  int key0, keys;   // place of the first one in the sequence, and how many there are
+  unsigned tokens;  // whose lists have them, by bits
+};
+// In LDS: words of one; and how many there may be, of AT_ONCE segments, of which at most every fourth is the wave's, after one that was left, and
+// with the copy that makes an odd number even.  (With 64 segments at once, LDS would hold one workgroup less.)
+template <bool FAR>
+constexpr int HALF_WORDS = FAR ? 8 : 4;
+constexpr int AT_ONCE = 32, MOST_HALVES = 4 * AT_ONCE / 4 + 2;
+
+// A wave's halves.
+struct Walk {
+  int share, shares;     // segments of number `share` modulo `shares` (a power of two, 4 at least) are the wave's
+  int from, all, before; // next segments of lists, how many there are, and the number of those that stand before them
+  int at, count;         // the halves in LDS
+};
+
+// The halves of the next AT_ONCE segments of the tile's lists, one segment a lane.  SHARED: several tokens, whose lists lie one after the other in
+// LDS; else the one token's list in memory.
+template <bool SHARED, bool FAR>
+__device__ __forceinline__ void find_halves(const SparseParams& p, const Tile& t, const int32_t* lists, uint32_t* halves, Walk& w) {
+  const int lane = threadIdx.x & 63, u = w.from + lane;
+  const uint64_t below = (1ull << lane) - 1;
+  unsigned tokens = 0;
+  int block = 0, offset = 0;
+  if (lane < AT_ONCE && u < w.all) {
+    const int i = div(u, p.segments);
+    offset = (u - i * p.segments.d) * SEGMENT;
+    block = lists[i];
+    // (keys past the tile's last token do not count)
+    if (block >= 0 && block < p.s.table_cols && block * p.c.page.d + offset < t.key_end) {
+      tokens = 1u;
       if (SHARED) {
         const int mine = div(i, p.list);
         tokens = 1u << mine;
         for (int x = 0; x < t.tokens; ++x)
-          if (x != mine && has(lists + x * p.top, p.top, b)) tokens |= 1u << x;
-        if (tokens & ((1u << mine) - 1)) tokens = 0;
-      }
-      if (tokens) {
-        const int pg = p.s.table[t.seq * p.s.table_stride + b];
-        e.tokens = tokens;
-        e.block = b;
-        e.page = (unsigned)pg < (unsigned)p.c.num_pages ? pg : 0;  // (the host cannot see the table's contents)
+          if (x != mine && has(lists + x * p.top, p.top, block)) tokens |= 1u << x;
+        if (tokens & ((1u << mine) - 1)) tokens = 0;  // (an earlier token's entry stands for it)
       }
     }
   }
-  e.number = before + (int)__popcll(__ballot(e.tokens != 0) & ((1ull << lane) - 1));
+  const uint64_t stand = __ballot(tokens != 0);
+  const int number = w.before + (int)__popcll(stand & below);
+  const bool mine = tokens != 0 && (number & (w.shares - 1)) == w.share;
+  const int key0 = block * p.c.page.d + offset, keys = mine ? min(min(p.c.page.d - offset, SEGMENT), t.key_end - key0) : 0;
+  const int n = (keys + 15) >> 4;  // 0 to 4
+  const uint64_t b0 = __ballot(n & 1), b1 = __ballot(n & 2), b2 = __ballot(n & 4);
+  if (mine) {
+    const int pg = p.s.table[t.seq * p.s.table_stride + block];
+    const int64_t page = (unsigned)pg < (unsigned)p.c.num_pages ? pg : 0;  // (the host cannot see the table's contents)
+    const int64_t code = page * p.c.page_stride + t.kv_head * p.c.head_stride + offset * p.c.token_stride;
+    const int64_t sf = page * p.c.sf_page_stride + t.kv_head * p.c.sf_head_stride + offset * p.c.sf_token_stride;
+    uint32_t* to = halves + (w.count + (int)__popcll(b0 & below) + 2 * (int)__popcll(b1 & below) + 4 * (int)__popcll(b2 & below)) * HALF_WORDS<FAR>;
+    for (int x = 0; x < n; ++x, to += HALF_WORDS<FAR>) {
+      const int64_t c = code + 16 * x * p.c.token_stride, f = sf + 16 * x * p.c.sf_token_stride;
+      *(v4u*)to = (v4u){(uint32_t)c, (uint32_t)f, (uint32_t)(key0 + 16 * x), (uint32_t)min(16, keys - 16 * x) | tokens << 16};
+      if (FAR) *(v2u*)(to + 4) = (v2u){(uint32_t)(c >> 32), (uint32_t)(f >> 32)};
+    }
+  }
+  w.count += (int)__popcll(b0) + 2 * (int)__popcll(b1) + 4 * (int)__popcll(b2);
+  w.before += (int)__popcll(stand);
+  w.from += AT_ONCE;
 }
 
-// 16 keys of one block.
-struct Half {
-  int page, offset, key0;  // place of the first key within its page, and in the sequence
-  int keys;                // how many there are (0: none)
-  unsigned tokens;
-};
-
-// A wave's segments, 16 keys at a time.  `share` of `shares` (a power of two).
-struct Walk {
-  Entries e;
-  uint64_t left;           // lanes whose entries are still to come
-  int from, before;        // next entries, and the number of those that stand before them
-  int block, page, segment, offset, end;  // the present entry; place within its page
-  unsigned tokens;
-};
-
-template <bool SHARED>
-__device__ __forceinline__ bool next_segment(const SparseParams& p, const Tile& t, const int32_t* lists, int segments, int share, int shares, Walk& w) {
-  w.segment += shares;
-  while (w.segment >= segments) {
-    while (!w.left) {
-      if (w.from >= t.tokens * p.top) return false;
-      load_entries<SHARED>(p, t, lists, w.from, w.before, w.e);
-      w.from += 64;
-      w.before += (int)__popcll(__ballot(w.e.tokens != 0));
-      // segment s of entry n is number n * segments + s
-      w.left = __ballot(w.e.tokens != 0 && (int)((unsigned)(share - w.e.number * segments) & (unsigned)(shares - 1)) < segments);
+// The wave's next 32 keys, as two halves; the second one may be a copy of the first that no query sees.  false: there are none.
+// (The wave reads what its own lanes wrote: its LDS operations complete in order, so only the compiler has to keep theirs.)
+template <bool SHARED, bool FAR>
+__device__ __forceinline__ bool next_tile(const SparseParams& p, const Tile& t, const int32_t* lists, uint32_t* halves, Walk& w, Half<FAR> (&h)[2]) {
+  constexpr int WORDS = HALF_WORDS<FAR>;
+  if (w.at + 2 > w.count) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int lane = threadIdx.x & 63;
+    const bool left = w.at < w.count;
+    if (left && lane < WORDS) halves[lane] = halves[w.at * WORDS + lane];
+    w.at = 0;
+    w.count = left ? 1 : 0;
+    while (w.count < 2 && w.from < w.all) find_halves<SHARED, FAR>(p, t, lists, halves, w);
+    if (w.count == 0) return false;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (w.count == 1) {
+      if (lane < WORDS) halves[WORDS + lane] = lane == 3 ? halves[3] & 0xFFFFu : halves[lane];
+      w.count = 2;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    const int l = __builtin_ctzll(w.left);
-    w.left &= w.left - 1;
-    w.block = __builtin_amdgcn_readlane(w.e.block, l);
-    w.page = __builtin_amdgcn_readlane(w.e.page, l);
-    w.tokens = (unsigned)__builtin_amdgcn_readlane((int)w.e.tokens, l);
-    w.segment = (share - __builtin_amdgcn_readlane(w.e.number, l) * segments) & (shares - 1);
   }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t* from = halves + (w.at + x) * WORDS;
+    const v4u a = *(const v4u*)from;
+    const uint32_t last = (uint32_t)uniform((int)a.w);
+    h[x].code = (uint32_t)uniform((int)a.x);
+    h[x].sf = (uint32_t)uniform((int)a.y);
+    h[x].key0 = uniform((int)a.z);
+    h[x].keys = (int)(last & 0xFFFFu);
+    h[x].tokens = last >> 16;
+    if constexpr (FAR) {
+      const v2u b = *(const v2u*)(from + 4);
+      h[x].code |= (int64_t)uniform((int)b.x) << 32;
+      h[x].sf |= (int64_t)uniform((int)b.y) << 32;
+    }
+  }
+  w.at += 2;
   return true;
 }
 
-template <int D, bool SHARED, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(const SparseParams p) {
-  constexpr int KEYS = 32, TILE = KEYS * D * 2;
-  constexpr int CH = D / 16, PASS = 64 / CH, NP = KEYS / PASS;  // V: 16-code chunks of a row, rows of a load, loads
+// V tiles lie in LDS as codes, rows of D bytes in 16-byte chunks.  A transposing read takes the same chunk of 32 rows, 8 to a lane group, which
+// are spread over all banks.
+template <int D>
+__device__ __forceinline__ int v_swizzle(int row) {
+  return D == 64 ? row >> 2 & 3 : D == 128 ? row >> 1 & 7 : row & 15;
+}
+
+// Codes that are NaN become zeros.
+__device__ __forceinline__ v4u clear_nan(v4u x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] &= ~(((((x[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
+  return x;
+}
+
+// 16 bytes a lane from `base` + `at` + `also` to LDS, the lanes' one after the other from `dst` on; or a byte, as a word.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t base, int at, int also, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (DG_LDS void*)dst, 16, at, also, 0, 0);
+}
+__device__ __forceinline__ void copy_byte_to_lds(__amdgpu_buffer_rsrc_t base, int at, int also, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (DG_LDS void*)dst, 1, at, also, 0, 0);
+}
+
+// Reads of LDS that copies have filled.  In assembly, each with its own wait: before a read that it knows to be one of LDS, the compiler
+// waits for all copies that are on their way to LDS, those of the next tile too.  The caller waits for the ones it reads.
+//
+// Two 16-byte pieces, 256 bytes apart:
+__device__ __forceinline__ void read_copied(uint32_t at, v4u& a, v4u& b) {
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:256\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(a), "=&v"(b)
+               : "v"(at)
+               : "memory");
+}
+// Four transposing reads: in each group of 16 lanes, lane 2 r + h names an 8-byte row (r = 0..7, h = 0..1), and lane 8 h + c gets byte c of
+// the rows 0..7 of its half h.
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[4], v2i (&x)[4]) {
+  asm volatile("ds_read_b64_tr_b8 %0, %4\n\tds_read_b64_tr_b8 %1, %5\n\tds_read_b64_tr_b8 %2, %6\n\tds_read_b64_tr_b8 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(const DG_LDS uint8_t*)p; }
+// Wait until at most N vector-memory operations of this wave are on their way.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt is a 6-bit field");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// What bounds it: memory latency and the vector unit, which is busy about half of the time.  So a wave keeps K of the next 32 keys on their way to
+// registers, and V of the next 64 to a ring of two tiles in LDS, where the copies take no registers (128 of them let four waves share a SIMD).
+template <int D, bool SHARED, int WAVES, bool FAR>
+__global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse_kernel(const SparseParams p) {
+  constexpr int KEYS = 32, TILE = KEYS * D;
+  constexpr int CH = D / 16, PASS = 64 / CH, NP = KEYS / PASS;  // V: 16-code chunks of a row, rows of a copy, copies
   constexpr int JD = 64;                                        // values of D joined at once
   constexpr int JOIN = WAVES * 16 * (JD + 4) * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * TILE > JOIN ? WAVES * TILE : JOIN];
+  __shared__ __attribute__((aligned(256))) uint8_t lds[WAVES * 2 * TILE > JOIN ? WAVES * 2 * TILE : JOIN];
+  __shared__ __attribute__((aligned(16))) uint32_t v_scales[WAVES][2][2][64];  // scale codes of a half's values, 16 of them, four times
+  __shared__ __attribute__((aligned(16))) uint32_t halves[WAVES][MOST_HALVES * HALF_WORDS<FAR>];
   __shared__ float mz[WAVES][2][16];
   extern __shared__ int32_t tile_lists[];  // [tile_tokens][top] (SHARED)
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), g = lane >> 4, col = lane & 15;
-  uint8_t* vt = lds + wave * TILE;
+  uint8_t* vt = lds + wave * 2 * TILE;
   Tile t;
   if (!get_tile(p, t, blockIdx.x, p.parts)) return;
   const Row row = row_of(p, t, col);
@@ -202,216 +296,197 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) sparse_kernel(co
     __syncthreads();
     lists = tile_lists;
   }
-  const int segments = (p.c.page.d + SEGMENT - 1) / SEGMENT, shares = WAVES * p.parts, share = t.part * WAVES + wave;
-  const int64_t head_at = t.kv_head * p.c.head_stride, head_sf = t.kv_head * p.c.sf_head_stride;
   const unsigned every = (1u << t.tokens) - 1;
-
   Walk w;
-  // the next 16 keys of the wave's share
-  auto next_half = [&](Half& h) {
-    if (w.offset >= w.end) {
-      if (!next_segment<SHARED>(p, t, lists, segments, share, shares, w)) {
-        h.keys = 0;
-        h.tokens = 0;
-        return;
-      }
-      w.offset = w.segment * SEGMENT;
-      w.end = min(min(p.c.page.d, w.offset + SEGMENT), t.key_end - w.block * p.c.page.d);
-      if (w.end <= w.offset) {  // (a segment past the last token's place)
-        h.keys = -1;
-        return;
-      }
-    }
-    h.page = w.page;
-    h.offset = w.offset;
-    h.key0 = w.block * p.c.page.d + w.offset;
-    h.keys = min(16, w.end - w.offset);
-    h.tokens = w.tokens;
-    w.offset += 16;
-  };
-  auto start = [&]() {
-    w.left = 0;
-    w.from = w.before = 0;
-    w.segment = segments;
-    w.offset = w.end = 0;
-  };
-  // the next 32: two halves, the second one maybe empty (a copy of the first then, which no query sees)
-  auto next_tile = [&](Half (&h)[2]) {
-    do next_half(h[0]);
-    while (h[0].keys < 0);
-    if (h[0].keys == 0) return false;
-    do next_half(h[1]);
-    while (h[1].keys < 0);
-    if (h[1].keys == 0) {
-      h[1] = h[0];
-      h[1].tokens = 0;
-    }
-    return true;
+  w.shares = WAVES * p.parts;
+  w.share = t.part * WAVES + wave;
+  w.all = t.tokens * p.top * p.segments.d;
+
+  // whether every row sees all 32 keys
+  auto is_whole = [&](const Half<FAR> (&h)[2]) {
+    return h[0].tokens == every && h[1].tokens == every && h[0].keys == 16 && h[1].keys == 16 && h[0].key0 + 15 <= t.place0 && h[1].key0 + 15 <= t.place0;
   };
 
-  v4u kr[2][D / 64], vr[NP];
-  uint32_t ks[2], vs[NP];
-  // (through buffer descriptors of the pages, whose addresses are scalar)
-  auto fetch_k = [&](const Half (&h)[2]) {
+  // Rows past a half's keys repeat its last one.  Codes go through buffer descriptors of the pages, whose addresses are scalar; lane
+  // l % 32 has the scale code of key l % 32.
+  v4u kr[2][D / 64];
+  uint8_t ks[2];  // (bytes until they are used: wider, they would be widened, and so waited for, where they are loaded)
+  // Everything goes through buffer descriptors of the cache, with the half's offset in a scalar register.  (FAR, for caches of 4 GiB and more:
+  // descriptors of the half.)  Rows past a half's keys repeat its last one; `some` false: all repeat the first one.  (The loads are issued all the
+  // same: past a branch the compiler would wait for all that is on its way.)
+  const int ts = (int)p.c.token_stride, sts = (int)p.c.sf_token_stride;
+  const int k_row = col * ts, k_chunk = 16 * g, sf_row = col * sts, v_row = lane / CH;
+  auto from = [&](const uint8_t* base, typename Half<FAR>::Offset at) { return rsrc(FAR ? base + at : base, -1); };
+  auto also = [&](typename Half<FAR>::Offset at) { return FAR ? 0 : (int)at; };
+  auto fetch_k = [&](const Half<FAR> (&h)[2], bool some) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int off = h[x].offset + min(col, h[x].keys - 1);
-      const __amdgpu_buffer_rsrc_t codes = rsrc(p.c.k + h[x].page * p.c.page_stride + head_at), sf = rsrc(p.c.k_sf + h[x].page * p.c.sf_page_stride + head_sf);
+      const int last = some ? h[x].keys - 1 : 0, at = min(k_row, last * ts) + k_chunk;
+      const __amdgpu_buffer_rsrc_t codes = from(p.c.k, h[x].code);
 #pragma unroll
-      for (int y = 0; y < D / 64; ++y) kr[x][y] = __builtin_amdgcn_raw_buffer_load_b128(codes, off * (int)p.c.token_stride + 16 * g + 64 * y, 0, 0);
-      ks[x] = __builtin_amdgcn_raw_buffer_load_b8(sf, off * (int)p.c.sf_token_stride, 0, 0);
+      for (int y = 0; y < D / 64; ++y) kr[x][y] = __builtin_amdgcn_raw_buffer_load_b128(codes, at + 64 * y, also(h[x].code), 0);
+      ks[x] = __builtin_amdgcn_raw_buffer_load_b8(from(p.c.k_sf, h[x].sf), min(sf_row, last * sts), also(h[x].sf), 0);
     }
   };
-  auto fetch_v = [&](const Half (&h)[2]) {
-    __amdgpu_buffer_rsrc_t codes[2], sf[2];
+  auto copy_v = [&](const Half<FAR> (&h)[2], int slot, bool some) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) codes[x] = rsrc(p.c.v + h[x].page * p.c.page_stride + head_at), sf[x] = rsrc(p.c.v_sf + h[x].page * p.c.sf_page_stride + head_sf);
+    for (int x = 0; x < 2; ++x) {
+      const int last = some ? h[x].keys - 1 : 0;
+      const __amdgpu_buffer_rsrc_t codes = from(p.c.v, h[x].code);
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int r = n * PASS + lane / CH, x = n * PASS / 16;  // (a load's rows are in one half)
-      const int off = h[x].offset + min(r & 15, h[x].keys - 1);
-      vr[n] = __builtin_amdgcn_raw_buffer_load_b128(codes[x], off * (int)p.c.token_stride + 16 * (lane % CH), 0, 0);
-      vs[n] = __builtin_amdgcn_raw_buffer_load_b8(sf[x], off * (int)p.c.sf_token_stride, 0, 0);
+      for (int n = x * NP / 2; n < (x + 1) * NP / 2; ++n) {
+        const int r = n * PASS + v_row;
+        copy_to_lds(codes, min((r & 15) * ts, last * ts) + 16 * (lane % CH ^ v_swizzle<D>(r)), also(h[x].code), vt + slot * TILE + n * 1024);
+      }
+      copy_byte_to_lds(from(p.c.v_sf, h[x].sf), min(sf_row, last * sts), also(h[x].sf), v_scales[wave][slot][x]);
     }
   };
 
   v4f o[D / 16];
   float m, z;
-  // A hidden value's weight is zero, which is not enough where it is NaN or infinite.  Nobody looks for such values at first: they
-  // leave a NaN in some output.  A wave that ends with an output that is no number goes over its keys again with care: what is no number among the values
-  // that some row does not see goes to LDS as zero, and is added at the end to the outputs of the rows that see it.
-  bool odd = false;  // the wave has cleared a value
-  Half now[2], next[2];
+  // A hidden value's weight is zero, which is not enough where it is NaN (or its scale so large that weights overflow).  Nobody looks for such
+  // values at first: they leave a NaN in some output.  A wave that ends with an output that is no number goes over its keys again with care: NaN among
+  // the values of tiles that some row does not see in whole go to the outputs of the rows that see them, and become zeros; no weight is infinite.
 #pragma unroll 1
   for (int careful = 0;; ++careful) {
-  m = NEG_INF, z = 0.f;
+    m = NEG_INF, z = 0.f;
 #pragma unroll
-  for (int d = 0; d < D / 16; ++d) o[d] = (v4f){0.f, 0.f, 0.f, 0.f};
-  start();
-  bool more = next_tile(now);
-  if (more) {
-    fetch_k(now);
-    fetch_v(now);
-  }
-  while (more) {
-    more = next_tile(next);
-    v4f s[2];
-    s[0] = s[1] = (v4f){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float scale = __uint_as_float(ks[x] << 23);
-#pragma unroll
-      for (int y = 0; y < D / 64; ++y) {
-        const v8bf lo = __builtin_bit_cast(v8bf, widen8(kr[x][y].x, kr[x][y].y, scale));
-        const v8bf hi = __builtin_bit_cast(v8bf, widen8(kr[x][y].z, kr[x][y].w, scale));
-        s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, q[2 * y], s[x], 0, 0, 0);
-        s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, q[2 * y + 1], s[x], 0, 0, 0);
-      }
+    for (int d = 0; d < D / 16; ++d) o[d] = (v4f){0.f, 0.f, 0.f, 0.f};
+    w.from = w.before = w.at = w.count = 0;
+    // Each turn issues V of a tile, works on the tile before, whose V and K are there or on their way, and issues K of the tile.
+    Half<FAR> now[2], next[2];
+    int slot = 1;  // of `next`
+    bool more = next_tile<SHARED, FAR>(p, t, lists, halves[wave], w, now);
+    if (more) {
+      copy_v(now, 0, true);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_k(now, true);
+      next[0] = now[0], next[1] = now[1];
     }
-    if (more) fetch_k(next);
+#pragma unroll 1
+    while (more) {
+      more = next_tile<SHARED, FAR>(p, t, lists, halves[wave], w, next);
+      copy_v(next, slot, more);  // (without more, `next` is still the last tile)
+      __builtin_amdgcn_sched_barrier(0);
+      v4f s[2];
+      s[0] = s[1] = (v4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const int r = lane / CH + n * PASS, c = lane % CH;
-      const float scale = __uint_as_float(vs[n] << 23);
-      *(v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c) * 16) = widen8(vr[n].x, vr[n].y, scale);
-      *(v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c + 1) * 16) = widen8(vr[n].z, vr[n].w, scale);
-    }
-    // whether every row sees all 32 keys
-    const bool whole = now[0].tokens == every && now[1].tokens == every && now[0].keys == 16 && now[1].keys == 16 &&
-                       now[0].key0 + 15 <= t.place0 && now[1].key0 + 15 <= t.place0;
-    if (!whole) {
-      if (__builtin_expect(careful, 0)) {
-        odd = true;
+      for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float scale = __uint_as_float((uint32_t)ks[x] << 23);
+          const v8bf lo = __builtin_bit_cast(v8bf, widen8(kr[x][y].x, kr[x][y].y, scale));
+          const v8bf hi = __builtin_bit_cast(v8bf, widen8(kr[x][y].z, kr[x][y].w, scale));
+          s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, q[2 * y], s[x], 0, 0, 0);
+          s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, q[2 * y + 1], s[x], 0, 0, 0);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_k(next, more);
+      __builtin_amdgcn_sched_barrier(0);
+      uint8_t* v = vt + (slot ^ 1) * TILE;
+      // (V of this tile is there, as its K is, which came later; said once more: only V and K of the next one may be on their way)
+      wait_vm<NP + 2 + D / 32 + 2>();
+      if (!is_whole(now)) {
+        // keys of each half that the lane's query sees: the first ones
+        int count[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          count[x] = now[x].tokens >> row.token & 1 ? min(now[x].keys, place - now[x].key0 + 1) : 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[x][e] = e < count[x] - 4 * g ? s[x][e] : NEG_INF;
+        }
+        if (__builtin_expect(careful, 0)) {
+          int l = lane;
+          asm volatile("" : "+v"(l));  // (so that no register holds what is computed from it through the loop)
 #pragma unroll 1
-        for (int n = 0; n < NP; ++n) {
-          const int r = lane / CH + n * PASS, c = lane % CH;
+          for (int j = 0; j < KEYS; ++j)
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              const uint32_t four = *(const uint32_t*)(v + j * D + 16 * (d ^ v_swizzle<D>(j)) + 4 * (l >> 4));
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((j & 15) < (j < 16 ? count[0] : count[1]) && (four >> 8 * e & 0x7F) == 0x7F) o[d][e] = __builtin_nanf("");
+            }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            v4u* at = (v4u*)(vt + r * 2 * D + narrow_chunk<D>(r, 2 * c + x) * 16);
-            *at = clear_odd(*at);
+          for (int n = 0; n < NP; ++n) {
+            v4u* at = (v4u*)(v + n * 1024 + l * 16);
+            *at = clear_nan(*at);
           }
         }
       }
-      // keys of each half that the lane's query sees: the first `count`
+      float top = s[0][0];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[x][e]);
+      top = groups_max(top) * p.scale_log2;  // (the scale is positive)
+      if (__any(top > m + SLACK)) {
+        const float raised = fmaxf(m, top);
+        const float f = raised == NEG_INF ? 1.f : exp2_hw(m - raised);
+        m = raised;
+        z *= f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[d] *= f;
+      }
+      const float sub = m == NEG_INF ? 0.f : -m;  // nothing seen yet: every weight is 2^-inf = 0
+      // (the wave reads what its other lanes wrote: its LDS operations complete in order, so only the compiler has to keep theirs)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      v4u x4, sf[2];
+      read_copied(lds_address(&v_scales[wave][slot ^ 1][0][4 * g]), sf[0], sf[1]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[x][e] = exp2_hw(__builtin_fmaf(s[x][e], p.scale_log2, sub));
+          z += s[x][e];
+        }
+      // The value's scale goes to its weight: exact, so the weight is rounded to BF16 as it would be without.
+      if (__builtin_expect(careful, 0)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float scaled = s[x][e] * __uint_as_float(sf[x][e] << 23);  // (a hidden place may hold any scale)
+            s[x][e] = s[x][e] == 0.f ? 0.f : scaled > MOST_BF16 ? MOST_BF16 : scaled;
+          }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[x][e] *= __uint_as_float(sf[x][e] << 23);
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int count = now[x].tokens >> row.token & 1 ? min(now[x].keys, place - now[x].key0 + 1) - 4 * g : 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = e < count ? s[x][e] : NEG_INF;
+        x4[2 * x] = pack2(s[x][0], s[x][1]);
+        x4[2 * x + 1] = pack2(s[x][2], s[x][3]);
       }
-    }
-    if (more) fetch_v(next);
-    float top = s[0][0];
+      const v8bf wt = __builtin_bit_cast(v8bf, x4);
+      // a transposing read takes a row of each of 8 keys in 2 lanes: those of the group's weights, 4 g.. and 16 + 4 g..
+      const int rr = col >> 1, key = rr < 4 ? 4 * g + rr : 12 + 4 * g + rr;
+      uint32_t at = lds_address(v) + key * D + 16 * v_swizzle<D>(key) + 8 * (lane & 1);
+      asm volatile("" : "+v"(at));  // (or D / 16 addresses would be held through the loop)
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+      for (int d0 = 0; d0 < D / 16; d0 += 4) {
+        v2i c[4];
+        const uint32_t from[4] = {at ^ 16 * d0, at ^ 16 * (d0 + 1), at ^ 16 * (d0 + 2), at ^ 16 * (d0 + 3)};
+        read_transposed(from, c);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, s[x][e]);
-    top = groups_max(top) * p.scale_log2;  // (the scale is positive)
-    if (__any(top > m + SLACK)) {
-      const float raised = fmaxf(m, top);
-      const float f = raised == NEG_INF ? 1.f : exp2_hw(m - raised);
-      m = raised;
-      z *= f;
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) o[d] *= f;
-    }
-    const float sub = m == NEG_INF ? 0.f : -m;  // nothing seen yet: every weight is 2^-inf = 0
-    v4u x4;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[x][e] = exp2_hw(__builtin_fmaf(s[x][e], p.scale_log2, sub));
-        z += s[x][e];
+        for (int d = 0; d < 4; ++d)
+          o[d0 + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, widen8((unsigned)c[d].x, (unsigned)c[d].y, 1.f)), wt, o[d0 + d], 0, 0, 0);
       }
-      x4[2 * x] = pack2(s[x][0], s[x][1]);
-      x4[2 * x + 1] = pack2(s[x][2], s[x][3]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      now[0] = next[0], now[1] = next[1];
+      slot ^= 1;
     }
-    const v8bf wt = __builtin_bit_cast(v8bf, x4);
-    // the wave reads what its other lanes wrote: its LDS operations complete in order, so only the
-    // compiler has to keep theirs
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const int r = 4 * g + (col >> 2);
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) {
-      const int at = r * 2 * D + narrow_chunk<D>(r, 2 * d + ((lane & 3) >> 1)) * 16 + (lane & 1) * 8;
-      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LDS v4s*)(vt + at));
-      const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LDS v4s*)(vt + at + 16 * 2 * D));
-      const v8s a = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), wt, o[d], 0, 0, 0);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    now[0] = next[0];
-    now[1] = next[1];
-  }
     if (careful) break;
     float sum = 0.f;  // (a NaN or infinity times zero is NaN)
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) sum += (o[d].x * 0.f + o[d].y * 0.f) + (o[d].z * 0.f + o[d].w * 0.f);
     if (__builtin_expect(!__any(sum != 0.f), 1)) break;
-  }
-
-  if (__builtin_expect(odd, 0)) {
-    start();
-    while (next_tile(now)) {
-      if (now[0].tokens == every && now[1].tokens == every && now[0].keys == 16 && now[1].keys == 16 && now[0].key0 + 15 <= t.place0 &&
-          now[1].key0 + 15 <= t.place0)
-        continue;
-      for (int x = 0; x < 2; ++x)
-        for (int j = 0; j < now[x].keys; ++j) {
-          const int off = now[x].offset + j;
-          const uint8_t* codes = p.c.v + now[x].page * p.c.page_stride + head_at + off * p.c.token_stride;
-          const uint32_t sf = p.c.v_sf[now[x].page * p.c.sf_page_stride + head_sf + off * p.c.sf_token_stride];
-          const bool sees = (now[x].tokens >> row.token & 1) && now[x].key0 + j <= place;
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            const v4f add = odd_values(*(const unsigned*)(codes + 16 * d + 4 * g), sf);
-            if (sees) o[d] += add;
-          }
-        }
-    }
   }
 
   // join the waves: rescale to the common maximum and add up through LDS, JD values of D at a time
@@ -471,12 +546,12 @@ __global__ void __launch_bounds__(256) join_kernel(const SparseParams p) {
   const Row row = row_of(p, t, r);
   float m = NEG_INF, z = 0.f;
   v4f o = {0.f, 0.f, 0.f, 0.f};
-  constexpr int AT_ONCE = 4;  // (loads that go out together)
-  for (int x = group; x < p.parts; x += G * AT_ONCE) {
-    v2f a[AT_ONCE];
-    v4f b[AT_ONCE];
+  constexpr int TOGETHER = 4;  // loads that go out together
+  for (int x = group; x < p.parts; x += G * TOGETHER) {
+    v2f a[TOGETHER];
+    v4f b[TOGETHER];
 #pragma unroll
-    for (int u = 0; u < AT_ONCE; ++u) {
+    for (int u = 0; u < TOGETHER; ++u) {
       a[u] = (v2f){NEG_INF, 0.f};
       if (x + u * G < p.parts) {
         const int64_t at = (t.slot + x + u * G) * 16 + r;
@@ -485,7 +560,7 @@ __global__ void __launch_bounds__(256) join_kernel(const SparseParams p) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < AT_ONCE; ++u) {
+    for (int u = 0; u < TOGETHER; ++u) {
       // no part, or one in which the row sees nothing (one whose scores are all NaN has no maximum either, but a NaN for its
       // sum, which stays)
       if (a[u].x == NEG_INF && a[u].y == 0.f) continue;
@@ -520,15 +595,23 @@ template <int D>
 hipError_t launch(const SparseParams& p, hipStream_t stream) {
   const unsigned tiles = (unsigned)((int64_t)p.items * p.c.num_heads * p.head_tiles);
   const size_t lists = (size_t)p.tile_tokens * p.top * 4;
-  if (p.waves == 4 && p.tile_tokens > 1)
-    hipLaunchKernelGGL((sparse_kernel<D, true, 4>), dim3(tiles * p.parts), dim3(256), lists, stream, p);
-  else if (p.waves == 4)
-    hipLaunchKernelGGL((sparse_kernel<D, false, 4>), dim3(tiles * p.parts), dim3(256), 0, stream, p);
-  else if constexpr (D != 256) {
-    if (p.tile_tokens > 1)
-      hipLaunchKernelGGL((sparse_kernel<D, true, 8>), dim3(tiles * p.parts), dim3(512), lists, stream, p);
+  const dim3 grid(tiles * p.parts), threads(p.waves * 64);
+  const bool shared = p.tile_tokens > 1;
+  if (p.far) {
+    if (shared)
+      hipLaunchKernelGGL((sparse_kernel<D, true, 4, true>), grid, threads, lists, stream, p);
     else
-      hipLaunchKernelGGL((sparse_kernel<D, false, 8>), dim3(tiles * p.parts), dim3(512), 0, stream, p);
+      hipLaunchKernelGGL((sparse_kernel<D, false, 4, true>), grid, threads, 0, stream, p);
+  } else if (p.waves == 4) {
+    if (shared)
+      hipLaunchKernelGGL((sparse_kernel<D, true, 4, false>), grid, threads, lists, stream, p);
+    else
+      hipLaunchKernelGGL((sparse_kernel<D, false, 4, false>), grid, threads, 0, stream, p);
+  } else if constexpr (D != 256) {
+    if (shared)
+      hipLaunchKernelGGL((sparse_kernel<D, true, 8, false>), grid, threads, lists, stream, p);
+    else
+      hipLaunchKernelGGL((sparse_kernel<D, false, 8, false>), grid, threads, 0, stream, p);
   } else {
     return hipErrorInvalidValue;
   }

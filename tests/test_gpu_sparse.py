@@ -313,7 +313,8 @@ def test_values_that_are_no_numbers_reach_who_sees_them(dim, page, sms):
                 for h in range(4):
                     row = got[0][t, h].float().cpu().numpy()
                     if h < 2 and seen(t, 0, j):
-                        assert not np.isfinite(row if kind == "key" else row[5]).any(), (kind, j, t, h)
+                        # (a value of 2^132 counts by its weight)
+                        assert not (np.abs(row if kind == "key" else row[5]) < 1e30).any(), (kind, j, t, h)
                     else:
                         # (a NaN score raises no maximum, and the rows of a tile raise theirs together: last bits may change)
                         was = clean[0][t, h].float().cpu().numpy()
@@ -334,10 +335,12 @@ def test_queries_that_are_no_numbers():
         assert out[rest].isfinite().all()
 
 
-def test_a_cache_past_4_gib():
-    heads, page, dim, pages = 8, 64, 128, 70000  # 4.6 GB of codes
+@pytest.mark.parametrize("dim,news", [(128, [3, 1]), (64, [5, 2]), (256, [2, 9]), (64, [1, 1]), (128, [1, 1]), (256, [1, 1])])
+def test_a_cache_past_4_gib(dim, news):
+    heads, page = 8, 64
+    pages = 2 ** 32 // (heads * page * dim) + 3000
     k_cache, v_cache = dg.fp8_kv_cache_empty(pages, heads, page, dim, device=DEV)
-    p = kv_gen.problem([500, 300], [3, 1], 16, heads, dim, page, 23)
+    p = kv_gen.problem([500, 300], news, 16, heads, dim, page, 23)
     blocks = lists(p, heads, 4, 2)
     used = p["table"][p["table"] >= 0]
     used = np.unique(used[used < len(p["k"][0])])
@@ -347,9 +350,11 @@ def test_a_cache_past_4_gib():
             c[0][to], c[1][to] = cuda(p[x][0][pg]), cuda(p[x][1][pg])
     table = np.vectorize(lambda x: far.get(int(x), -1))(p["table"]).astype(np.int32)
     q = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
-    got = dg.fp8_block_sparse_attention(q, k_cache, v_cache, cuda(table), cuda(p["lens"]), cuda(blocks), cu_seqlens_q=cuda(p["cu"]), max_seqlen_q=3,
-                                        return_lse=True)
-    check(p, got, blocks)
+    for sms in (1, 256, 4000):
+        with num_sms(sms):
+            got = dg.fp8_block_sparse_attention(q, k_cache, v_cache, cuda(table), cuda(p["lens"]), cuda(blocks), cu_seqlens_q=cuda(p["cu"]),
+                                                max_seqlen_q=max(news), return_lse=True)
+        check(p, got, blocks)
     keys = dg.fp8_kv_block_keys_empty(pages, heads, dim, device=DEV)
     to = torch.tensor(sorted(far.values()), dtype=torch.int32, device=DEV)
     dg.fp8_kv_block_keys_update(k_cache, keys, to)
