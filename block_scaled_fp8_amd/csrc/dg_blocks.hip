@@ -40,24 +40,42 @@ __global__ void __launch_bounds__(KEYS_WAVES * 64) block_keys_kernel(const Block
   double s[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = 0.0;
-  for (int t = r; t < p.c.page.d; t += ROWS) {
-    v4u x = *(const v4u*)(codes + t * p.c.token_stride);
-    const uint32_t sf = sfs[t * p.c.sf_token_stride];
-    const double scale = __hiloint2double((int)((sf + 1023 - 127) << 20), 0);
-    if (__builtin_expect(__any(attn::may_be_odd(x, 0)), 0)) {  // a NaN counts as zero
+  constexpr int TOGETHER = 4;  // loads that go out together
+  for (int t0 = r; t0 < p.c.page.d; t0 += ROWS * TOGETHER) {
+    v4u x[TOGETHER];
+    uint32_t sf[TOGETHER];
+    unsigned nan = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const unsigned nan = (((x[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;  // one for each NaN
-        x[i] &= ~(nan * 0xFFu);
+    for (int u = 0; u < TOGETHER; ++u) {
+      const int t = t0 + u * ROWS;
+      x[u] = (v4u){0, 0, 0, 0};
+      sf[u] = 127;
+      if (t < p.c.page.d) {
+        x[u] = *(const v4u*)(codes + t * p.c.token_stride);
+        sf[u] = sfs[t * p.c.sf_token_stride];
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], true);
-      s[4 * i] = __builtin_fma((double)lo.x, scale, s[4 * i]);
-      s[4 * i + 1] = __builtin_fma((double)lo.y, scale, s[4 * i + 1]);
-      s[4 * i + 2] = __builtin_fma((double)hi.x, scale, s[4 * i + 2]);
-      s[4 * i + 3] = __builtin_fma((double)hi.y, scale, s[4 * i + 3]);
+    for (int u = 0; u < TOGETHER; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nan |= (x[u][i] & 0x7F7F7F7Fu) + 0x01010101u;
+    if (__builtin_expect(__any((nan & 0x80808080u) != 0), 0)) {  // a NaN counts as zero
+#pragma unroll
+      for (int u = 0; u < TOGETHER; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[u][i] &= ~(((((x[u][i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
+    }
+#pragma unroll
+    for (int u = 0; u < TOGETHER; ++u) {
+      const double scale = __hiloint2double((int)((sf[u] + 1023 - 127) << 20), 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[u][i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[u][i], true);
+        s[4 * i] = __builtin_fma((double)lo.x, scale, s[4 * i]);
+        s[4 * i + 1] = __builtin_fma((double)lo.y, scale, s[4 * i + 1]);
+        s[4 * i + 2] = __builtin_fma((double)hi.x, scale, s[4 * i + 2]);
+        s[4 * i + 3] = __builtin_fma((double)hi.y, scale, s[4 * i + 3]);
+      }
     }
   }
 #pragma unroll

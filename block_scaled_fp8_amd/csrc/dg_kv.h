@@ -66,6 +66,7 @@ struct RopeParams {
   int32_t rot, num_tokens, q_heads, kv_heads;
   float eps;
   int32_t weights_bf16;
+  int32_t stream_out;               // 1: results are written past the caches
   KvCache c;
   const int64_t* slots;
   FastDiv pieces;                   // waves that share a token (backward: of the section)

@@ -44,18 +44,30 @@ __device__ __forceinline__ void load16(const void* base, int64_t at, const Lane&
 __device__ __forceinline__ unsigned pack2(float x, float y) {
   return __builtin_bit_cast(unsigned, (v2bf){(__bf16)x, (__bf16)y});
 }
-template <bool BF16>
+// STREAM: past the caches.  Results of more than they hold are written so: they would only drive out what is still to be read (8192 tokens of
+// 32 + 8 heads of 128 into the cache 40.6 -> 36.2 us, forward and backward 82.3 -> 79.1); small ones stay for the reader after.
+template <bool BF16, bool STREAM>
 __device__ __forceinline__ void store16(void* base, int64_t at, const Lane& l, const float (&x)[16]) {
+  constexpr int N = BF16 ? 1 : 2;  // 16-byte pieces of a chunk
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int64_t to = at + (c ? l.c1 : l.c0);
     const float* y = x + 8 * c;
+    v4u out[N];
     if constexpr (BF16) {
-      *(v4u*)((uint16_t*)base + to) = (v4u){pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
+      out[0] = (v4u){pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; i += 4)
-        *(v4u*)((float*)base + to + i) = (v4u){__float_as_uint(y[i]), __float_as_uint(y[i + 1]), __float_as_uint(y[i + 2]), __float_as_uint(y[i + 3])};
+      for (int i = 0; i < 2; ++i)
+        out[i] = (v4u){__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3])};
+    }
+    v4u* dst = BF16 ? (v4u*)((uint16_t*)base + to) : (v4u*)((float*)base + to);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(out[i], dst + i);
+      else
+        dst[i] = out[i];
     }
   }
 }
@@ -107,7 +119,7 @@ __device__ __forceinline__ void load_weights(const void* w, bool bf16, const Lan
 }
 
 // ---------------------------------------------------------------- forward
-template <int D, bool BF16, bool INTER, bool WRITE>
+template <int D, bool BF16, bool INTER, bool WRITE, bool STREAM>
 __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
   constexpr int L = D / 16, HEADS = 64 / L;
   const int lane = threadIdx.x & 63, l = lane % L;
@@ -155,11 +167,11 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
     return;
   }
   const Rows& to = is_q ? p.q_out : p.k_out;
-  store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+  store16<BF16, STREAM>(to.p, token * to.token_stride + head * to.head_stride, my, x);
 }
 
 // ---------------------------------------------------------------- backward
-template <int D, bool BF16, bool INTER>
+template <int D, bool BF16, bool INTER, bool STREAM>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
   constexpr int L = D / 16, HEADS = 64 / L;
   __shared__ float sums[2][WAVES][D];
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = r * (t[i] - x[i] * mean);
       }
-      store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+      store16<BF16, STREAM>(to.p, token * to.token_stride + head * to.head_stride, my, x);
     }
     // over the wave's rows: lanes l, l + L, ...
 #pragma unroll
@@ -239,19 +251,26 @@ __global__ void __launch_bounds__(1024) weights_kernel(const RopeParams p) {
   (i < D ? p.dq_weight : p.dk_weight)[i % D] = s;
 }
 
-template <int D, bool BF16, bool INTER>
-hipError_t forward(const RopeParams& p, bool write, hipStream_t stream) {
+template <int D, bool BF16, bool INTER, bool STREAM>
+hipError_t forward_as(const RopeParams& p, bool write, hipStream_t stream) {
   const unsigned grid = (unsigned)(((int64_t)p.num_tokens * p.pieces.d + WAVES - 1) / WAVES);
   if (write)
-    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, true>), dim3(grid), dim3(THREADS), 0, stream, p);
+    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, true, STREAM>), dim3(grid), dim3(THREADS), 0, stream, p);
   else
-    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, false>), dim3(grid), dim3(THREADS), 0, stream, p);
+    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, false, STREAM>), dim3(grid), dim3(THREADS), 0, stream, p);
   return hipGetLastError();
+}
+template <int D, bool BF16, bool INTER>
+hipError_t forward(const RopeParams& p, bool write, hipStream_t stream) {
+  return p.stream_out ? forward_as<D, BF16, INTER, true>(p, write, stream) : forward_as<D, BF16, INTER, false>(p, write, stream);
 }
 
 template <int D, bool BF16, bool INTER>
 hipError_t backward(const RopeParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((backward_kernel<D, BF16, INTER>), dim3(p.workgroups), dim3(THREADS), 0, stream, p);
+  if (p.stream_out)
+    hipLaunchKernelGGL((backward_kernel<D, BF16, INTER, true>), dim3(p.workgroups), dim3(THREADS), 0, stream, p);
+  else
+    hipLaunchKernelGGL((backward_kernel<D, BF16, INTER, false>), dim3(p.workgroups), dim3(THREADS), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.workgroups == 1) return e;
   hipLaunchKernelGGL((weights_kernel<D>), dim3(2 * D / 32), dim3(1024), 0, stream, p);
