@@ -124,12 +124,12 @@ __device__ __forceinline__ uint32_t sortable(float x) {
 }
 
 // Largest over W = 1, 2, 4, 8 or 16 neighbouring lanes.
-__device__ __forceinline__ float columns_max(float x, int w) {
-  auto other = [](float v, auto ctrl) { return __uint_as_float((unsigned)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true)); };
-  if (w > 1) x = fmaxf(x, other(x, std::integral_constant<int, 0xB1>()));
-  if (w > 2) x = fmaxf(x, other(x, std::integral_constant<int, 0x4E>()));
-  if (w > 4) x = fmaxf(x, other(x, std::integral_constant<int, 0x141>()));
-  if (w > 8) x = fmaxf(x, other(x, std::integral_constant<int, 0x140>()));
+__device__ __forceinline__ uint32_t columns_max(uint32_t x, int w) {
+  auto other = [](uint32_t v, auto ctrl) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xf, 0xf, true); };
+  if (w > 1) x = max(x, other(x, std::integral_constant<int, 0xB1>()));
+  if (w > 2) x = max(x, other(x, std::integral_constant<int, 0x4E>()));
+  if (w > 4) x = max(x, other(x, std::integral_constant<int, 0x141>()));
+  if (w > 8) x = max(x, other(x, std::integral_constant<int, 0x140>()));
   return x;
 }
 
@@ -212,7 +212,6 @@ __device__ __forceinline__ void score(const SelectParams& p, const Tokens& t, in
     load_pages(first);
     for (int c = wave; c < tiles; c += p.waves) {
       const int token = c * per_tile + col / width, h = head0 + col % width;
-      const bool live = token < t.tokens && h < p.group.d;
       const uint16_t* src = p.s.q + (t.first_row + min(token, t.tokens - 1)) * p.s.q_token_stride +
                             (t.kv_head * p.group.d + min(h, p.group.d - 1)) * p.s.q_head_stride + 16 * g;
       v4u x[Y][2];
@@ -226,7 +225,7 @@ __device__ __forceinline__ void score(const SelectParams& p, const Tokens& t, in
       m = __float_as_uint(attn::groups_max(__uint_as_float(m)));
       const uint32_t e = m ? max((int)(m >> 23) - 6 + ((m & 0x7FFFFFu) > 0x7E0000u ? 1 : 0), 1) : 127u;
       const float inv = __uint_as_float((254u - e) << 23);
-      if (g == 0) query_scales[c][col] = live ? __uint_as_float(e << 23) : attn::NEG_INF;
+      if (g == 0) query_scales[c][col] = __uint_as_float(e << 23);
 #pragma unroll
       for (int y = 0; y < Y; ++y) codes[c][y][lane] = to_codes(x[y][0], x[y][1], inv);
     }
@@ -240,6 +239,8 @@ __device__ __forceinline__ void score(const SelectParams& p, const Tokens& t, in
 #pragma unroll
       for (int y = 0; y < Y; ++y) q[c][y] = codes[c][y][lane];
     }
+    // (columns of a token without a head)
+    const bool part_empty = head0 + width > p.group.d, dead = head0 + col % width >= p.group.d;
     for (int b0 = first; b0 < hi; b0 += step * AHEAD) {
       v4u k[AHEAD][Y];
       float scale[AHEAD];
@@ -270,8 +271,9 @@ __device__ __forceinline__ void score(const SelectParams& p, const Tokens& t, in
           v4u w;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x = sq[c] == attn::NEG_INF ? sq[c] : (float)s[i] * sk[i] * sq[c];
-            w[i] = sortable(columns_max(x, width));
+            w[i] = sortable((float)s[i] * sk[i] * sq[c]);
+            if (part_empty) w[i] = dead ? 0u : w[i];
+            w[i] = columns_max(w[i], width);
           }
           const int token = c * per_tile + col / width;
           if (col % width == 0 && token < t.tokens) {
