@@ -19,6 +19,8 @@
 // their own without asking each other, and put them into LDS as halves of 16 keys, two of which make a wave's tile.
 #include <type_traits>
 
+#include <cfloat>
+
 #include "dg_attn_device.h"
 
 namespace dg {
@@ -82,19 +84,15 @@ __device__ __forceinline__ Row row_of(const SparseParams& p, const Tile& t, int 
   return {token, t.kv_head * p.group.d + t.head0 + r - token * p.group.d};
 }
 
-// The first of `top` ascending numbers (negative ones, at the end, count as larger than all) that is not below v: whether it is v.
+// Whether v >= 0 is one of `top` ascending numbers (negative ones, at the end, count as larger than all).  All lanes take the same steps.
 __device__ __forceinline__ bool has(const int32_t* list, int top, int v) {
-  int at = 0, n = top;
-  while (n > 0) {
-    const int half = n >> 1, x = list[at + half];
-    if (x >= 0 && x < v) {
-      at += half + 1;
-      n -= half + 1;
-    } else {
-      n = half;
-    }
+  int at = 0;
+  for (int n = top; n > 1;) {
+    const int half = n >> 1;
+    at += (uint32_t)list[at + half - 1] < (uint32_t)v ? half : 0;
+    n -= half;
   }
-  return at < top && list[at] == v;
+  return list[at] == v;
 }
 
 // Up to 16 keys of one block.
@@ -216,6 +214,12 @@ __device__ __forceinline__ int v_swizzle(int row) {
   return D == 64 ? row >> 2 & 3 : D == 128 ? row >> 1 & 7 : row & 15;
 }
 
+// K tiles do too: a read takes a chunk of 16 rows in each lane group, and LDS serves 8 lanes at a time.
+template <int D>
+__device__ __forceinline__ int k_swizzle(int row) {
+  return D == 64 ? row >> 1 & 3 : row & 7;
+}
+
 // Codes that are NaN become zeros.
 __device__ __forceinline__ v4u clear_nan(v4u x) {
 #pragma unroll
@@ -249,6 +253,21 @@ __device__ __forceinline__ void read_transposed(const uint32_t (&at)[4], v2i (&x
                : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
                : "memory");
 }
+// A lane's 16 bytes of a row of each half, OFFSET bytes apart, at each of two places.
+template <int OFFSET>
+__device__ __forceinline__ void read_rows(uint32_t at, v4u& a, v4u& b) {
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(a), "=&v"(b)
+               : "v"(at), "n"(OFFSET)
+               : "memory");
+}
+template <int OFFSET>
+__device__ __forceinline__ void read_rows(uint32_t at, uint32_t at2, v4u& a, v4u& b, v4u& a2, v4u& b2) {
+  asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(a), "=&v"(b), "=&v"(a2), "=&v"(b2)
+               : "v"(at), "v"(at2), "n"(OFFSET)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(const DG_LDS uint8_t*)p; }
 // Wait until at most N vector-memory operations of this wave are on their way.
 template <int N>
@@ -266,12 +285,12 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse
   constexpr int JD = 64;                                        // values of D joined at once
   constexpr int JOIN = WAVES * 16 * (JD + 4) * 4;
   __shared__ __attribute__((aligned(256))) uint8_t lds[WAVES * 2 * TILE > JOIN ? WAVES * 2 * TILE : JOIN];
-  __shared__ __attribute__((aligned(16))) uint32_t v_scales[WAVES][2][2][64];  // scale codes of a half's values, 16 of them, four times
+  __shared__ __attribute__((aligned(16))) uint32_t v_scales[WAVES][2][64];  // scale codes of a half's values, 16 of them, four times
   __shared__ __attribute__((aligned(16))) uint32_t halves[WAVES][MOST_HALVES * HALF_WORDS<FAR>];
   __shared__ float mz[WAVES][2][16];
   extern __shared__ int32_t tile_lists[];  // [tile_tokens][top] (SHARED)
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), g = lane >> 4, col = lane & 15;
-  uint8_t* vt = lds + wave * 2 * TILE;
+  uint8_t *kt = lds + wave * 2 * TILE, *v = kt + TILE;
   Tile t;
   if (!get_tile(p, t, blockIdx.x, p.parts)) return;
   const Row row = row_of(p, t, col);
@@ -302,33 +321,38 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse
   w.share = t.part * WAVES + wave;
   w.all = t.tokens * p.top * p.segments.d;
 
+  // whether every row sees all 16 keys of a half or none
+  auto is_sharp = [&](const Half<FAR> (&h)[2]) { return h[0].keys == 16 && h[1].keys == 16 && h[0].key0 + 15 <= t.place0 && h[1].key0 + 15 <= t.place0; };
+
   // whether every row sees all 32 keys
   auto is_whole = [&](const Half<FAR> (&h)[2]) {
-    return h[0].tokens == every && h[1].tokens == every && h[0].keys == 16 && h[1].keys == 16 && h[0].key0 + 15 <= t.place0 && h[1].key0 + 15 <= t.place0;
+    return h[0].tokens == every && h[1].tokens == every && is_sharp(h);
   };
 
-  // Rows past a half's keys repeat its last one.  Codes go through buffer descriptors of the pages, whose addresses are scalar; lane
+  // Codes go through buffer descriptors of the pages, whose addresses are scalar; lane
   // l % 32 has the scale code of key l % 32.
-  v4u kr[2][D / 64];
   uint8_t ks[2];  // (bytes until they are used: wider, they would be widened, and so waited for, where they are loaded)
   // Everything goes through buffer descriptors of the cache, with the half's offset in a scalar register.  (FAR, for caches of 4 GiB and more:
-  // descriptors of the half.)  Rows past a half's keys repeat its last one; `some` false: all repeat the first one.  (The loads are issued all the
-  // same: past a branch the compiler would wait for all that is on its way.)
+  // descriptors of the half.)  Rows past a half's keys give bytes of its last one; `some` false: all those of its first one.  (The loads are issued
+  // all the same, so that as many are on their way in each turn.)
   const int ts = (int)p.c.token_stride, sts = (int)p.c.sf_token_stride;
-  const int k_row = col * ts, k_chunk = 16 * g, sf_row = col * sts, v_row = lane / CH;
+  const int sf_row = col * sts, v_row = lane / CH;
   auto from = [&](const uint8_t* base, typename Half<FAR>::Offset at) { return rsrc(FAR ? base + at : base, -1); };
   auto also = [&](typename Half<FAR>::Offset at) { return FAR ? 0 : (int)at; };
-  auto fetch_k = [&](const Half<FAR> (&h)[2], bool some) {
+  auto copy_k = [&](const Half<FAR> (&h)[2], bool some) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int last = some ? h[x].keys - 1 : 0, at = min(k_row, last * ts) + k_chunk;
+      const int last = some ? h[x].keys - 1 : 0;
       const __amdgpu_buffer_rsrc_t codes = from(p.c.k, h[x].code);
 #pragma unroll
-      for (int y = 0; y < D / 64; ++y) kr[x][y] = __builtin_amdgcn_raw_buffer_load_b128(codes, at + 64 * y, also(h[x].code), 0);
+      for (int n = x * NP / 2; n < (x + 1) * NP / 2; ++n) {
+        const int r = n * PASS + v_row;
+        copy_to_lds(codes, min((r & 15) * ts + 16 * (lane % CH ^ k_swizzle<D>(r)), last * ts + D - 16), also(h[x].code), kt + n * 1024);
+      }
       ks[x] = __builtin_amdgcn_raw_buffer_load_b8(from(p.c.k_sf, h[x].sf), min(sf_row, last * sts), also(h[x].sf), 0);
     }
   };
-  auto copy_v = [&](const Half<FAR> (&h)[2], int slot, bool some) {
+  auto copy_v = [&](const Half<FAR> (&h)[2], bool some) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int last = some ? h[x].keys - 1 : 0;
@@ -336,37 +360,49 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse
 #pragma unroll
       for (int n = x * NP / 2; n < (x + 1) * NP / 2; ++n) {
         const int r = n * PASS + v_row;
-        copy_to_lds(codes, min((r & 15) * ts, last * ts) + 16 * (lane % CH ^ v_swizzle<D>(r)), also(h[x].code), vt + slot * TILE + n * 1024);
+        copy_to_lds(codes, min((r & 15) * ts + 16 * (lane % CH ^ v_swizzle<D>(r)), last * ts + D - 16), also(h[x].code), v + n * 1024);
       }
-      copy_byte_to_lds(from(p.c.v_sf, h[x].sf), min(sf_row, last * sts), also(h[x].sf), v_scales[wave][slot][x]);
+      copy_byte_to_lds(from(p.c.v_sf, h[x].sf), min(sf_row, last * sts), also(h[x].sf), v_scales[wave][x]);
     }
   };
 
   v4f o[D / 16];
-  float m, z;
+  float m, z, shift;
   // A hidden value's weight is zero, which is not enough where it is NaN (or its scale so large that weights overflow).  Nobody looks for such
   // values at first: they leave a NaN in some output.  A wave that ends with an output that is no number goes over its keys again with care: NaN among
   // the values of tiles that some row does not see in whole go to the outputs of the rows that see them, and become zeros; no weight is infinite.
 #pragma unroll 1
   for (int careful = 0;; ++careful) {
-    m = NEG_INF, z = 0.f;
+    m = NEG_INF, z = 0.f, shift = FLT_MAX;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) o[d] = (v4f){0.f, 0.f, 0.f, 0.f};
     w.from = w.before = w.at = w.count = 0;
-    // Each turn issues V of a tile, works on the tile before, whose V and K are there or on their way, and issues K of the tile.
+    // A turn takes K of a tile from LDS and issues K of the next one, takes V and issues V of the next one: what it waits for was issued half a
+    // turn and more before, and the other one is on its way meanwhile.
     Half<FAR> now[2], next[2];
-    int slot = 1;  // of `next`
     bool more = next_tile<SHARED, FAR>(p, t, lists, halves[wave], w, now);
     if (more) {
-      copy_v(now, 0, true);
+      copy_k(now, true);
       __builtin_amdgcn_sched_barrier(0);
-      fetch_k(now, true);
+      copy_v(now, true);
       next[0] = now[0], next[1] = now[1];
     }
 #pragma unroll 1
     while (more) {
-      more = next_tile<SHARED, FAR>(p, t, lists, halves[wave], w, next);
-      copy_v(next, slot, more);  // (without more, `next` is still the last tile)
+      more = next_tile<SHARED, FAR>(p, t, lists, halves[wave], w, next);  // (without more, `next` is still the last tile)
+      __builtin_amdgcn_sched_barrier(0);
+      wait_vm<NP + 2>();  // only V may be on its way
+      v4u kr[2][D / 64];
+      uint32_t k_at = lds_address(kt) + col * D + 16 * (g ^ k_swizzle<D>(col));
+      if constexpr (D == 64) {
+        read_rows<16 * D>(k_at, kr[0][0], kr[1][0]);
+      } else {
+#pragma unroll
+        for (int y = 0; y < D / 64; y += 2) read_rows<16 * D>(k_at ^ 64 * y, k_at ^ 64 * (y + 1), kr[0][y], kr[1][y], kr[0][y + 1], kr[1][y + 1]);
+      }
+      const float k_scale[2] = {__uint_as_float((uint32_t)ks[0] << 23), __uint_as_float((uint32_t)ks[1] << 23)};
+      __builtin_amdgcn_sched_barrier(0);
+      copy_k(next, more);
       __builtin_amdgcn_sched_barrier(0);
       v4f s[2];
       s[0] = s[1] = (v4f){0.f, 0.f, 0.f, 0.f};
@@ -374,28 +410,30 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse
       for (int y = 0; y < D / 64; ++y)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float scale = __uint_as_float((uint32_t)ks[x] << 23);
-          const v8bf lo = __builtin_bit_cast(v8bf, widen8(kr[x][y].x, kr[x][y].y, scale));
-          const v8bf hi = __builtin_bit_cast(v8bf, widen8(kr[x][y].z, kr[x][y].w, scale));
+          const v8bf lo = __builtin_bit_cast(v8bf, widen8(kr[x][y].x, kr[x][y].y, k_scale[x]));
+          const v8bf hi = __builtin_bit_cast(v8bf, widen8(kr[x][y].z, kr[x][y].w, k_scale[x]));
           s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, q[2 * y], s[x], 0, 0, 0);
           s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, q[2 * y + 1], s[x], 0, 0, 0);
         }
       __builtin_amdgcn_sched_barrier(0);
-      fetch_k(next, more);
-      __builtin_amdgcn_sched_barrier(0);
-      uint8_t* v = vt + (slot ^ 1) * TILE;
-      // (V of this tile is there, as its K is, which came later; said once more: only V and K of the next one may be on their way)
-      wait_vm<NP + 2 + D / 32 + 2>();
+      float sub[2] = {shift, shift};
       if (!is_whole(now)) {
         // keys of each half that the lane's query sees: the first ones
         int count[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          count[x] = now[x].tokens >> row.token & 1 ? min(now[x].keys, place - now[x].key0 + 1) : 0;
+        for (int x = 0; x < 2; ++x) count[x] = now[x].tokens >> row.token & 1 ? min(now[x].keys, place - now[x].key0 + 1) : 0;
+        // A query that sees all of a half or nothing: -inf for all its keys at once.
+        if (is_sharp(now) && !careful) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[x][e] = e < count[x] - 4 * g ? s[x][e] : NEG_INF;
+          for (int x = 0; x < 2; ++x) sub[x] = count[x] > 0 ? shift : NEG_INF;
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[x][e] = e < count[x] - 4 * g ? s[x][e] : NEG_INF;
         }
         if (__builtin_expect(careful, 0)) {
+          wait_vm<NP + 2>();
           int l = lane;
           asm volatile("" : "+v"(l));  // (so that no register holds what is computed from it through the loop)
 #pragma unroll 1
@@ -415,31 +453,48 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse
           }
         }
       }
-      float top = s[0][0];
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[x][e]);
-      top = groups_max(top) * p.scale_log2;  // (the scale is positive)
-      if (__any(top > m + SLACK)) {
-        const float raised = fmaxf(m, top);
-        const float f = raised == NEG_INF ? 1.f : exp2_hw(m - raised);
-        m = raised;
-        z *= f;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) o[d] *= f;
-      }
-      const float sub = m == NEG_INF ? 0.f : -m;  // nothing seen yet: every weight is 2^-inf = 0
-      // (the wave reads what its other lanes wrote: its LDS operations complete in order, so only the compiler has to keep theirs)
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      v4u x4, sf[2];
-      read_copied(lds_address(&v_scales[wave][slot ^ 1][0][4 * g]), sf[0], sf[1]);
+      // Exponents against the row's largest score so far; only one that passes it by more than SLACK (compared as integers, which hold for what
+      // is positive) raises it.  A row without a score has the largest number for a shift, so that its first one does.
+      v4f w2[2];
+      int most = 0;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[x][e] = exp2_hw(__builtin_fmaf(s[x][e], p.scale_log2, sub));
+          w2[x][e] = __builtin_fmaf(s[x][e], p.scale_log2, sub[x]);
+          most = max(most, (int)__float_as_uint(w2[x][e]));
+        }
+      if (__any(most > (int)__float_as_uint(SLACK))) {
+        float top = NEG_INF;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, sub[x] == NEG_INF ? NEG_INF : s[x][e]);
+        const float raised = fmaxf(m, groups_max(top) * p.scale_log2);  // (the scale is positive)
+        const float f = raised == NEG_INF ? 1.f : exp2_hw(m - raised);
+        m = raised;
+        shift = m == NEG_INF ? FLT_MAX : -m;
+        if (__any(z != 0.f)) {  // (else nothing has been summed)
+          z *= f;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) o[d] *= f;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w2[x][e] = __builtin_fmaf(s[x][e], p.scale_log2, sub[x] == NEG_INF ? NEG_INF : shift);
+      }
+      // (the wave reads what its other lanes wrote: its LDS operations complete in order, so only the compiler has to keep theirs)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      v4u x4, sf[2];
+      wait_vm<NP + 2>();  // only K of the next tile may be on its way
+      read_copied(lds_address(&v_scales[wave][0][4 * g]), sf[0], sf[1]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[x][e] = exp2_hw(w2[x][e]);
           z += s[x][e];
         }
       // The value's scale goes to its weight: exact, so the weight is rounded to BF16 as it would be without.
@@ -479,9 +534,11 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_sched_barrier(0);
+      copy_v(next, more);
+      __builtin_amdgcn_sched_barrier(0);
       now[0] = next[0], now[1] = next[1];
-      slot ^= 1;
     }
+    wait_vm<0>();  // (or a copy would still go to LDS that others write)
     if (careful) break;
     float sum = 0.f;  // (a NaN or infinity times zero is NaN)
 #pragma unroll
