@@ -14,7 +14,7 @@
 // Lane group g (lane / 16) and column lane % 16 have the roles that they have in attention of few rows over all keys: S^T in
 // blocks of 16 keys, lane group g with keys 4 g + i of its column's query.
 //
-// The lists' blocks, in segments of 64 keys, go 32 to a wave at a time, one a lane: a lane looks its block up in the other tokens' lists (they
+// The lists' blocks, in segments of 64 keys, go 64 to a wave at a time, one a lane: a lane looks its block up in the other tokens' lists (they
 // ascend), and drops it where an earlier one has it.  The remaining ones are dealt in turn to the waves of the tile's workgroups, which find
 // their own without asking each other, and put them into LDS as halves of 16 keys, two of which make a wave's tile.
 #include <type_traits>
@@ -107,7 +107,7 @@ struct Half {
 // with the copy that makes an odd number even.  (With 64 segments at once, LDS would hold one workgroup less.)
 template <bool FAR>
 constexpr int HALF_WORDS = FAR ? 8 : 4;
-constexpr int AT_ONCE = 32, MOST_HALVES = 4 * AT_ONCE / 4 + 2;
+constexpr int AT_ONCE = 64, MOST_HALVES = 4 * AT_ONCE / 4 + 2;
 
 // A wave's halves.
 struct Walk {
@@ -124,7 +124,7 @@ __device__ __forceinline__ void find_halves(const SparseParams& p, const Tile& t
   const uint64_t below = (1ull << lane) - 1;
   unsigned tokens = 0;
   int block = 0, offset = 0;
-  if (lane < AT_ONCE && u < w.all) {
+  if (u < w.all) {
     const int i = div(u, p.segments);
     offset = (u - i * p.segments.d) * SEGMENT;
     block = lists[i];
@@ -134,8 +134,10 @@ __device__ __forceinline__ void find_halves(const SparseParams& p, const Tile& t
       if (SHARED) {
         const int mine = div(i, p.list);
         tokens = 1u << mine;
-        for (int x = 0; x < t.tokens; ++x)
-          if (x != mine && has(lists + x * p.top, p.top, block)) tokens |= 1u << x;
+        for (int i = 1, x = mine; i < t.tokens; ++i) {
+          x = x + 1 == t.tokens ? 0 : x + 1;
+          if (has(lists + x * p.top, p.top, block)) tokens |= 1u << x;
+        }
         if (tokens & ((1u << mine) - 1)) tokens = 0;  // (an earlier token's entry stands for it)
       }
     }
