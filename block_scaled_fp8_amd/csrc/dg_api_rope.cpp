@@ -68,8 +68,6 @@ dg::RopeParams kernel_params(const dg_norm_rope* a) {
   p.kv_heads = a->num_kv_heads;
   p.eps = a->eps;
   p.weights_bf16 = a->weight_dtype == DG_IN_BF16;
-  // (the eight second-level caches hold 32 MiB)
-  p.stream_out = int64_t(a->num_tokens) * (a->num_q_heads + a->num_kv_heads) * a->head_dim * element_size(a) > (int64_t(32) << 20);
   return p;
 }
 

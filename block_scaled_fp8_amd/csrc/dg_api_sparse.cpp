@@ -99,11 +99,11 @@ int check_grid(const Batch& a, int64_t workgroups, int threads) {
   return DG_OK;
 }
 
-// Choosing: tokens of a workgroup, its waves, and workgroups that share the blocks.
+// Choosing: tokens of a workgroup, and workgroups that share the blocks.
 struct SelectPlan {
   int64_t tile_tokens, items, row_words;
   bool one_tile;
-  int waves, parts;
+  int parts;
 };
 SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, int32_t table_cols, int32_t top, int32_t first, int32_t last, int num_sms) {
   const int32_t group = a.num_q_heads / num_kv_heads;
@@ -119,12 +119,10 @@ SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
     pl.tile_tokens /= 2;
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
   pl.one_tile = pl.tile_tokens <= per_tile;
-  pl.waves = pl.one_tile && head_dim != 256 && scored > 512 ? 16 : 8;
   pl.parts = 1;
   // Few tiles of many blocks: a workgroup for each 256 blocks.
   const int64_t tiles = pl.items * num_kv_heads;
   if (pl.one_tile && scored > 512 && 4 * tiles <= num_sms) {
-    pl.waves = 8;
     const int64_t by_blocks = ceil_div(scored, 256), by_units = num_sms / tiles;
     pl.parts = int(by_blocks < by_units ? by_blocks : by_units);
   }
@@ -173,7 +171,7 @@ SparsePlan sparse_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
   const int64_t with_rows = a.total_q / pl.tile_tokens + a.batch;  // of the items, at most
   const int64_t work = (with_rows < pl.items ? with_rows : pl.items) * num_kv_heads * pl.head_tiles;
-  const int64_t segments = pl.tile_tokens * top * ceil_div(page_size, 64), slots = int64_t(num_sms) * (head_dim == 256 ? 1 : 3);
+  const int64_t segments = pl.tile_tokens * top * ceil_div(page_size, 64), slots = num_sms;
   pl.parts = 1;
   pl.waves = 4;
   // Short lists of few tiles: eight waves instead of parts, whose second kernel costs the host more than it saves the device.  (At
@@ -254,7 +252,7 @@ int dg_fp8_kv_select_blocks(const dg_fp8_block_keys* keys, int32_t page_size, in
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
   const SelectPlan pl = select_plan(a, keys->num_heads, keys->head_dim, table_cols, top, first, last, num_sms);
-  if (int s = check_grid(a, pl.items * keys->num_heads, pl.waves * 64)) return s;
+  if (int s = check_grid(a, pl.items * keys->num_heads, dg::SELECT_WAVES * 64)) return s;
   const int64_t need = select_workspace(pl, keys->num_heads);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);
@@ -273,7 +271,6 @@ int dg_fp8_kv_select_blocks(const dg_fp8_block_keys* keys, int32_t page_size, in
   p.tile_tokens = int32_t(pl.tile_tokens);
   p.items = int32_t(pl.items);
   p.row_words = int32_t(pl.row_words);
-  p.waves = pl.waves;
   p.parts = pl.parts;
   p.scores = static_cast<uint32_t*>(workspace);
   p.out = blocks;

@@ -201,7 +201,7 @@ __device__ __forceinline__ void score(const SelectParams& p, const Tokens& t, in
   const int width = p.group.d > 8 ? 16 : p.group.d > 4 ? 8 : p.group.d > 2 ? 4 : p.group.d;  // columns of a token
   const int per_tile = 16 / width, tiles = (t.tokens + per_tile - 1) / per_tile;
   const int32_t* table = p.s.table + t.seq * p.s.table_stride;
-  const int first = lo + 16 * (part * p.waves + wave), step = 16 * p.waves * parts;
+  const int first = lo + 16 * (part * SELECT_WAVES + wave), step = 16 * SELECT_WAVES * parts;
   int pages[AHEAD];
   auto load_pages = [&](int b0) {
 #pragma unroll
@@ -210,7 +210,7 @@ __device__ __forceinline__ void score(const SelectParams& p, const Tokens& t, in
   for (int head0 = 0; head0 < p.group.d; head0 += 16) {
     if (head0) __syncthreads();
     load_pages(first);
-    for (int c = wave; c < tiles; c += p.waves) {
+    for (int c = wave; c < tiles; c += SELECT_WAVES) {
       const int token = c * per_tile + col / width, h = head0 + col % width;
       const uint16_t* src = p.s.q + (t.first_row + min(token, t.tokens - 1)) * p.s.q_token_stride +
                             (t.kv_head * p.group.d + min(h, p.group.d - 1)) * p.s.q_head_stride + 16 * g;
@@ -442,10 +442,8 @@ __device__ __forceinline__ void choose(const SelectParams& p, int place, const u
     });
 }
 
-constexpr int select_threads(int head_dim, int tiles) { return tiles == 1 && head_dim != 256 ? 1024 : 512; }
-
 template <int D, int TILES>
-__global__ void __launch_bounds__(select_threads(D, TILES), D == 256 ? 2 : 4) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(SELECT_WAVES * 64, D == 256 ? 2 : 4) select_kernel(const SelectParams p) {
   extern __shared__ __attribute__((aligned(16))) uint32_t scores[];  // [tile_tokens][row_words], then [waves][CANDIDATES]
   __shared__ __attribute__((aligned(16))) v4u codes[TILES][D / 64][64];  // the queries as operands
   __shared__ float query_scales[TILES][16];
@@ -456,14 +454,14 @@ __global__ void __launch_bounds__(select_threads(D, TILES), D == 256 ? 2 : 4) se
     score<D, TILES>(p, t, p.first, p.first, blocks - p.last, 0, 1, scores, codes, query_scales);
     __syncthreads();
   }
-  for (int token = wave; token < t.tokens; token += p.waves)
+  for (int token = wave; token < t.tokens; token += SELECT_WAVES)
     choose(p, t.place0 + token, scores + token * p.row_words, scores + p.tile_tokens * p.row_words + wave * CANDIDATES,
            p.out + ((int64_t)(t.first_row + token) * p.num_heads + t.kv_head) * p.top);
 }
 
 // The two steps as kernels of their own, with the scores in memory.
 template <int D>
-__global__ void __launch_bounds__(512, D == 256 ? 2 : 4) score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(SELECT_WAVES * 64, D == 256 ? 2 : 4) score_kernel(const SelectParams p) {
   __shared__ __attribute__((aligned(16))) v4u codes[1][D / 64][64];
   __shared__ float query_scales[1][16];
   Tokens t;
@@ -495,7 +493,7 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectPara
 template <int D>
 hipError_t select(const SelectParams& p, bool one_tile, hipStream_t stream) {
   const unsigned tiles = (unsigned)((int64_t)p.items * p.num_heads);
-  const dim3 threads(p.waves * 64);
+  const dim3 threads(SELECT_WAVES * 64);
   if (p.parts > 1) {
     hipLaunchKernelGGL((score_kernel<D>), dim3(tiles * p.parts), threads, 0, stream, p);
     const hipError_t e = hipGetLastError();
@@ -503,7 +501,7 @@ hipError_t select(const SelectParams& p, bool one_tile, hipStream_t stream) {
     hipLaunchKernelGGL((choose_kernel), dim3(tiles * p.tile_tokens), dim3(CHOOSE_THREADS), (size_t)(p.row_words + CANDIDATES) * 4, stream, p);
     return hipGetLastError();
   }
-  const size_t lds = ((size_t)p.tile_tokens * p.row_words + (size_t)p.waves * CANDIDATES) * 4;
+  const size_t lds = ((size_t)p.tile_tokens * p.row_words + (size_t)SELECT_WAVES * CANDIDATES) * 4;
   if (one_tile)
     hipLaunchKernelGGL((select_kernel<D, 1>), dim3(tiles), threads, lds, stream, p);
   else

@@ -66,7 +66,6 @@ struct RopeParams {
   int32_t rot, num_tokens, q_heads, kv_heads;
   float eps;
   int32_t weights_bf16;
-  int32_t stream_out;               // 1: results are written past the caches
   KvCache c;
   const int64_t* slots;
   FastDiv pieces;                   // waves that share a token (backward: of the section)
@@ -146,11 +145,11 @@ struct SelectParams {
   FastDiv q_tiles;               // tiles of tokens per sequence
   int32_t tile_tokens, items;    // tokens of a tile; batch * q_tiles
   int32_t row_words;             // words of a token's scores
-  int32_t waves;                 // of a workgroup
   int32_t parts;                 // workgroups that share a tile's blocks, with the scores in memory; 1: one kernel, scores in LDS
   uint32_t* scores;              // [items, heads, tile_tokens, row_words] (parts > 1)
   int32_t* out;                  // [total_q, heads, top]
 };
+constexpr int SELECT_WAVES = 8;  // of a workgroup
 // tiles of 16 columns (a token's heads, rounded up to a power of two) of a workgroup: their codes stay in registers
 constexpr int select_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
 // one_tile: a workgroup's tokens fit one tile of columns

@@ -44,9 +44,15 @@ __device__ __forceinline__ void load16(const void* base, int64_t at, const Lane&
 __device__ __forceinline__ unsigned pack2(float x, float y) {
   return __builtin_bit_cast(unsigned, (v2bf){(__bf16)x, (__bf16)y});
 }
-// STREAM: past the caches.  Results of more than they hold are written so: they would only drive out what is still to be read (8192 tokens of
-// 32 + 8 heads of 128 into the cache 40.6 -> 36.2 us, forward and backward 82.3 -> 79.1); small ones stay for the reader after.
-template <bool BF16, bool STREAM>
+// The second-level cache writes results through as they come instead of all at once when the kernel ends.  8192 tokens of 32 + 8 heads of 128,
+// forward and what reads the results next: 50.1 us for ordinary stores, 48.1 so; with cold caches 54.7 and 55.0.  (Past all caches, the call alone is
+// faster yet, into the FP8 cache 36.0 us where this one takes 39.2 and ordinary stores 40.6, but its reader has to fetch the results from HBM:
+// with cold caches 64.9 for both.)
+__device__ __forceinline__ void store_through(v4u* to, v4u x) {
+  // (a wave may not write the registers of such a store in the next cycle)
+  asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 1" ::"v"(to), "v"(x) : "memory");
+}
+template <bool BF16>
 __device__ __forceinline__ void store16(void* base, int64_t at, const Lane& l, const float (&x)[16]) {
   constexpr int N = BF16 ? 1 : 2;  // 16-byte pieces of a chunk
 #pragma unroll
@@ -63,12 +69,7 @@ __device__ __forceinline__ void store16(void* base, int64_t at, const Lane& l, c
     }
     v4u* dst = BF16 ? (v4u*)((uint16_t*)base + to) : (v4u*)((float*)base + to);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (STREAM)
-        __builtin_nontemporal_store(out[i], dst + i);
-      else
-        dst[i] = out[i];
-    }
+    for (int i = 0; i < N; ++i) store_through(dst + i, out[i]);
   }
 }
 
@@ -119,7 +120,7 @@ __device__ __forceinline__ void load_weights(const void* w, bool bf16, const Lan
 }
 
 // ---------------------------------------------------------------- forward
-template <int D, bool BF16, bool INTER, bool WRITE, bool STREAM>
+template <int D, bool BF16, bool INTER, bool WRITE>
 __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
   constexpr int L = D / 16, HEADS = 64 / L;
   const int lane = threadIdx.x & 63, l = lane % L;
@@ -167,11 +168,11 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
     return;
   }
   const Rows& to = is_q ? p.q_out : p.k_out;
-  store16<BF16, STREAM>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+  store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
 }
 
 // ---------------------------------------------------------------- backward
-template <int D, bool BF16, bool INTER, bool STREAM>
+template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
   constexpr int L = D / 16, HEADS = 64 / L;
   __shared__ float sums[2][WAVES][D];
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = r * (t[i] - x[i] * mean);
       }
-      store16<BF16, STREAM>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+      store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
     }
     // over the wave's rows: lanes l, l + L, ...
 #pragma unroll
@@ -251,26 +252,19 @@ __global__ void __launch_bounds__(1024) weights_kernel(const RopeParams p) {
   (i < D ? p.dq_weight : p.dk_weight)[i % D] = s;
 }
 
-template <int D, bool BF16, bool INTER, bool STREAM>
-hipError_t forward_as(const RopeParams& p, bool write, hipStream_t stream) {
-  const unsigned grid = (unsigned)(((int64_t)p.num_tokens * p.pieces.d + WAVES - 1) / WAVES);
-  if (write)
-    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, true, STREAM>), dim3(grid), dim3(THREADS), 0, stream, p);
-  else
-    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, false, STREAM>), dim3(grid), dim3(THREADS), 0, stream, p);
-  return hipGetLastError();
-}
 template <int D, bool BF16, bool INTER>
 hipError_t forward(const RopeParams& p, bool write, hipStream_t stream) {
-  return p.stream_out ? forward_as<D, BF16, INTER, true>(p, write, stream) : forward_as<D, BF16, INTER, false>(p, write, stream);
+  const unsigned grid = (unsigned)(((int64_t)p.num_tokens * p.pieces.d + WAVES - 1) / WAVES);
+  if (write)
+    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, true>), dim3(grid), dim3(THREADS), 0, stream, p);
+  else
+    hipLaunchKernelGGL((forward_kernel<D, BF16, INTER, false>), dim3(grid), dim3(THREADS), 0, stream, p);
+  return hipGetLastError();
 }
 
 template <int D, bool BF16, bool INTER>
 hipError_t backward(const RopeParams& p, hipStream_t stream) {
-  if (p.stream_out)
-    hipLaunchKernelGGL((backward_kernel<D, BF16, INTER, true>), dim3(p.workgroups), dim3(THREADS), 0, stream, p);
-  else
-    hipLaunchKernelGGL((backward_kernel<D, BF16, INTER, false>), dim3(p.workgroups), dim3(THREADS), 0, stream, p);
+  hipLaunchKernelGGL((backward_kernel<D, BF16, INTER>), dim3(p.workgroups), dim3(THREADS), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.workgroups == 1) return e;
   hipLaunchKernelGGL((weights_kernel<D>), dim3(2 * D / 32), dim3(1024), 0, stream, p);
