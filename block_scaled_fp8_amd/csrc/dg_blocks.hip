@@ -303,11 +303,11 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
 
-// The largest number that at least `need` of what `count` counts reach, from `low`, which `reach` of them do, to `high`.  Leaves in
-// `reach` how many reach it; with EARLY, any number that exactly `need` reach will do.
-template <bool EARLY, class Count>
-__device__ __forceinline__ uint32_t threshold(uint32_t low, uint32_t high, int need, int& reach, Count count) {
-  while (low < high && !(EARLY && reach == need)) {
+// The largest number that at least `need` of what `count` counts reach, from `low`, which `reach` of them do, to `high`; or any smaller one that no
+// more than `enough` reach.  Leaves in `reach` how many reach it, and in `high` a number that is no smaller than the largest.
+template <class Count>
+__device__ __forceinline__ uint32_t threshold(uint32_t low, uint32_t& high, int need, int enough, int& reach, Count count) {
+  while (low < high && reach > enough) {
     const uint32_t mid = low + (high - low) / 2 + 1;
     const int n = count(mid);
     if (n >= need)
@@ -363,7 +363,10 @@ __device__ __forceinline__ void choose(const SelectParams& p, int place, const u
     // (the smallest of the lanes' largest is reached by every lane; no score is 0)
     low = need <= 64 ? max(~wave_max(~kept[0]), 1u) : 1u;
     int reach = keeping(low);
-    if (reach >= need) low = threshold<true>(low, high, need, reach, keeping);
+    if (reach >= need) {
+      uint32_t end = high;
+      low = threshold(low, end, need, need, reach, keeping);
+    }
     held = 0;
 #pragma unroll 4
     for (int i0 = 0; i0 < count; i0 += 64) {
@@ -395,9 +398,8 @@ __device__ __forceinline__ void choose(const SelectParams& p, int place, const u
     high = wave_max(most);
     low = need <= 64 ? max(~wave_max(~most), 1u) : 1u;
   }
-  auto search = [&](auto reaching) {
-    int reach = reaching(low);
-    const uint32_t t = threshold<true>(low, high, need, reach, reaching);
+  auto search = [&](auto reaching, int reach) {
+    const uint32_t t = threshold(low, high, need, need, reach, reaching);
     if (reach == need) {
       int at = p.first;
 #pragma unroll 4
@@ -422,24 +424,48 @@ __device__ __forceinline__ void choose(const SelectParams& p, int place, const u
     }
   };
   auto search_held = [&](auto registers) {
-    search([&](uint32_t t) {
+    constexpr int R = decltype(registers)::value;
+    auto reaching = [&](uint32_t t) {
       int n = 0;
 #pragma unroll
-      for (int r = 0; r < decltype(registers)::value; ++r) n += (int)__popcll(__ballot(x[r] >= t));
+      for (int r = 0; r < R; ++r) n += (int)__popcll(__ballot(x[r] >= t));
       return n;
-    });
+    };
+    int reach = reaching(low);
+    if (need <= 64) {
+      // down to 64 of them, which then go to a lane each
+      low = threshold(low, high, need, 64, reach, reaching);
+      if (reach <= 64) {
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint64_t some = __ballot(x[r] >= low);
+          if (x[r] >= low) candidates[n + (int)__popcll(some & below)] = x[r];
+          n += (int)__popcll(some);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const uint32_t y = lane < reach ? candidates[lane] : 0u;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        return search([&](uint32_t t) { return (int)__popcll(__ballot(y >= t)); }, reach);
+      }
+    }
+    search(reaching, reach);
   };
   if (held <= 128)
     search_held(std::integral_constant<int, 2>());
   else if (held <= CANDIDATES)
     search_held(std::integral_constant<int, HELD>());
-  else  // (more candidates than there is room for: more than 256 blocks to choose, or many equal scores)
-    search([&](uint32_t t) {
+  else {  // (more candidates than there is room for: more than 256 blocks to choose, or many equal scores)
+    const auto reaching = [&](uint32_t t) {
       int n = 0;
 #pragma unroll 8
       for (int i0 = 0; i0 < count; i0 += 64) n += (int)__popcll(__ballot(i0 + lane < count && row[min(i0 + lane, count - 1)] >= t));
       return n;
-    });
+    };
+    search(reaching, reaching(low));
+  }
 }
 
 template <int D, int TILES>
