@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(KEYS_WAVES * 64) block_keys_kernel(const Block
     }
   }
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) *(v2d*)&sums[wave][r][16 * l + i] = (v2d){s[i], s[i + 1]};
+  // (pairs of a lane's eight change places by the lane's number, so that lanes next to each other write to, and read from, different banks)
+  for (int i = 0; i < 16; i += 2) *(v2d*)&sums[wave][r][16 * l + (i ^ 2 * (lane & 7))] = (v2d){s[i], s[i + 1]};
   // (the wave reads what its own lanes wrote: its LDS operations complete in order)
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(KEYS_WAVES * 64) block_keys_kernel(const Block
   for (int e = 0; e < E; ++e) {
     mean[e] = 0.0;
 #pragma unroll
-    for (int x = 0; x < ROWS; ++x) mean[e] += sums[wave][x][E * lane + e];
+    for (int x = 0; x < ROWS; ++x) mean[e] += sums[wave][x][(E * lane + e) ^ 2 * ((x * L + E * lane / 16) & 7)];
     mean[e] /= (double)p.c.page.d;
     top = max(top, (uint64_t)__double_as_longlong(__builtin_fabs(mean[e])));
   }
