@@ -111,7 +111,8 @@ SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
   SelectPlan pl;
   const int64_t scored = table_cols > top ? table_cols - first - last : 1;
   pl.row_words = ceil_div(scored, 16) * 16 + 4;
-  // Scores of up to 64 KiB, so that two workgroups share a compute unit.
+  // Scores of up to 64 KiB, so that two workgroups share a compute unit.  Fewer tokens than a workgroup can take, where they would leave compute units
+  // without one (64 tokens over 512 blocks: 10.5 us, else 19.2; with four workgroups for a unit 13.2).
   const int64_t fit = 65536 / (4 * pl.row_words), per_tile = 16 / width;
   pl.tile_tokens = per_tile * dg::select_tiles(head_dim);
   while (pl.tile_tokens > 1 && (pl.tile_tokens > fit || pl.tile_tokens >= 2 * a.most_tokens() ||
@@ -120,7 +121,8 @@ SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
   pl.one_tile = pl.tile_tokens <= per_tile;
   pl.parts = 1;
-  // Few tiles of many blocks: a workgroup for each 256 blocks.
+  // Few tiles of many blocks: a workgroup for each 256 blocks (2 sequences of 2048 blocks and 4 heads: 17.2 us, in one part 23.6; 500 blocks for 8 heads,
+  // which stay in one, 7.6).
   const int64_t tiles = pl.items * num_kv_heads;
   if (pl.one_tile && scored > 512 && 4 * tiles <= num_sms) {
     const int64_t by_blocks = ceil_div(scored, 256), by_units = num_sms / tiles;
@@ -174,12 +176,15 @@ SparsePlan sparse_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
   const int64_t segments = pl.tile_tokens * top * ceil_div(page_size, 64), slots = num_sms;
   pl.parts = 1;
   pl.waves = 4;
-  // Short lists of few tiles: eight waves instead of parts, whose second kernel costs the host more than it saves the device.  (At
-  // 256 values a head eight waves run out of registers.)
+  // Short lists of few tiles: eight waves instead of parts, whose second kernel costs the host more than it saves the device (one token of 8 key
+  // heads over 16 blocks of 64: choice and attention 21 us a call with the host, in parts 31; on the device alone 10.3 and 9.6; over 32 blocks
+  // 14.6 and 9.6).  (At 256 values a head eight waves run out of registers.)
   if (head_dim != 256 && work <= num_sms && segments > 4 && segments <= 20) {
     pl.waves = 8;
     return pl;
   }
+  // Parts until there is a workgroup for each compute unit (8 sequences, 8 key heads, 64 blocks: 19.0 us, in one part 34.6; with three for a unit
+  // 20.3), of eight segments at least, two for a wave (1 sequence: 9.9 us, in one part 33).
   while (pl.parts < 64 && 2 * pl.parts * work <= slots && 8 * pl.parts <= segments) pl.parts *= 2;
   return pl;
 }

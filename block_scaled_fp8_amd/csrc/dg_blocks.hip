@@ -21,7 +21,7 @@ typedef double v2d __attribute__((ext_vector_type(2)));
 // ---------------------------------------------------------------- block keys
 // A wave has a page and head: D / 16 lanes a key of 16 codes each, 1024 / D keys at a time.  The sum is taken in 64 bits, where
 // codes (multiples of 2^-9 up to 448) under scales of up to 2^25 apart add up without rounding.  Bound by reading
-// the keys.
+// the keys, for which four loads of a lane go out together (2047 pages of 64 keys and 8 heads of 128: 30 us, 4.6 TB/s; one at a time 40).
 constexpr int KEYS_WAVES = 4;
 
 template <int D>
@@ -114,6 +114,10 @@ __global__ void __launch_bounds__(KEYS_WAVES * 64) block_keys_kernel(const Block
 // largest over a token's columns goes to LDS as a number that compares like the score.  Then a wave has a token: it
 // finds the largest threshold that enough scores reach by bisection, a compare and a population count for 64 of them, and writes
 // the chosen blocks in order.
+//
+// What bounds it: latency.  A workgroup's steps (queries to codes, keys through their pages' numbers, the choice) wait for each other; a chunk of
+// 2048 tokens over 512 blocks (32 + 8 heads of 128) takes 46 us, 30 of them for the scores, with the vector units busy for half of the time.  The
+// workgroup's 4 tiles of 16 columns take a block key from memory once (44 us; 2 tiles 52, 8 tiles 50), by 8 waves (4: 58).
 //
 // Few sequences with many blocks leave most of the chip idle in that form.  There the scores go to memory, a slice of
 // the blocks to a workgroup, and a second kernel with a wave for each token and key head chooses.

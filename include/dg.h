@@ -512,6 +512,9 @@ int64_t dg_fp8_kv_select_blocks_workspace(int32_t batch, int32_t total_q, int32_
  *  blocks : device int32 [total_q, cache->num_heads, top], contiguous: block numbers, strictly ascending, negative ones
  *           at the end only.  (What is not so gives wrong sums, but reads nothing outside the cache.)  Blocks past the query's
  *           place, and past the table, hold nothing that it sees.  A query without a key gives zeros and lse = -infinity.
+ *  top in [1, 2^20], and top * ceil(page_size / 64) <= 2^30.
+ * A value's scale multiplies its weight here: a value of 2^120 and more counts by its weight, and gives what that product and
+ * sum give, a number, an infinity or NaN, at its place of the head for the queries that see it.
  * The same call gives the same results in every run (no atomics); a token's last bits depend on the shape of the call and the lists of
  * the tokens beside it.
  */
