@@ -68,14 +68,17 @@ dg::RopeParams kernel_params(const dg_norm_rope* a) {
   p.kv_heads = a->num_kv_heads;
   p.eps = a->eps;
   p.weights_bf16 = a->weight_dtype == DG_IN_BF16;
+  const int heads = dg::rope_heads(a->head_dim);
+  p.q_pieces = (a->num_q_heads + heads - 1) / heads;
+  p.kv_pieces = (a->num_kv_heads + heads - 1) / heads;
   return p;
 }
 
 int forward(const dg_norm_rope* a, dg::Rows q, dg::Rows k, dg::Rows v, dg::Rows q_out, dg::Rows k_out, const dg_fp8_kv_cache* cache,
             const int64_t* slots, hipStream_t stream) {
-  const int esz = element_size(a), rows = a->num_q_heads + (cache ? 2 : 1) * a->num_kv_heads;
-  const int heads = dg::rope_heads(a->head_dim), pieces = (rows + heads - 1) / heads;
+  const int esz = element_size(a);
   dg::RopeParams p = kernel_params(a);
+  const int pieces = p.q_pieces + (cache ? 2 : 1) * p.kv_pieces;
   p.pieces = dg::fast_div(pieces);
   if (cache) p.c = dg::kernel_cache(cache);
   // A grid has less than 2^32 threads (one of more is cut to its low 32 bits without an error): 2^25 waves at a time.

@@ -68,7 +68,8 @@ struct RopeParams {
   int32_t weights_bf16;
   KvCache c;
   const int64_t* slots;
-  FastDiv pieces;                   // waves that share a token (backward: of the section)
+  FastDiv pieces;                   // waves that share a token (forward)
+  int32_t q_pieces, kv_pieces;      // those of its queries, and of its keys (forward: and as many of its values)
   float *dq_weight, *dk_weight;     // [head dim]
   float* parts;                     // [workgroups, 2, head dim] sums of the weights' gradients (workgroups > 1)
   int32_t workgroups;               // backward only

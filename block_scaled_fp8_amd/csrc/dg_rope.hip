@@ -11,7 +11,7 @@
 // Bound by memory.  A row is D / 16 lanes of 16 values, two chunks of eight that hold whole pairs: lane l < R / 16
 // has chunks l and l + R / 16 (interleaved: 2 l and 2 l + 1), so a pair never leaves its lane, and both
 // forms take the same cosines and sines, 8 l to 8 l + 7.  The rest of the row goes in pairs of chunks to the
-// lanes after those.  A wave takes 1024 / D heads of one token.  8192 tokens of 32 + 8 heads of 128, BF16: forward 26 us (168 MB: 6.4 TB/s with
+// lanes after those.  A wave takes 1024 / D heads of one token, of queries or keys or values.  8192 tokens of 32 + 8 heads of 128, BF16: forward 26 us (168 MB: 6.4 TB/s with
 // what the caches hold), backward 46 (252 MB, 5.5 TB/s) and 4 for the weights, forward into the cache 30 (189 MB, 6.3 TB/s).
 #include <type_traits>
 
@@ -128,48 +128,48 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * WAVES + (threadIdx.x >> 6));
   const int token = div(wave, p.pieces);
   if (token >= p.num_tokens) return;
-  // rows of a token: its queries, keys and (where they are written) values
-  const int row = (wave - token * p.pieces.d) * HEADS + lane / L;
-  const int keys = row - p.q_heads, values = keys - p.kv_heads;
-  if (keys >= (WRITE ? 2 : 1) * p.kv_heads) return;
-  const bool is_q = keys < 0, is_v = WRITE && values >= 0;
-  const int head = is_q ? row : is_v ? values : keys;
+  // a wave's rows are all queries, all keys or all values (where these are written), so what depends on that is scalar
+  const int piece = wave - token * p.pieces.d, after_q = piece - p.q_pieces, after_k = after_q - p.kv_pieces;
+  const bool is_q = after_q < 0, is_v = WRITE && after_k >= 0;
+  const int head = (is_q ? piece : is_v ? after_k : after_q) * HEADS + lane / L;
+  if (head >= (is_q ? p.q_heads : p.kv_heads)) return;
   const int64_t position = p.positions[token];
   const bool live = (uint64_t)position < (uint64_t)p.num_positions;
-  Place at;
-  bool put = false;
-  if (WRITE && !is_q) {
-    put = live && place_of(p.c, p.slots[token], head, at);
-    if (!put) return;
-  }
+  int64_t slot = 0;
+  if (WRITE) slot = p.slots[token];
   const Lane my = is_v ? Lane{16 * l, 16 * l + 8, false} : lane_of<D, INTER>(l, p.rot);
-  const Rows& from = is_q ? p.q : is_v ? p.v : p.k;
-  float x[16] = {};
-  if (live) {
-    load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
-    if (!is_v) {
-      float w[16];
-      Angles a;
-      load_weights(is_q ? p.q_weight : p.k_weight, p.weights_bf16, my, w);
-      if (my.turns) load_angles(p, position, l, a);
-      const float r = inverse_rms<D>(x, p.eps);
+  const Rows from = is_q ? p.q : is_v ? p.v : p.k, to = is_q ? p.q_out : p.k_out;
+  const int64_t to_row = token * to.token_stride + head * to.head_stride;
+  if (!live) {
+    const float zeros[16] = {};
+    if (!WRITE || is_q) store16<BF16>(to.p, to_row, my, zeros);
+    return;
+  }
+  float x[16];
+  load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
+  if (!is_v) {
+    float w[16];
+    Angles a;
+    load_weights(is_q ? p.q_weight : p.k_weight, p.weights_bf16, my, w);
+    if (my.turns) load_angles(p, position, l, a);
+    const float r = inverse_rms<D>(x, p.eps);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
-      if (my.turns) turn<INTER, 1>(x, a);
-    }
+    for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+    if (my.turns) turn<INTER, 1>(x, a);
   }
   if (WRITE && !is_q) {
+    Place at;
+    if (!place_of(p.c, slot, head, at)) return;
     uint32_t sf;
     v2u codes[2];
     encode<L>(x, codes, sf);
-    uint8_t* to = (is_v ? p.c.v : p.c.k) + at.code;
-    *(v2u*)(to + my.c0) = codes[0];
-    *(v2u*)(to + my.c1) = codes[1];
+    uint8_t* dst = (is_v ? p.c.v : p.c.k) + at.code;
+    *(v2u*)(dst + my.c0) = codes[0];
+    *(v2u*)(dst + my.c1) = codes[1];
     if (l == 0) (is_v ? p.c.v_sf : p.c.k_sf)[at.sf] = (uint8_t)sf;
     return;
   }
-  const Rows& to = is_q ? p.q_out : p.k_out;
-  store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+  store16<BF16>(to.p, to_row, my, x);
 }
 
 // ---------------------------------------------------------------- backward
@@ -177,40 +177,48 @@ template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
   constexpr int L = D / 16, HEADS = 64 / L;
   __shared__ float sums[2][WAVES][D];
-  const int lane = threadIdx.x & 63, l = lane % L, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, l = lane % L, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Lane my = lane_of<D, INTER>(l, p.rot);
 #pragma unroll 1
   for (int section = 0; section < 2; ++section) {
-    const Rows &from = section ? p.k : p.q, &grad = section ? p.dk : p.dq, &to = section ? p.k_out : p.q_out;
-    const int heads = section ? p.kv_heads : p.q_heads, pieces = (heads + HEADS - 1) / HEADS;
+    const Rows from = section ? p.k : p.q, grad = section ? p.dk : p.dq, to = section ? p.k_out : p.q_out;
+    const int heads = section ? p.kv_heads : p.q_heads, pieces = section ? p.kv_pieces : p.q_pieces;
     float w[16], dw[16] = {};
     load_weights(section ? p.k_weight : p.q_weight, p.weights_bf16, my, w);
-    const int64_t items = (int64_t)p.num_tokens * pieces;
-    for (int64_t item = blockIdx.x * WAVES + wave; item < items; item += p.workgroups * WAVES) {
-      const int token = (int)(item / pieces), head = (int)(item - (int64_t)token * pieces) * HEADS + lane / L;
+    // every (workgroups * WAVES)th piece
+    const int step = p.workgroups * WAVES, step_token = step / pieces, step_piece = step - step_token * pieces;
+    const int id = blockIdx.x * WAVES + wave;
+    int token = id / pieces, piece = id - token * pieces;
+    for (; token < p.num_tokens; token += step_token) {
+      const int head = piece * HEADS + lane / L, at = token;
+      piece += step_piece;
+      if (piece >= pieces) piece -= pieces, ++token;
       if (head >= heads) continue;
-      const int64_t position = p.positions[token];
-      float x[16] = {}, t[16] = {};
-      if ((uint64_t)position < (uint64_t)p.num_positions) {
-        Angles a;
-        load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
-        load16<BF16>(grad.p, token * grad.token_stride + head * grad.head_stride, my, t);
-        if (my.turns) load_angles(p, position, l, a);
-        const float r = inverse_rms<D>(x, p.eps);
-        if (my.turns) turn<INTER, -1>(t, a);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] *= r;
-          dw[i] = __builtin_fmaf(t[i], x[i], dw[i]);
-          t[i] *= w[i];
-          s = __builtin_fmaf(t[i], x[i], s);
-        }
-        const float mean = row_sum<L>(s) * (1.f / D);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = r * (t[i] - x[i] * mean);
+      const int64_t position = p.positions[at], to_row = at * to.token_stride + head * to.head_stride;
+      if ((uint64_t)position >= (uint64_t)p.num_positions) {
+        const float zeros[16] = {};
+        store16<BF16>(to.p, to_row, my, zeros);
+        continue;
       }
-      store16<BF16>(to.p, token * to.token_stride + head * to.head_stride, my, x);
+      float x[16], t[16];
+      Angles a;
+      load16<BF16>(from.p, at * from.token_stride + head * from.head_stride, my, x);
+      load16<BF16>(grad.p, at * grad.token_stride + head * grad.head_stride, my, t);
+      if (my.turns) load_angles(p, position, l, a);
+      const float r = inverse_rms<D>(x, p.eps);
+      if (my.turns) turn<INTER, -1>(t, a);
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] *= r;
+        dw[i] = __builtin_fmaf(t[i], x[i], dw[i]);
+        t[i] *= w[i];
+        s = __builtin_fmaf(t[i], x[i], s);
+      }
+      const float mean = row_sum<L>(s) * (1.f / D);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = r * (t[i] - x[i] * mean);
+      store16<BF16>(to.p, to_row, my, x);
     }
     // over the wave's rows: lanes l, l + L, ...
 #pragma unroll
