@@ -140,13 +140,13 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
   const Lane my = is_v ? Lane{16 * l, 16 * l + 8, false} : lane_of<D, INTER>(l, p.rot);
   const Rows from = is_q ? p.q : is_v ? p.v : p.k, to = is_q ? p.q_out : p.k_out;
   const int64_t to_row = token * to.token_stride + head * to.head_stride;
+  float x[16];  // (on its way before its position is known)
+  load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
   if (!live) {
     const float zeros[16] = {};
     if (!WRITE || is_q) store16<BF16>(to.p, to_row, my, zeros);
     return;
   }
-  float x[16];
-  load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
   if (!is_v) {
     float w[16];
     Angles a;
@@ -195,15 +195,15 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
       if (piece >= pieces) piece -= pieces, ++token;
       if (head >= heads) continue;
       const int64_t position = p.positions[at], to_row = at * to.token_stride + head * to.head_stride;
+      float x[16], t[16];  // (on their way before the position is known)
+      load16<BF16>(from.p, at * from.token_stride + head * from.head_stride, my, x);
+      load16<BF16>(grad.p, at * grad.token_stride + head * grad.head_stride, my, t);
       if ((uint64_t)position >= (uint64_t)p.num_positions) {
         const float zeros[16] = {};
         store16<BF16>(to.p, to_row, my, zeros);
         continue;
       }
-      float x[16], t[16];
       Angles a;
-      load16<BF16>(from.p, at * from.token_stride + head * from.head_stride, my, x);
-      load16<BF16>(grad.p, at * grad.token_stride + head * grad.head_stride, my, t);
       if (my.turns) load_angles(p, position, l, a);
       const float r = inverse_rms<D>(x, p.eps);
       if (my.turns) turn<INTER, -1>(t, a);
