@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
   if (!is_v) {
     float w[16];
     Angles a;
+    load_angles(p, position, my.turns ? l : 0, a);
+    // (last: what has come by the branch on their type is waited for in it)
     load_weights(is_q ? p.q_weight : p.k_weight, p.weights_bf16, my, w);
-    if (my.turns) load_angles(p, position, l, a);
     const float r = inverse_rms<D>(x, p.eps);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
         continue;
       }
       Angles a;
-      if (my.turns) load_angles(p, position, l, a);
+      load_angles(p, position, my.turns ? l : 0, a);
       const float r = inverse_rms<D>(x, p.eps);
       if (my.turns) turn<INTER, -1>(t, a);
       float s = 0.f;
