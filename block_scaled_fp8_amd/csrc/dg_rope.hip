@@ -195,7 +195,9 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
       piece += step_piece;
       if (piece >= pieces) piece -= pieces, ++token;
       if (head >= heads) continue;
-      const int64_t position = p.positions[at], to_row = at * to.token_stride + head * to.head_stride;
+      // (no result overlaps the positions, so the load may be scalar)
+      const int64_t position = ((const __attribute__((address_space(4))) int64_t*)p.positions)[at];
+      const int64_t to_row = at * to.token_stride + head * to.head_stride;
       float x[16], t[16];  // (on their way before the position is known)
       load16<BF16>(from.p, at * from.token_stride + head * from.head_stride, my, x);
       load16<BF16>(grad.p, at * grad.token_stride + head * grad.head_stride, my, t);
@@ -207,6 +209,9 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
       Angles a;
       load_angles(p, position, my.turns ? l : 0, a);
       const float r = inverse_rms<D>(x, p.eps);
+      // (loaded with the rows, not where only the turning lanes are)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(a.c[i]), "+v"(a.s[i]));
       if (my.turns) turn<INTER, -1>(t, a);
       float s = 0.f;
 #pragma unroll
