@@ -102,8 +102,8 @@ int forward(const dg_norm_rope* a, dg::Rows q, dg::Rows k, dg::Rows v, dg::Rows 
 }
 
 // Workgroups of the backward kernel: its waves go over (token, heads of a wave) in turn, and each workgroup leaves one set
-// of the weights' sums.  Four for a compute unit: 8192 tokens of 32 + 8 heads of 128, forward and backward, take 81.5 us, with two 86.6, and with eight the
-// backward kernel takes 2.5 us more.
+// of the weights' sums.  Four for a compute unit, as many as it holds: 8192 tokens of 32 + 8 heads of 128, forward and backward, take 78.0 us, with
+// five (and registers for them) 80.9; with two and with eight it was 5 and 2.5 us more.
 int backward_workgroups(int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int num_sms) {
   const int heads = dg::rope_heads(head_dim);
   const int most = num_q_heads > num_kv_heads ? num_q_heads : num_kv_heads;

@@ -11,8 +11,9 @@
 // Bound by memory.  A row is D / 16 lanes of 16 values, two chunks of eight that hold whole pairs: lane l < R / 16
 // has chunks l and l + R / 16 (interleaved: 2 l and 2 l + 1), so a pair never leaves its lane, and both
 // forms take the same cosines and sines, 8 l to 8 l + 7.  The rest of the row goes in pairs of chunks to the
-// lanes after those.  A wave takes 1024 / D heads of one token, of queries or keys or values.  8192 tokens of 32 + 8 heads of 128, BF16: forward 26 us (168 MB: 6.4 TB/s with
-// what the caches hold), backward 46 (252 MB, 5.5 TB/s) and 4 for the weights, forward into the cache 30 (189 MB, 6.3 TB/s).
+// lanes after those.  A wave takes 1024 / D heads of one token, all of them queries, keys or values, and its loads go out together, before anything
+// waits.  8192 tokens of 32 + 8 heads of 128, BF16: forward 26 us (168 MB: 6.5 TB/s with what the caches hold), backward 44 (252 MB, 5.7 TB/s)
+// and 4 for the weights, forward into the cache 30 (189 MB, 6.3 TB/s).
 #include <type_traits>
 
 #include "dg_kv_device.h"
@@ -45,10 +46,9 @@ __device__ __forceinline__ void load16(const void* base, int64_t at, const Lane&
 __device__ __forceinline__ unsigned pack2(float x, float y) {
   return __builtin_bit_cast(unsigned, (v2bf){(__bf16)x, (__bf16)y});
 }
-// The second-level cache writes results through as they come instead of all at once when the kernel ends.  8192 tokens of 32 + 8 heads of 128,
-// forward and what reads the results next: 50.1 us for ordinary stores, 48.1 so; with cold caches 54.7 and 55.0.  (Past all caches, the call alone is
-// faster yet, into the FP8 cache 36.0 us where this one takes 39.2 and ordinary stores 40.6, but its reader has to fetch the results from HBM:
-// with cold caches 64.9 for both.)
+// The second-level cache writes results through as they come instead of all at once when the kernel ends: 8192 tokens of 32 + 8 heads of 128, forward
+// and what reads its results next, 48.1 us, by ordinary stores 50.1.  (Stores past all caches end sooner yet, but whoever reads their results has to
+// fetch them from HBM: with cold caches 64.9 us in place of 55.0.)
 __device__ __forceinline__ void store_through(v4u* to, v4u x) {
   // (a wave may not write the registers of such a store in the next cycle)
   asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 1" ::"v"(to), "v"(x) : "memory");
@@ -154,9 +154,12 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
     // (last: what has come by the branch on their type is waited for in it)
     load_weights(is_q ? p.q_weight : p.k_weight, p.weights_bf16, my, w);
     const float r = inverse_rms<D>(x, p.eps);
+    // (the weight first: two BF16's product is exact; r last: it rounds once what the turn has rounded)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+    for (int i = 0; i < 16; ++i) x[i] *= w[i];
     if (my.turns) turn<INTER, 1>(x, a);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] *= r;
   }
   if (WRITE && !is_q) {
     Place at;
