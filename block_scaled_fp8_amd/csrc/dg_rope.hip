@@ -46,31 +46,45 @@ __device__ __forceinline__ void load16(const void* base, int64_t at, const Lane&
 __device__ __forceinline__ unsigned pack2(float x, float y) {
   return __builtin_bit_cast(unsigned, (v2bf){(__bf16)x, (__bf16)y});
 }
-// The second-level cache writes results through as they come instead of all at once when the kernel ends: 8192 tokens of 32 + 8 heads of 128, forward
-// and what reads its results next, 48.1 us, by ordinary stores 50.1.  (Stores past all caches end sooner yet, but whoever reads their results has to
-// fetch them from HBM: with cold caches 64.9 us in place of 55.0.)
+// The second-level cache writes results through as they come instead of all at once when the kernel ends, where a store of a wave covers whole
+// lines' halves: BF16 rows of which all values turn, in halves, on such addresses (8192 tokens of 32 + 8 heads of 128, forward and backward 78.0 us, by ordinary stores 79.6; into
+// the FP8 cache 36.0 and 37.2).  Elsewhere a lane's 16 bytes have others' behind them, which that cache has to gather (FP32, 3307 tokens of 48 + 3 heads of
+// 256, interleaved: forward 80 us, written through 159; BF16 heads of 128 interleaved 29 and 49).  (Stores past all caches are faster alone, but
+// whoever reads the results has to fetch them from HBM: forward and its reader with cold caches 64.9 us, else 55.)
+template <int D, bool BF16, bool INTER>
+__device__ __forceinline__ bool whole_lines(int rot, const Rows& to) {
+  return BF16 && !INTER && rot == D && (((uintptr_t)to.p | (uintptr_t)(2 * to.token_stride) | (uintptr_t)(2 * to.head_stride)) & 63) == 0;
+}
 __device__ __forceinline__ void store_through(v4u* to, v4u x) {
   // (a wave may not write the registers of such a store in the next cycle)
   asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 1" ::"v"(to), "v"(x) : "memory");
 }
 template <bool BF16>
-__device__ __forceinline__ void store16(void* base, int64_t at, const Lane& l, const float (&x)[16]) {
+__device__ __forceinline__ void store16(void* base, int64_t at, const Lane& l, bool through, const float (&x)[16]) {
   constexpr int N = BF16 ? 1 : 2;  // 16-byte pieces of a chunk
+  v4u out[2][N];
+  v4u* dst[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int64_t to = at + (c ? l.c1 : l.c0);
+    dst[c] = BF16 ? (v4u*)((uint16_t*)base + to) : (v4u*)((float*)base + to);
     const float* y = x + 8 * c;
-    v4u out[N];
     if constexpr (BF16) {
-      out[0] = (v4u){pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
+      out[c][0] = (v4u){pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        out[i] = (v4u){__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3])};
+        out[c][i] = (v4u){__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3])};
     }
-    v4u* dst = BF16 ? (v4u*)((uint16_t*)base + to) : (v4u*)((float*)base + to);
+  }
+  if (through) {
+    store_through(dst[0], out[0][0]);
+    store_through(dst[1], out[1][0]);
+  } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) store_through(dst + i, out[i]);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < N; ++i) dst[c][i] = out[c][i];
   }
 }
 
@@ -140,11 +154,12 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
   const Lane my = is_v ? Lane{16 * l, 16 * l + 8, false} : lane_of<D, INTER>(l, p.rot);
   const Rows from = is_q ? p.q : is_v ? p.v : p.k, to = is_q ? p.q_out : p.k_out;
   const int64_t to_row = token * to.token_stride + head * to.head_stride;
+  const bool through = whole_lines<D, BF16, INTER>(p.rot, to);
   float x[16];  // (on its way before its position is known)
   load16<BF16>(from.p, token * from.token_stride + head * from.head_stride, my, x);
   if (!live) {
     const float zeros[16] = {};
-    if (!WRITE || is_q) store16<BF16>(to.p, to_row, my, zeros);
+    if (!WRITE || is_q) store16<BF16>(to.p, to_row, my, through, zeros);
     return;
   }
   if (!is_v) {
@@ -173,7 +188,7 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
     if (l == 0) (is_v ? p.c.v_sf : p.c.k_sf)[at.sf] = (uint8_t)sf;
     return;
   }
-  store16<BF16>(to.p, to_row, my, x);
+  store16<BF16>(to.p, to_row, my, through, x);
 }
 
 // ---------------------------------------------------------------- backward
@@ -187,6 +202,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
   for (int section = 0; section < 2; ++section) {
     const Rows from = section ? p.k : p.q, grad = section ? p.dk : p.dq, to = section ? p.k_out : p.q_out;
     const int heads = section ? p.kv_heads : p.q_heads, pieces = section ? p.kv_pieces : p.q_pieces;
+    const bool through = whole_lines<D, BF16, INTER>(p.rot, to);
     float w[16], dw[16] = {};
     load_weights(section ? p.k_weight : p.q_weight, p.weights_bf16, my, w);
     // every (workgroups * WAVES)th piece
@@ -206,7 +222,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
       load16<BF16>(grad.p, at * grad.token_stride + head * grad.head_stride, my, t);
       if ((uint64_t)position >= (uint64_t)p.num_positions) {
         const float zeros[16] = {};
-        store16<BF16>(to.p, to_row, my, zeros);
+        store16<BF16>(to.p, to_row, my, through, zeros);
         continue;
       }
       Angles a;
@@ -227,7 +243,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const RopeParams p) {
       const float mean = row_sum<L>(s) * (1.f / D);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = r * (t[i] - x[i] * mean);
-      store16<BF16>(to.p, to_row, my, x);
+      store16<BF16>(to.p, to_row, my, through, x);
     }
     // over the wave's rows: lanes l, l + L, ...
 #pragma unroll
