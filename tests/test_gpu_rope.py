@@ -87,6 +87,30 @@ def test_in_place(bf16):
     assert got[0] is q and torch.equal(q, want[0]) and torch.equal(k, want[1])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("offset,gap", [(8, 0), (0, 8), (32, 0), (0, 32)])
+def test_results_at_any_address(dim, offset, gap):
+    """Rows that begin 16 or 64 bytes into a line, and rows with gaps between them: the same values, and nothing beside them."""
+    p = rope_gen.problem(21, 9, 2, dim, dim, True, 11)
+    q, k, _, args = operands(p)
+    grads = cuda(p["dq"], True), cuda(p["dk"], True)
+    want, back = dg.qk_norm_rope(q, k, *args), dg.qk_norm_rope_backward(*grads, q, k, *args)
+    wide = [torch.full((21 * h * (dim + gap) + offset,), 77, dtype=torch.bfloat16, device=DEV) for h in (9, 2)]
+    out = [x[offset:].view(21, -1, dim + gap)[..., :dim] for x in wide]
+    for call, ref in ((lambda: dg.qk_norm_rope(q, k, *args, out=tuple(out)), want),
+                      (lambda: dg.qk_norm_rope_backward(*grads, q, k, *args, out=tuple(out)), back)):
+        assert all(torch.equal(x, y) for x, y in zip(call(), ref))
+        assert all((x[:offset] == 77).all() and (x[offset:].view(-1, dim + gap)[:, dim:] == 77).all() for x in wide)
+
+
+def test_a_table_without_positions():
+    p = rope_gen.problem(5, 3, 1, 64, 64, True, 12)
+    q, k, _, (qw, kw, cs, pos) = operands(p)
+    args = qw, kw, cs[:0], pos
+    assert all((x == 0).all() for x in dg.qk_norm_rope(q, k, *args))
+    assert all((x == 0).all() for x in dg.qk_norm_rope_backward(cuda(p["dq"], True), cuda(p["dk"], True), q, k, *args))
+
+
 def test_no_tokens():
     w, cs = torch.ones(128, device=DEV), torch.zeros((4, 128), device=DEV)
     q, k = torch.zeros((0, 4, 128), device=DEV), torch.zeros((0, 2, 128), device=DEV)
