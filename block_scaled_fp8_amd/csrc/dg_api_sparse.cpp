@@ -316,7 +316,14 @@ int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, i
   const int num_sms = dg::api_num_sms();
   if (num_sms <= 0) return api_fail(DG_ERR_HIP, "could not query the device's compute-unit count");
   const SparsePlan pl = sparse_plan(a, cache->num_heads, cache->head_dim, cache->page_size, top, num_sms);
-  if (int s = check_grid(a, pl.items * cache->num_heads * pl.head_tiles * (pl.parts > 16 ? pl.parts : 16), pl.waves * 64)) return s;
+  const int64_t tiles = pl.items * cache->num_heads * pl.head_tiles;
+  const bool far = is_far(cache);
+  const int waves = far ? 4 : pl.waves;
+  if (int s = check_grid(a, tiles * pl.parts, waves * 64)) return s;
+  // (the join, which only parts have, gives each of a tile's 16 rows a workgroup)
+  if (pl.parts > 1) {
+    if (int s = check_grid(a, tiles * 16, 256)) return s;
+  }
   const int64_t need = workspace_of(pl, cache->num_heads, cache->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return api_fail(workspace ? DG_ERR_SHAPE : DG_ERR_NULL, "this call needs a workspace of %lld bytes", (long long)need);
@@ -338,8 +345,8 @@ int dg_fp8_block_sparse_attention(const dg_fp8_kv_cache* cache, int32_t batch, i
   p.tile_tokens = int32_t(pl.tile_tokens);
   p.head_tiles = int32_t(pl.head_tiles);
   p.items = int32_t(pl.items);
-  p.far = is_far(cache);
-  p.waves = p.far ? 4 : pl.waves;
+  p.far = far;
+  p.waves = waves;
   p.parts = int32_t(pl.parts);
   p.part_o = static_cast<float*>(workspace);
   p.part_mz = p.part_o + (pl.parts > 1 ? part_rows(pl, cache->num_heads) * cache->head_dim : 0);

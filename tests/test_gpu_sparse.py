@@ -244,6 +244,17 @@ def test_many_blocks():
     check(p, whole, blocks)
 
 
+def test_many_short_sequences_without_a_bound():
+    """No max_seqlen_q: a launch has a tile for every token of every sequence, of which few have rows."""
+    say("many short sequences")
+    news = [1 + (b % 97 == 5) for b in range(1024)]
+    p = kv_gen.problem([1 + 7 * b % 60 for b in range(1024)], news, 16, 1, 64, 16, 14)
+    blocks = lists(p, 1, 3, 4)
+    q = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
+    caches = [(cuda(p[x][0]), cuda(p[x][1])) for x in "kv"]
+    check(p, dg.fp8_block_sparse_attention(q, *caches, cuda(p["table"]), cuda(p["lens"]), cuda(blocks), cu_seqlens_q=cuda(p["cu"]), return_lse=True), blocks)
+
+
 def test_scale_and_strides():
     p = kv_gen.problem([90, 70, 33], [5, 2, 9], 6, 2, 128, 16, 12)
     blocks = lists(p, 2, 3, 0)

@@ -101,6 +101,24 @@ def test_more_tiles_than_a_launch_holds_are_refused():
         dg.set_num_sms(0)
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would launch kernels on fake addresses")
+def test_ordinary_calls_of_many_tiles_reach_the_launch():
+    """Without a device they end in a launch error: no check of sizes refuses them, here or in the choice of blocks."""
+    heads = cache(num_heads=8, page_size=64, page_stride=65536, head_stride=8192, sf_page_stride=512, sf_head_stride=64)
+    dg.set_num_sms(256)
+    try:
+        for kw in (dict(batch=32, total_q=8192, hq=64, max_q=8192), dict(batch=128, total_q=8192, hq=32, max_q=8192),
+                   dict(batch=1, total_q=131072, hq=128, max_q=131072), dict(batch=1, total_q=131072, hq=128, cu=None, max_q=0)):
+            d = dict(kw, qts=kw["hq"] * 128, top=16)
+            assert attend(heads, ots=kw["hq"] * 128, **d) == HIP, kw
+            assert select(keys(num_heads=8), page=64, **d) == HIP, kw
+        # the most that a launch of four waves holds, and one tile more
+        for batch, code in ((32, HIP), (33, SHAPE)):
+            assert attend(heads, batch=batch, total_q=1 << 17, hq=64, max_q=(1 << 17) - 2, qts=8192, ots=8192, top=16) == code, batch
+    finally:
+        dg.set_num_sms(0)
+
+
 def test_a_workspace_that_is_missing_or_small_is_refused():
     dg.set_num_sms(256)
     try:
