@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 2 : FAR ? 3 : 4) sparse
     }
   }
   const int64_t list_stride = (int64_t)p.c.num_heads * p.top;
-  const int32_t* lists = p.blocks + (int64_t)t.first_row * list_stride + t.kv_head * p.top;
+  const int32_t* lists = p.blocks + t.first_row * list_stride + (int64_t)t.kv_head * p.top;
   if (SHARED) {
     for (int i = threadIdx.x; i < t.tokens * p.top; i += WAVES * 64) {
       const int x = div(i, p.list);

@@ -255,6 +255,20 @@ def test_many_short_sequences_without_a_bound():
     check(p, dg.fp8_block_sparse_attention(q, *caches, cuda(p["table"]), cuda(p["lens"]), cuda(blocks), cu_seqlens_q=cuda(p["cu"]), return_lse=True), blocks)
 
 
+def test_lists_past_32_bits():
+    """A token's lists of 4097 key heads and 2^19 entries: the last head's begins 2^31 entries behind the first one's."""
+    heads, top = 4097, 2 ** 19
+    say("lists past 32 bits")
+    p = kv_gen.problem([40], [1], heads, heads, 64, 16, 15)
+    few = lists(p, heads, 2, 6)
+    few[0, [0, heads - 1]] = [[0, 2], [1, 2]]
+    blocks = torch.full((1, heads, top), -1, dtype=torch.int32, device=DEV)
+    blocks[:, :, :2] = cuda(few)
+    q = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
+    caches = [(cuda(p[x][0]), cuda(p[x][1])) for x in "kv"]
+    check(p, dg.fp8_block_sparse_attention(q, *caches, cuda(p["table"]), cuda(p["lens"]), blocks, return_lse=True), few)
+
+
 def test_scale_and_strides():
     p = kv_gen.problem([90, 70, 33], [5, 2, 9], 6, 2, 128, 16, 12)
     blocks = lists(p, 2, 3, 0)
