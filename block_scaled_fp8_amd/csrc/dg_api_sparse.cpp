@@ -169,11 +169,13 @@ SparsePlan sparse_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
   pl.tile_tokens = group > 16 ? 1 : 16 / group;
   if (pl.tile_tokens > a.most_tokens()) pl.tile_tokens = a.most_tokens();
   if (pl.tile_tokens * top > kMaxListed) pl.tile_tokens = top < kMaxListed ? kMaxListed / top : 1;
+  const int64_t list = top * ceil_div(page_size, 64);  // segments of a token's list: at most 2^30, as all of a tile's have to be
+  if (pl.tile_tokens * list > kMaxIndex) pl.tile_tokens = kMaxIndex / list;
   pl.head_tiles = ceil_div(group, 16);
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
   const int64_t with_rows = a.total_q / pl.tile_tokens + a.batch;  // of the items, at most
   const int64_t work = (with_rows < pl.items ? with_rows : pl.items) * num_kv_heads * pl.head_tiles;
-  const int64_t segments = pl.tile_tokens * top * ceil_div(page_size, 64), slots = num_sms;
+  const int64_t segments = pl.tile_tokens * list, slots = num_sms;
   pl.parts = 1;
   pl.waves = 4;
   // Short lists of few tiles: eight waves instead of parts, whose second kernel costs the host more than it saves the device (one token of 8 key

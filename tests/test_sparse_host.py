@@ -148,6 +148,17 @@ def test_a_workspace_that_is_missing_or_small_is_refused():
         dg.set_num_sms(0)
 
 
+def test_a_tiles_segments_stay_within_32_bits():
+    """The largest pages that a cache may have, 2^19 segments of 64 keys each: 16 tokens of 256 blocks would be 2^31 segments, so a tile has eight."""
+    dg.set_num_sms(256)
+    try:
+        size = dg.lib().dg_fp8_block_sparse_attention_workspace
+        tiles = lambda page, top: size(1, 16, 1, 1, 64, 1, 0, page, top) // (64 * 16 * (64 + 2) * 4)  # noqa: E731  (of 64 parts each)
+        assert tiles((1 << 25) - 1, 256) == 2 and tiles((1 << 25) - 1, 128) == 1 and tiles(1 << 24, 256) == 1 and tiles(1 << 24, 128) == 1
+    finally:
+        dg.set_num_sms(0)
+
+
 def test_the_binding_refuses():
     codes, scales = dg.fp8_kv_block_keys_empty(4, 2, 64, device="cpu")
     assert codes.dtype == torch.int8 and (scales == 1).all()
