@@ -169,6 +169,11 @@ __global__ void __launch_bounds__(THREADS) forward_kernel(const RopeParams p) {
     // (last: what has come by the branch on their type is waited for in it)
     load_weights(is_q ? p.q_weight : p.k_weight, p.weights_bf16, my, w);
     const float r = inverse_rms<D>(x, p.eps);
+    // Squares past FP32's range: finite values become zeros before their products pass it too, whose infinities times r would be NaN.
+    if (__builtin_expect(r == 0.f, 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= 0.f;
+    }
     // (the weight first: two BF16's product is exact; r last: it rounds once what the turn has rounded)
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] *= w[i];

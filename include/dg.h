@@ -543,7 +543,9 @@ int64_t dg_fp8_block_sparse_attention_workspace(int32_t batch, int32_t total_q, 
  *  positions         : device int64 [num_tokens], rows of cos_sin.  A token whose position is negative or past the table is a
  *                      padding token: its rows come back as zeros and add nothing to the weights' gradients.
  *  eps               : finite, not negative.
- * Everything is computed in FP32 and rounded once.  A row's squares are summed in FP32: a row of values past 2^60 or so gives zeros.
+ * Everything is computed in FP32 and rounded once.  A row's squares are summed in FP32: a finite row whose sum passes FP32's range (values past
+ * 2^60 or so) gives zeros, an infinite value NaN at its place and in its pair, a NaN a row of them.  With eps = 0 a row of zeros gives NaN, and one of
+ * values below 2^-60 or so, whose squares fall out of that range, loses digits or gives infinities.
  */
 typedef struct {
   int32_t num_tokens, num_q_heads, num_kv_heads, head_dim;

@@ -140,6 +140,52 @@ def test_numbers_that_are_none_stay_in_their_row():
     assert (back[0][0] == 0).all() and back[2].isfinite().all()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("dim,rot", [(64, 64), (128, 48), (256, 256)])
+def test_rows_of_large_numbers(dim, rot, bf16, interleaved):
+    """Up to 2^59 they are like any other; those whose squares pass FP32's range are zeros, up to the largest numbers and under weights above 1."""
+    p = rope_gen.problem(24, 4, 2, dim, rot, bf16, 13)
+    for n in "qk":
+        p[n] /= np.abs(p[n]).max(-1, keepdims=True)  # (by the largest, which becomes 1)
+        p[n] = rope_gen.to_type(p[n], bf16) * 2.0 ** 59
+        p[n + "w"] = rope_gen.to_type(1.3 + 0.1 * np.abs(p[n + "w"]), bf16)
+    q, k, v, args = operands(p)
+    grads = cuda(p["dq"], bf16), cuda(p["dk"], bf16)
+    want, back = dg.qk_norm_rope(q, k, *args, eps=EPS, interleaved=interleaved), dg.qk_norm_rope_backward(*grads, q, k, *args, eps=EPS, interleaved=interleaved)
+    check_forward(p, want, interleaved)
+    # (gradients come out under 2^-59, still well above the smallest numbers)
+    check_backward(p, back, interleaved)
+    huge = {5: 2.0 ** 66, 6: 2.0 ** 100, 7: 3.3e38, 8: -3.3e38}
+    for t, x in huge.items():
+        q[t, 1], k[t, 0] = x, x
+        q[t, 1, ::3] *= -1
+    k[9, 1], k[9, 1, dim - 1] = 1.0, 2.0 ** 127  # (one such value)
+    caches = dg.fp8_kv_cache_empty(2, 2, 16, dim, device=DEV)
+    for call in (lambda: dg.qk_norm_rope(q, k, *args, eps=EPS, interleaved=interleaved),
+                 lambda: (dg.qk_norm_rope_fp8_kv_cache_write(q, k, v, *args, *caches, torch.arange(24, device=DEV), eps=EPS, interleaved=interleaved),)):
+        for y, was, rows in zip(call(), want, ([(t, 1) for t in huge], [(t, 0) for t in huge] + [(9, 1)])):
+            for t, h in rows:
+                assert (y[t, h] == 0).all(), (t, h, y[t, h])
+                y[t, h] = was[t, h]
+            assert torch.equal(y, was)
+    codes, sf = (x.transpose(1, 2).flatten(0, 1)[:24] for x in caches[0])
+    assert all(not (codes[t, h] & 0x7F).any() and sf[t, h] == 127 for t, h in [(t, 0) for t in huge] + [(9, 1)])
+    got = dg.qk_norm_rope_backward(*grads, q, k, *args, eps=EPS, interleaved=interleaved)
+    assert all((got[0][t, 1] == 0).all() and (got[1][t, 0] == 0).all() for t in huge) and got[2].isfinite().all() and got[3].isfinite().all()
+
+
+def test_infinities_among_large_numbers_stay():
+    p = rope_gen.problem(8, 2, 1, 64, 32, False, 14)
+    q, k, _, args = operands(p)
+    q[5, 0] = 3e38
+    q[5, 0, 40], q[6, 1, 50], q[7, 0, 3] = float("inf"), float("nan"), float("-inf")
+    got = dg.qk_norm_rope(q, k, *args)[0]
+    # what does not turn and is infinite is NaN, the rest of the row zero; a pair that turns has it in both places; a NaN is in all sums
+    assert got[5, 0, 40].isnan() and got[5, 0].isnan().sum() == 1 and (got[5, 0, :40] == 0).all()
+    assert got[6, 1].isnan().all() and got[7, 0].isnan().nonzero().flatten().tolist() == [3, 19]
+
+
 @pytest.mark.parametrize("order", ["hpt", "thd"])
 @pytest.mark.parametrize("bf16,interleaved", [(True, False), (True, True), (False, False)])
 @pytest.mark.parametrize("case,page", [((61, 8, 2, 128, 128), 16), ((40, 9, 3, 64, 32), 7), ((23, 4, 2, 256, 64), 64), ((1, 32, 8, 128, 128), 64)])
