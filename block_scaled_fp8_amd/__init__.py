@@ -17,6 +17,7 @@ Weight scales for 128x128 blocks (recipe (1, 128, 128)) are passed untransformed
 FP32 [.., ceil(n/128), sf_k] K-major.
 """
 import ctypes
+import operator
 import os
 
 import torch
@@ -862,8 +863,9 @@ def fp8_kv_select_blocks(q, block_keys, block_table, seq_lens, page_size, top, f
             return fp8_kv_select_blocks(q, block_keys, block_table, seq_lens, page_size, top, first, last, cu_seqlens_q, max_seqlen_q, out)
     _, hk, d = shape
     total, hq, batch, cols, ts, cu, max_q, blind = _sequences(q, d, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, dev)
+    page_size, first, last = operator.index(page_size), operator.index(first), operator.index(last)
     want = (total, hk, int(top))
-    if want[2] < 1 or max(want[2], int(page_size), int(first), int(last)) > _INT32:
+    if want[2] < 1 or max(want[2], page_size, first, last) > _INT32 or min(page_size, first, last) < -_INT32 - 1:
         raise ValueError("top must be positive, and top, page_size, first and last fit 32 bits")
     if out is None:
         out = q.new_full(want, -1, dtype=torch.int32) if blind else q.new_empty(want, dtype=torch.int32)

@@ -12,7 +12,7 @@ import block_scaled_fp8_amd as dg
 import oracle
 from oracle.blocks import int8_scale
 from tests import kv_gen
-from tests.test_kv_host import CACHE_FAULTS, cache
+from tests.test_kv_host import CACHE_FAULTS, OnGpu, cache, fake_cache, recorder  # noqa: F401
 
 DG_OK, NULL, DTYPE, SHAPE, LAYOUT, UNSUPPORTED, HIP = 0, -1, -2, -3, -4, -5, -6
 P, P_MIS, P_ODD = 4096, 4104, 4097   # fake addresses: never dereferenced
@@ -171,6 +171,37 @@ def test_the_binding_refuses():
         dg.fp8_kv_block_keys_update(cache_, (codes, scales), torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         dg.fp8_block_sparse_attention(q, cache_, cache_, table, lens, torch.zeros((3, 2, 4), dtype=torch.int32))
+
+
+def test_numbers_past_32_bits_are_refused(recorder):  # noqa: F811
+    """None reaches the library cut to its low 32 bits, large or negative; what 32 bits hold does, for the library to refuse."""
+    keys_ = tuple(OnGpu(x) for x in dg.fp8_kv_block_keys_empty(6, 2, 64, device="cpu"))
+    q, table = OnGpu(torch.zeros((3, 4, 64), dtype=torch.bfloat16)), OnGpu(torch.zeros((3, 5), dtype=torch.int32))
+    lens, out = OnGpu(torch.zeros(3, dtype=torch.int32)), OnGpu(torch.zeros((3, 2, 4), dtype=torch.int32))
+    good = dict(page_size=16, top=4, first=1, last=2)
+
+    def call(**kw):
+        dg.fp8_kv_select_blocks(q, keys_, table, lens, out=out, **{**good, **kw})
+
+    for name, x in good.items():
+        for cut in (2 ** 32, -2 ** 32, 2 ** 64, -2 ** 70):
+            with pytest.raises(ValueError, match="32 bits"):
+                call(**{name: x + cut})
+        with pytest.raises(TypeError):
+            call(**{name: "4" if name != "top" else None})
+    with pytest.raises(ValueError, match="32 bits"):
+        call(first=2 ** 31)
+    assert not recorder.calls
+    call(first=-2 ** 31, last=np.int64(2), page_size=np.int32(16), top=np.int64(4))
+    args = recorder.calls["dg_fp8_kv_select_blocks"][-1]
+    assert args[1] == 16 and args[14:17] == (4, -2 ** 31, 2) and all(type(args[i]) is int for i in (1, 14, 15, 16))
+    assert recorder.calls["dg_fp8_kv_select_blocks_workspace"][-1][8:] == (4, -2 ** 31, 2)
+    # attention's bound saturates, as full attention's does
+    cu = OnGpu(torch.zeros(4, dtype=torch.int32))
+    attn_out = OnGpu(torch.zeros((3, 4, 64), dtype=torch.bfloat16))
+    for given, passed in ((2 ** 32 + 5, 2 ** 31 - 1), (-2 ** 32, -1)):
+        dg.fp8_block_sparse_attention(q, *fake_cache(), table, lens, out, cu_seqlens_q=cu, max_seqlen_q=given, out=attn_out)
+        assert recorder.calls["dg_fp8_block_sparse_attention"][-1][8] == passed
 
 
 # ---------------------------------------------------------------- pins of the oracle
