@@ -111,21 +111,29 @@ SelectPlan select_plan(const Batch& a, int32_t num_kv_heads, int32_t head_dim, i
   SelectPlan pl;
   const int64_t scored = table_cols > top ? table_cols - first - last : 1;
   pl.row_words = ceil_div(scored, 16) * 16 + 4;
-  // Scores of up to 64 KiB, so that two workgroups share a compute unit.  Fewer tokens than a workgroup can take, where they would leave compute units
-  // without one (64 tokens over 512 blocks: 10.5 us, else 19.2; with four workgroups for a unit 13.2).
-  const int64_t fit = 65536 / (4 * pl.row_words), per_tile = 16 / width;
-  pl.tile_tokens = per_tile * dg::select_tiles(head_dim);
-  while (pl.tile_tokens > 1 && (pl.tile_tokens > fit || pl.tile_tokens >= 2 * a.most_tokens() ||
-                                a.batch * ceil_div(a.most_tokens(), pl.tile_tokens) * num_kv_heads < num_sms))
-    pl.tile_tokens /= 2;
+  // Scores of up to 64 KiB.  Two workgroups share a compute unit's 160 KiB of LDS only where they leave room for both beside candidates and the queries'
+  // codes: fewer tokens for that in sequences of eight tiles and more, whose tiles share the keys in the caches, as long as none of a tile's 16 columns
+  // is empty (a chunk of 2048 over 960 blocks, 32 + 8 heads of 128: 81 us, in larger tiles 112; over 2000 blocks 210 and 229, with 64 + 8 heads 251 and
+  // 318; but 32 sequences of 16 new tokens over 3600 blocks 242 and 199).  (At 256 values a head registers hold one workgroup anyway.)
+  // Fewer tokens, too, where they would leave compute units without a workgroup (64 tokens over 512 blocks: 10.5 us, else 19.2; with four workgroups for
+  // a unit 13.2).
+  const int64_t per_tile = 16 / width, tiles = dg::select_tiles(head_dim), row = 4 * pl.row_words;
+  const int64_t beside = 4 * dg::SELECT_WAVES * dg::SELECT_CANDIDATES + tiles * (16 * head_dim + 64);
+  const int64_t fit = 65536 / row, fit_two = head_dim == 256 ? fit : (160 * 1024 / 2 - beside) / row;
+  auto larger_than_pays = [&](int64_t tokens) {
+    return tokens > fit || (tokens > fit_two && tokens > per_tile && 8 * tokens <= a.most_tokens()) || tokens >= 2 * a.most_tokens() ||
+           a.batch * ceil_div(a.most_tokens(), tokens) * num_kv_heads < num_sms;
+  };
+  pl.tile_tokens = per_tile * tiles;
+  while (pl.tile_tokens > 1 && larger_than_pays(pl.tile_tokens)) pl.tile_tokens /= 2;
   pl.items = a.batch * ceil_div(a.most_tokens(), pl.tile_tokens);
   pl.one_tile = pl.tile_tokens <= per_tile;
   pl.parts = 1;
   // Few tiles of many blocks: a workgroup for each 256 blocks (2 sequences of 2048 blocks and 4 heads: 17.2 us, in one part 23.6; 500 blocks for 8 heads,
   // which stay in one, 7.6).
-  const int64_t tiles = pl.items * num_kv_heads;
-  if (pl.one_tile && scored > 512 && 4 * tiles <= num_sms) {
-    const int64_t by_blocks = ceil_div(scored, 256), by_units = num_sms / tiles;
+  const int64_t all = pl.items * num_kv_heads;
+  if (pl.one_tile && scored > 512 && 4 * all <= num_sms) {
+    const int64_t by_blocks = ceil_div(scored, 256), by_units = num_sms / all;
     pl.parts = int(by_blocks < by_units ? by_blocks : by_units);
   }
   return pl;

@@ -323,8 +323,7 @@ __device__ __forceinline__ uint32_t threshold(uint32_t low, uint32_t& high, int 
   return low;
 }
 
-// A wave's room in LDS for scores that may be among the chosen.
-constexpr int CANDIDATES = 512;
+constexpr int CANDIDATES = SELECT_CANDIDATES;
 
 // The blocks of the token at `place`, by a wave, into `out`.  row: its scores, from block `first` on.
 __device__ __forceinline__ void choose(const SelectParams& p, int place, const uint32_t* row, uint32_t* candidates, int32_t* out) {

@@ -151,6 +151,7 @@ struct SelectParams {
   int32_t* out;                  // [total_q, heads, top]
 };
 constexpr int SELECT_WAVES = 8;  // of a workgroup
+constexpr int SELECT_CANDIDATES = 512;  // a wave's room in LDS for scores that may be among the chosen
 // tiles of 16 columns (a token's heads, rounded up to a power of two) of a workgroup: their codes stay in registers
 constexpr int select_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
 // one_tile: a workgroup's tokens fit one tile of columns
