@@ -63,6 +63,30 @@ def test_forward_and_backward(case, bf16, interleaved):
     check_backward(p, got, interleaved)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rot", [(64, 32), (128, 128), (256, 48)])
+def test_gradients_are_those_of_differences(dim, rot, interleaved):
+    """Along random directions, the library's FP32 gradients against central differences of the forward in 64 bits (off by h^2 / 6 of
+    the third derivative, and rounding / h: 1e-6 of the magnitudes as the oracle's own), within the bounds of their arithmetic."""
+    p = rope_gen.problem(9, 3, 2, dim, rot, False, 15)
+    q, k, _, args = operands(p)
+    got = dg.qk_norm_rope_backward(cuda(p["dq"], False), cuda(p["dk"], False), q, k, *args, eps=EPS, interleaved=interleaved)
+    rng, h = np.random.default_rng(1), 1e-5
+    for i, n in enumerate("qk"):
+        x, w, g = p[n], p[n + "w"], p["d" + n]
+        dx, dw = (got[j].double().cpu().numpy() for j in (i, 2 + i))
+        _, _, big, along, total = oracle.norm_rope_backward(g, x, w, p["cs"], p["pos"], EPS, interleaved)
+        tol, tol_w = rope_gen.rounded(rope_gen.backward32(big, along), dx, False), rope_gen.weights32(total, 1)
+        f = lambda x, w: (oracle.norm_rope(x, w, p["cs"], p["pos"], EPS, interleaved)[0] * g).sum()  # noqa: E731
+        for _ in range(10):
+            v = rng.standard_normal(x.shape) * np.abs(x).max(-1, keepdims=True)
+            want = (f(x + h * v, w) - f(x - h * v, w)) / (2 * h)
+            assert abs((dx * v).sum() - want) <= (tol * np.abs(v)).sum() + 1e-6 * np.abs(dx * v).sum()
+            v = rng.standard_normal(w.shape)
+            want = (f(x, w + h * v) - f(x, w - h * v)) / (2 * h)
+            assert abs((dw * v).sum() - want) <= (tol_w * np.abs(v)).sum() + 1e-6 * np.abs(dw * v).sum()
+
+
 @pytest.mark.parametrize("sms", [1, 3])
 def test_backward_with_many_rows_a_wave(sms):
     p = rope_gen.problem(301, 12, 3, 128, 128, True, 5)

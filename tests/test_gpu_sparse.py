@@ -122,6 +122,52 @@ def test_choice_from_a_wide_table():
     assert same(select(p, 40, 1, 1), oracle.select_blocks(p["q"], p["keys"], p["table"], p["lens"], p["cu"], 2, 40, 1, 1))
 
 
+# lengths, new tokens; heads, key heads, head dim, page
+FEW_LONG = {
+    "wide_heads": ([1300], [1], 4, 1, 256, 1),
+    "wide_heads_two": ([1300, 2900], [2, 1], 14, 2, 256, 2),
+    "forty_heads_one_key_head": ([1500], [2], 40, 1, 128, 1),
+    "forty_heads_one_key_head_64": ([1700, 900], [1, 1], 40, 1, 64, 1),
+    "forty_heads_one_key_head_256": ([1250], [1], 40, 1, 256, 1),
+}
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("top,first,last", [(8, 1, 2), (70, 3, 1), (600, 0, 2)])
+@pytest.mark.parametrize("name", sorted(FEW_LONG))
+def test_choice_in_parts(name, top, first, last, ties):
+    """Few tokens over more than 512 blocks: the scores by several workgroups, in several rounds where a key head has more than 16 heads."""
+    say("choice in parts", name, top, first, last, ties)
+    heads, kv_heads, dim, page = FEW_LONG[name][2:]
+    p = select_problem(*FEW_LONG[name], seed=top, ties=ties)
+    assert dg.lib().dg_fp8_kv_select_blocks_workspace(len(p["lens"]), int(p["cu"][-1]), heads, kv_heads, dim, 0, max(p["news"]), p["table"].shape[1], top,
+                                                      first, last) > 0
+    want = oracle.select_blocks(p["q"], p["keys"], p["table"], p["lens"], p["cu"], page, top, first, last)
+    assert same(select(p, top, first, last), want)
+    with num_sms(1):
+        assert same(select(p, top, first, last), want)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_choice_from_a_wide_table_in_one_kernel(dim):
+    """All of a token's 32768 scores in one workgroup's LDS."""
+    say("wide table in one kernel", dim)
+    p = select_problem([32768 * 2, 20000], [3, 2], 4, 2, dim, 2, 1, cols=32768)
+    with num_sms(1):
+        assert same(select(p, 40, 1, 1), oracle.select_blocks(p["q"], p["keys"], p["table"], p["lens"], p["cu"], 2, 40, 1, 1))
+
+
+@pytest.mark.parametrize("cols", [1000, 1900])
+@pytest.mark.parametrize("heads,dim", [(8, 128), (2, 64)])
+def test_choice_of_a_chunk_over_many_blocks(heads, dim, cols):
+    """Tiles of fewer tokens than LDS has room for, so that two workgroups share a compute unit."""
+    p = select_problem([cols - 1], [135], heads, 2, dim, 1, 2, cols=cols)
+    want = oracle.select_blocks(p["q"], p["keys"], p["table"], p["lens"], p["cu"], 1, 20, 1, 2)
+    for sms in (256, 1):
+        with num_sms(sms):
+            assert same(select(p, 20, 1, 2), want)
+
+
 def test_choice_with_queries_that_are_no_numbers():
     """They count as zeros: the choice of the other heads of the group, and of other tokens, stays."""
     p = select_problem([500], [20], 8, 2, 128, 8, 3)
@@ -269,6 +315,17 @@ def test_lists_past_32_bits():
     check(p, dg.fp8_block_sparse_attention(q, *caches, cuda(p["table"]), cuda(p["lens"]), blocks, return_lse=True), few)
 
 
+@pytest.mark.parametrize("sms", [256, 1, 4000])
+@pytest.mark.parametrize("heads,top", [(8, 1500), (4, 1300), (8, 5000), (2, 300)])
+def test_lists_that_fill_a_tiles_room(heads, top, sms):
+    """Long lists of several new tokens: tiles of two tokens, of three, of one, and of 13 (4096 entries of LDS)."""
+    say("long lists", heads, top, sms)
+    p = kv_gen.problem([5200, 4100], [5, 14], heads, 2, 64, 1, 16)
+    blocks = lists(p, 2, top, top, near=True)
+    with num_sms(sms):
+        check(p, run(p, blocks), blocks)
+
+
 def test_scale_and_strides():
     p = kv_gen.problem([90, 70, 33], [5, 2, 9], 6, 2, 128, 16, 12)
     blocks = lists(p, 2, 3, 0)
@@ -358,6 +415,48 @@ def test_queries_that_are_no_numbers():
         rest = torch.ones((7, 8), dtype=torch.bool, device=DEV)
         rest[2, 3] = False
         assert out[rest].isfinite().all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80, 0xFF80])
+def test_beside_queries_that_are_no_numbers(dim, bad):
+    """A NaN or infinite query's row sends its tile over the keys again with care: the other rows are within their bounds as ever."""
+    p = kv_gen.problem([100, 50], [6, 1], 8, 2, dim, 16, 24)
+    blocks = lists(p, 2, 4, 1, near=True)
+    blocks[:, :, 0] = np.where(blocks[:, :, 0] < 0, 0, blocks[:, :, 0])
+    clean = oracle.block_sparse_attention(p["q"], p["k"], p["v"], p["table"], p["lens"], p["cu"], blocks, dim ** -0.5)
+    p["q_bits"][2, 3, 9] = bad
+    for sms in (1, 4000):
+        with num_sms(sms):
+            out, lse = run(p, blocks)
+        assert out[2, 3].isnan().all() and not lse[2, 3].isfinite()
+        out[2, 3] = torch.from_numpy(clean["out"][2, 3])
+        lse[2, 3] = float(clean["lse"][2, 3])
+        check(p, (out, lse), blocks)
+
+
+@pytest.mark.parametrize("dim,news", [(128, [3, 1]), (64, [1, 1]), (256, [2, 9])])
+def test_a_cache_between_2_and_4_gib(dim, news):
+    """Offsets past 2^31 in the form of 32-bit offsets: on the last pages below 4 GiB."""
+    heads, page = 8, 64
+    pages = 2 ** 32 // (heads * page * dim) - 1
+    k_cache, v_cache = dg.fp8_kv_cache_empty(pages, heads, page, dim, device=DEV)
+    p = kv_gen.problem([500, 300], news, 16, heads, dim, page, 25)
+    blocks = lists(p, heads, 4, 2)
+    used = p["table"][p["table"] >= 0]
+    used = np.unique(used[used < len(p["k"][0])])
+    high = {int(pg): pages - 1 - 7 * i if i % 3 else pages // 2 - 1 + i for i, pg in enumerate(used)}
+    for x, c in (("k", k_cache), ("v", v_cache)):
+        for pg, to in high.items():
+            c[0][to], c[1][to] = cuda(p[x][0][pg]), cuda(p[x][1][pg])
+    table = np.vectorize(lambda x: high.get(int(x), -1))(p["table"]).astype(np.int32)
+    q = cuda(p["q_bits"].view(np.int16)).view(torch.bfloat16)
+    for sms in (1, 256, 4000):
+        say("2 to 4 GiB", dim, sms)
+        with num_sms(sms):
+            got = dg.fp8_block_sparse_attention(q, k_cache, v_cache, cuda(table), cuda(p["lens"]), cuda(blocks), cu_seqlens_q=cuda(p["cu"]),
+                                                max_seqlen_q=max(news), return_lse=True)
+        check(p, got, blocks)
 
 
 @pytest.mark.parametrize("dim,news", [(128, [3, 1]), (64, [5, 2]), (256, [2, 9]), (64, [1, 1]), (128, [1, 1]), (256, [1, 1])])
