@@ -854,7 +854,8 @@ def fp8_kv_select_blocks(q, block_keys, block_table, seq_lens, page_size, top, f
     largest, over the query heads that share a key head, of the product of the query in 8-bit codes and the block key: exact, so the
     choice is the same in any call that has the token.
 
-    ``q``, ``block_table``, ``seq_lens``, ``cu_seqlens_q``, ``max_seqlen_q``: as for ``fp8_paged_attention``; the table has at most 32768 columns.
+    ``q``, ``block_table``, ``seq_lens``, ``cu_seqlens_q``, ``max_seqlen_q``: as for ``fp8_paged_attention``; the table has at most 32768 columns,
+    and for chunks should have no more than the longest sequence needs, as their time goes by them.
     ``block_keys``: up to date for all full pages before a token's own.  Only rows of a sequence are written (all -1 where no sequence
     can have a row)."""
     b, shape, dev = _block_keys(block_keys)

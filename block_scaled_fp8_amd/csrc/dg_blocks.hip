@@ -21,7 +21,9 @@ typedef double v2d __attribute__((ext_vector_type(2)));
 // ---------------------------------------------------------------- block keys
 // A wave has a page and head: D / 16 lanes a key of 16 codes each, 1024 / D keys at a time.  The sum is taken in 64 bits, where
 // codes (multiples of 2^-9 up to 448) under scales of up to 2^25 apart add up without rounding.  Bound by reading
-// the keys, for which four loads of a lane go out together (2047 pages of 64 keys and 8 heads of 128: 30 us, 4.6 TB/s; one at a time 40).
+// the keys, for which four loads of a lane go out together (2047 pages of 64 keys and 8 heads of 128: 29 us, 4.6 TB/s; one at a time 40).
+// Pages of 16 keys, 8188 of them: 67 us, bound by instructions (the vector units are busy for 90%): the sums' way through LDS, the mean and
+// its codes cost the same for 2 KiB of keys as for 8 (469 vector instructions a wave, with 64 keys 718).
 constexpr int KEYS_WAVES = 4;
 
 template <int D>
@@ -116,8 +118,13 @@ __global__ void __launch_bounds__(KEYS_WAVES * 64) block_keys_kernel(const Block
 // the chosen blocks in order.
 //
 // What bounds it: latency.  A workgroup's steps (queries to codes, keys through their pages' numbers, the choice) wait for each other; a chunk of
-// 2048 tokens over 512 blocks (32 + 8 heads of 128) takes 46 us, 30 of them for the scores, with the vector units busy for half of the time.  The
-// workgroup's 4 tiles of 16 columns take a block key from memory once (44 us; 2 tiles 52, 8 tiles 50), by 8 waves (4: 58).
+// 2048 tokens over 512 blocks (32 + 8 heads of 128) takes 44 us, 28 of them for the scores, with the vector units busy for half of the time.  The
+// workgroup's 4 tiles of 16 columns take a block key from memory once (with 2 tiles 53 us; 8 need more registers than there are: 68), by 8 waves (with
+// 4: 58).
+//
+// A token's scores all lie in LDS, with a place for each column of the table: a wide table leaves room for few tokens, and every tile reads all block
+// keys.  The same chunk, over the same 512 blocks, takes 57 us with 1024 columns, 84 with 2048, 155 with 4096, 290 with 8192 and 550 with 16384 or
+// 32768; single tokens 14 us with up to 8192 columns and 20 with more (64 sequences).
 //
 // Few sequences with many blocks leave most of the chip idle in that form.  There the scores go to memory, a slice of
 // the blocks to a workgroup, and a second kernel with a wave for each token and key head chooses.

@@ -13,7 +13,8 @@
 // forms take the same cosines and sines, 8 l to 8 l + 7.  The rest of the row goes in pairs of chunks to the
 // lanes after those.  A wave takes 1024 / D heads of one token, all of them queries, keys or values, and its loads go out together, before anything
 // waits.  8192 tokens of 32 + 8 heads of 128, BF16: forward 26 us (168 MB: 6.5 TB/s with what the caches hold), backward 44 (252 MB, 5.7 TB/s)
-// and 4 for the weights, forward into the cache 30 (189 MB, 6.3 TB/s).
+// and 4 for the weights, forward into the cache 30 (189 MB, 6.3 TB/s).  FP32: 4096 tokens forward 29 us (168 MB, 5.8 TB/s), backward with the weights
+// 48 (252 MB, 5.2 TB/s); 8192 tokens 67 and 103 (5.0 and 4.9 TB/s).
 #include <type_traits>
 
 #include "dg_kv_device.h"

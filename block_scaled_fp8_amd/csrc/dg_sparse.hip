@@ -103,6 +103,8 @@ struct Half {
   int key0, keys;   // place of the first one in the sequence, and how many there are
   unsigned tokens;  // whose lists have them, by bits
 };
+// (FAR, with offsets of 64 bits and a descriptor for each half, takes 177 to 181 us for the chunk of 2048 tokens where the other form takes 156 on pages as far
+// from each other, and 47 for 46 with 64 sequences of single tokens; so caches below 4 GiB have the other one.)
 // In LDS: words of one; and how many there may be, of AT_ONCE segments, of which at most every fourth is the wave's, after one that was left, and
 // with the copy that makes an odd number even.  (A segment for each lane: the chunk of 2048 tokens takes 181 us, with 32 at once 188.)
 template <bool FAR>
@@ -278,10 +280,13 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// What bounds it.  Chunks: the issue of instructions.  A tile of 32 keys of 128 codes takes 16 matrix instructions and about 200 vector ones, of which
-// 64 widen codes.  On a chunk of 2048 tokens (32 query heads, 8 key heads of 128, 16 of 512 blocks of 64 for each token; 175 us, 135 ns a tile and
-// compute unit) the vector units are busy for 79% of the time and the matrix units for 21%.  Single tokens: reading (64 sequences of 64 + 8 heads, 32 blocks
-// each: 41 us, 6.5 TB/s, some of it from the last-level cache).
+// What bounds it.  Chunks: the issue of instructions.  A tile of 32 keys of 128 codes takes 16 matrix instructions and 218 vector ones: 64 widen codes,
+// about 100 are the rest of its turn (exponentials, their test and sum 29; the values' scales and rounding 20; hiding keys 20 to 32; addresses 20; the halves'
+// numbers 8), the others find the lists' halves, raise the maximum, begin and end a wave, which has 17 tiles.  On a chunk of 2048 tokens (32 query heads, 8 key heads of
+// 128, 16 of 512 blocks of 64 for each token; 175 us) the vector units are busy for 79% of the time and the matrix units for 21%.  Single tokens:
+// reading (64 sequences of 64 + 8 heads, 32 blocks each: 41 us, 6.5 TB/s, some of it from the last-level cache).
+//   A half holds keys of one page only, so small pages leave tiles partly empty: 64 sequences of single tokens, each over 2048 keys of random blocks, take 49
+// to 50 us on pages of 16 keys and more, 60 on pages of 8, 102 of 4, 188 of 2 and 364 of 1.
 //   Both K and V come through LDS, by copies of whole rows: K straight into operand registers, 16 bytes of each of 16 rows to a lane group, is an
 // access to the first-level cache for every lane, 256 of the 363 that a tile had then (217 us for the chunk; through LDS 188, with 170).  A wave has room for one
 // tile of each: V is on its way while K is used, and the other way round.  With 39 KB for four waves, and less than 128 registers, four
